@@ -2,6 +2,9 @@
  * ordmerge.h -- C ABI of the GB300 (sm_103a) stable co-rank merge library
  * (libordmerge.so).
  *
+ * (With it, at the end: the ordered selections of a language model, routing
+ * to experts, grouping by expert and eviction from a cache.)
+ *
  * Operation.  C = merge(A, B): the stable merge of two arrays that are each
  * sorted nondecreasing.  When an element of A equals an element of B, the A
  * element comes first.  The work is split by the co-rank function: for an
@@ -154,9 +157,9 @@ om_status om_device_error(void *stream, uint32_t *detail);
  * With tracing on, every kernel launch is bracketed by two CUDA events on its
  * stream.  om_trace_read synchronises those events and returns, for kernel
  * kind `kind` (0 = partition, 1 = tile merge, 2 = block sort, 3 = co-rank
- * batch, 4 = the comparison merges below, 5 = one-pass merge), the number of
- * launches and their summed duration in milliseconds since the last
- * om_trace_reset.
+ * batch, 4 = the comparison merges below, 5 = one-pass merge, 6 = routing,
+ * 7 = grouping, 8 = accumulation and eviction), the number of launches and
+ * their summed duration in milliseconds since the last om_trace_reset.
  */
 om_status om_trace_enable(int on);
 om_status om_trace_reset(void);
@@ -302,6 +305,159 @@ om_status om_merge_keys(int key_type, int order, const void *A, int64_t m,
  */
 om_status om_merge_sort_keys(int key_type, int order, void *keys,
                              uint32_t *vals, int64_t n, void *stream);
+
+/* ---- ordered selection: routing, grouping, eviction --------------------- */
+
+/*
+ * What a language model orders: the experts of a token by their scores, the
+ * tokens by their experts, the entries of a cache by the attention they have
+ * drawn.  As in the merges, ties go to the earlier (lower) index.  All calls
+ * are asynchronous on `stream`; all but om_group_by_id allocate nothing.
+ * These calls do not need sorted input.
+ */
+
+/* Value types of logits and attention weights. */
+typedef enum {
+    OM_VALUE_F32 = 0,
+    OM_VALUE_BF16 = 1,
+    OM_VALUE_F16 = 2
+} om_value_type;
+
+typedef enum {
+    OM_SCORE_SOFTMAX = 0, /* s = softmax of the token's logits */
+    OM_SCORE_SIGMOID = 1  /* s = 1 / (1 + exp(-logit)) */
+} om_score;
+
+/*
+ * Routing to experts.  For each of `tokens` rows of `experts` logits (rows
+ * row_stride values apart, each row contiguous):
+ *   s_e = score of the logits;  c_e = s_e + bias_e  (bias may be NULL);
+ *   the experts form `groups` groups of equal size in order, a group's score
+ *   is the sum of its group_best (1 or 2) greatest c, and the group_picks
+ *   groups of greatest score stay open;
+ *   ids = the top_k open experts of greatest c, greatest first;
+ *   weights = scale * s of those (without the bias), divided by their sum
+ *   when renorm is nonzero.
+ * Equal c (and equal group scores) go to the lower index.  ids and weights
+ * hold tokens * top_k values.  c is computed in 32 bits; with no bias and
+ * group_best = 1 (or one group) the order is taken from the logits
+ * themselves, which the rounding of exp cannot tie.
+ *  - An expert whose logit is -inf or NaN has no score (softmax does not
+ *    count it); that one, and one whose bias is -inf or NaN, is never chosen.
+ *    A token with fewer than top_k experts left gets id -1 and weight 0 in
+ *    the slots left over, a wholly masked one in all of them.
+ *  - The renormalised weights come from shifted exponentials: they stay
+ *    right when every s underflows.
+ *  - 1 <= top_k <= group_picks * (experts / groups), groups divides experts.
+ *    At most 1024 experts, 32 groups and top_k 32, else OM_ERANGE.
+ */
+om_status om_route_topk(int value_type, const void *logits, int64_t tokens,
+                        int64_t experts, int64_t row_stride,
+                        const float *bias, int score, int groups,
+                        int group_picks, int group_best, int top_k, int renorm,
+                        float scale, int32_t *ids, float *weights,
+                        void *stream);
+
+/*
+ * Gradient of om_route_topk's weights: grad_logits (tokens * experts values
+ * of value_type, dense) from grad_weights (tokens * top_k) and the ids that
+ * the forward call gave.  The choice of experts is constant, the bias has no
+ * gradient.  With g = scale * grad_weights and w the weights over scale:
+ *   softmax            s_e * (g_e [e chosen] - sum g w)      for every e
+ *   softmax, renorm    w_e * (g_e - sum g w)                 for chosen e
+ *   sigmoid            g_e * s_e * (1 - s_e)                 for chosen e
+ *   sigmoid, renorm    w_e * (1 - s_e) * (g_e - sum g w)     for chosen e
+ * and zero elsewhere.  An id outside [0, experts), or of a logit -inf or NaN,
+ * is an empty slot.  The ids of one token must differ.  Limits as above.
+ */
+om_status om_route_topk_backward(int value_type, const void *logits,
+                                 int64_t tokens, int64_t experts,
+                                 int64_t row_stride, const int32_t *ids,
+                                 const float *grad_weights, int score,
+                                 int top_k, int renorm, float scale,
+                                 void *grad_logits, void *stream);
+
+/*
+ * Stable grouping of n slots by id: order lists the slots by rising id,
+ * equal ids in slot order, and slots whose id is outside [0, groups) last;
+ * offsets[g] (groups + 1 values) is where id g starts in it, offsets[groups]
+ * where the ids outside do; place is the inverse, order[place[i]] = i.
+ * What om_merge_sort_u32 on (id, slot) pairs gives, for few distinct ids, in
+ * a constant number of passes, with the offsets.  n <= 2^31 - 1 and
+ * groups <= 1024, else OM_ERANGE.  Larger calls take stream-ordered scratch
+ * from the library's pool (4 bytes per group and CTA).
+ */
+om_status om_group_by_id(const int32_t *ids, int64_t n, int64_t groups,
+                         int32_t *offsets, int32_t *order, int32_t *place,
+                         void *stream);
+
+/*
+ * Accumulated attention weight per cache entry.  weights holds the attention
+ * weights of `queries` queries: value (b, hq, q, i) at b * w_batch + hq *
+ * w_head + q * w_query + i.  Each of the kv_heads cache heads serves q_heads
+ * / kv_heads consecutive query heads.
+ *   out[b][h][i] = decay * score[b][h][i] + sum over the queries and query
+ *                  heads of h of weights(b, hq, q, i)   for i < lengths[b],
+ *                  0                                    up to `length`.
+ * Sums run in 32 bits in an order fixed by the shapes.  score (NULL: start
+ * from zero) and out are rows of `length` floats at b * batch stride + h *
+ * head stride; out may be score itself, with the same strides.  lengths
+ * (NULL: all `length`) is a device array of batch int32, clamped into
+ * [0, length]; nothing past them is read.  batch * kv_heads, q_heads and
+ * queries are at most 65535, strides 2^40, else OM_ERANGE.
+ */
+om_status om_accumulate_weights(int value_type, const void *weights,
+                                int64_t batch, int64_t q_heads,
+                                int64_t kv_heads, int64_t queries,
+                                int64_t length, int64_t w_batch,
+                                int64_t w_head, int64_t w_query,
+                                const float *score, int64_t s_batch,
+                                int64_t s_head, const int32_t *lengths,
+                                float decay, float *out, int64_t o_batch,
+                                int64_t o_head, void *stream);
+
+/*
+ * The entries of a cache that stay when each row (sequence b, head h) is cut
+ * to `budget`: the first `first`, the last `last` and, of those between, the
+ * ones of greatest score to fill the budget, equal scores to the lower
+ * index.  A row of n = lengths[b] <= budget entries keeps all of them.
+ * keep[b][h][0 .. budget) = their indices, rising, then -1; kept[b] =
+ * min(n, budget).  A NaN score counts as -inf.  first + last <= budget, else
+ * OM_EINVAL.  lengths as in om_accumulate_weights; batch <= 32767 and heads
+ * <= 65535, else OM_ERANGE.
+ */
+om_status om_evict_select(const float *score, int64_t batch, int64_t heads,
+                          int64_t length, int64_t s_batch, int64_t s_head,
+                          const int32_t *lengths, int64_t budget,
+                          int64_t first, int64_t last, int32_t *keep,
+                          int32_t *kept, void *stream);
+
+/*
+ * One array of a cache for om_evict_gather: entry (b, h, i), entry_bytes
+ * long, is at src + b * src_batch + h * src_head + i * src_entry, all in
+ * bytes; likewise dst.
+ */
+typedef struct {
+    const void *src;
+    void *dst;
+    int64_t entry_bytes;
+    int64_t src_batch, src_head, src_entry;
+    int64_t dst_batch, dst_head, dst_entry;
+} om_cache_array;
+
+/*
+ * Moves the kept entries of `count` (at most 8) cache arrays (keys, values,
+ * scores, ...) together: dst entry (b, h, j) = src entry (b, h, keep[b][h][j])
+ * for j < budget, zero bytes where keep is outside [0, length).  `arrays` is
+ * a host array, read before the call returns.  No dst may overlap a src,
+ * another dst or keep (compared by the span from the first to the last entry),
+ * nor share bytes between its own entries.  Vectors of 16 bytes where every
+ * address allows them.  Entry strides are at most 2^30 bytes, others 2^40.
+ */
+om_status om_evict_gather(const int32_t *keep, int64_t batch, int64_t heads,
+                          int64_t budget, int64_t length,
+                          const om_cache_array *arrays, int count,
+                          void *stream);
 
 #ifdef __cplusplus
 }

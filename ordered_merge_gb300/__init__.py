@@ -9,6 +9,9 @@ streams.
 Import fails loudly if the library has not been built
 (``python -m ordered_merge_gb300.build`` or ``__graft_entry__.build()``).
 
+The ordered selections of a language model (routing, grouping, eviction) are
+in ``selection.py``, reached through this package like the rest.
+
 Functions carry the C names (``om_merge_i32`` ...) with unprefixed aliases
 (``merge_i32`` ...).
 """
@@ -22,10 +25,19 @@ from .build import LIB_PATH
 OM_OK, OM_EINVAL, OM_ERANGE, OM_ENOMEM, OM_ECUDA, OM_EDEVICE = range(6)
 
 KIND_PARTITION, KIND_TILE_MERGE, KIND_BLOCK_SORT, KIND_CORANK, KIND_BASELINE, KIND_ONE_PASS = range(6)
+KIND_ROUTE, KIND_GROUP, KIND_EVICT = range(6, 9)
 
 # om_key_type codes and their element sizes
 KEY_TYPES = {"i32": (0, 4), "u32": (1, 4), "f32": (2, 4), "i64": (3, 8), "u64": (4, 8), "f64": (5, 8)}
 OM_ASCENDING, OM_DESCENDING = 0, 1
+
+
+class CacheArray(ctypes.Structure):
+    """om_cache_array: one array of a cache for om_evict_gather."""
+
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("entry_bytes", ctypes.c_int64),
+                ("src_batch", ctypes.c_int64), ("src_head", ctypes.c_int64), ("src_entry", ctypes.c_int64),
+                ("dst_batch", ctypes.c_int64), ("dst_head", ctypes.c_int64), ("dst_entry", ctypes.c_int64)]
 
 
 class OrdMergeError(RuntimeError):
@@ -80,6 +92,20 @@ def _load():
     lib.om_launch_count.restype = ctypes.c_uint64
     lib.om_subtiles_per_range.argtypes = [I64, I64, I64, I64, I64]
     lib.om_subtiles_per_range.restype = I64
+    F32 = ctypes.c_float
+    lib.om_route_topk.argtypes = [I32, P, I64, I64, I64, P, I32, I32, I32, I32, I32, I32, F32, P, P, P]
+    lib.om_route_topk.restype = I32
+    lib.om_route_topk_backward.argtypes = [I32, P, I64, I64, I64, P, P, I32, I32, I32, F32, P, P]
+    lib.om_route_topk_backward.restype = I32
+    lib.om_group_by_id.argtypes = [P, I64, I64, P, P, P, P]
+    lib.om_group_by_id.restype = I32
+    lib.om_accumulate_weights.argtypes = [I32, P, I64, I64, I64, I64, I64, I64, I64, I64, P, I64, I64, P, F32, P, I64,
+                                          I64, P]
+    lib.om_accumulate_weights.restype = I32
+    lib.om_evict_select.argtypes = [P, I64, I64, I64, I64, I64, P, I64, I64, I64, P, P, P]
+    lib.om_evict_select.restype = I32
+    lib.om_evict_gather.argtypes = [P, I64, I64, I64, I64, ctypes.POINTER(CacheArray), I32, P]
+    lib.om_evict_gather.restype = I32
     return lib
 
 
@@ -398,3 +424,17 @@ merge_i32_slices = om_merge_i32_slices
 merge_sort_u32 = om_merge_sort_u32
 device_error = om_device_error
 release_scratch = om_release_scratch
+
+# The ordered selections live in selection.py, which needs torch at import
+# time; it is loaded when one of its names is first used.
+_SELECTION = ("route_topk", "route_topk_backward", "group_by_id", "accumulate_weights", "evict_select", "evict_gather")
+
+
+def __getattr__(name: str):
+    if name.removeprefix("om_") in _SELECTION:
+        from . import selection
+
+        for base in _SELECTION:
+            globals()[base] = globals()["om_" + base] = getattr(selection, "om_" + base)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

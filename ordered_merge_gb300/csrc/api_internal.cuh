@@ -99,7 +99,10 @@ enum KernelKind {
     kKindCorank = 3,
     kKindBaseline = 4,
     kKindOnePass = 5,
-    kNumKinds = 6
+    kKindRoute = 6,
+    kKindGroup = 7,
+    kKindEvict = 8,
+    kNumKinds = 9
 };
 
 // ------------------------------------------------------------ device state --

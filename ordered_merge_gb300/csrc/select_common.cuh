@@ -1,0 +1,70 @@
+// Shared by the ordered-selection operators (route.cu, group.cu, evict.cu):
+// value types, the order-preserving integer image of a score and warp
+// reductions.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "ordmerge.h"
+
+namespace om {
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+
+// Order-preserving image of a float that is not NaN: a < b exactly when
+// image(a) < image(b), and -0 and +0 share one image (adding +0 makes -0
+// positive), so equal scores tie.  -inf maps to 0x007fffff, hence 0 is free
+// for "no candidate".
+__device__ __forceinline__ uint32_t score_image(float x) {
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+    return x;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+inline int value_bytes(int value_type) {
+    switch (value_type) {
+        case OM_VALUE_F32: return 4;
+        case OM_VALUE_BF16:
+        case OM_VALUE_F16: return 2;
+        default: return 0;
+    }
+}
+
+// Calls f with a value of the C++ type behind value_type (already checked).
+template <typename F>
+auto with_value_type(int value_type, F&& f) {
+    switch (value_type) {
+        case OM_VALUE_F32: return f(float{});
+        case OM_VALUE_BF16: return f(__nv_bfloat16{});
+        default: return f(__half{});
+    }
+}
+
+}  // namespace om

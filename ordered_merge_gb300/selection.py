@@ -1,0 +1,261 @@
+"""Binding of the library's ordered selections: routing to experts with its
+gradient, stable grouping by expert, accumulated attention weights and
+eviction from a cache.
+
+Like the rest of the package this is argument marshalling only: tensors'
+pointers, strides and the current stream go to the C ABI (declared in
+``include/ordmerge.h``), which validates and launches.  Outputs may be passed
+in; those not passed are allocated.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import CacheArray, _check, _lib, _stream
+
+VALUE_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _ptr(t):
+    return t.data_ptr() if t.numel() else None
+
+
+def _empty(shape, dtype, device, stream):
+    """New output, allocated for the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _placed(**tensors):
+    """Every tensor is on the current device (the one the library launches on)."""
+    device = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if device is None:
+            device = torch.cuda.current_device()
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{device}")
+
+
+def _dense(t, name: str, shape, dtype):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                         f"(got {t.dtype}, {tuple(t.shape)})")
+
+
+def _value_type(t, name: str) -> int:
+    if t.dtype not in VALUE_TYPES:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
+    return VALUE_TYPES[t.dtype]
+
+
+def _rows(t, name: str, dims: int):
+    """Strides of a tensor of `dims` dimensions whose last one is contiguous."""
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions (got {t.dim()})")
+    strides = t.stride()
+    if t.shape[-1] > 1 and strides[-1] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return strides
+
+
+def _score_code(score: str) -> int:
+    if score not in SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid' (got {score!r})")
+    return SCORES[score]
+
+
+def _lengths(lengths, batch: int):
+    if lengths is None:
+        return None
+    _dense(lengths, "lengths", (batch,), torch.int32)
+    return _ptr(lengths)
+
+
+def om_route_topk(logits, top_k: int, score: str = "softmax", bias=None, groups: int = 1, group_picks: int = 1,
+                  group_best: int = 1, renorm: bool = False, scale: float = 1.0, ids=None, weights=None, stream=None):
+    """(ids, weights) of the top_k experts of each row of logits [tokens,
+    experts]: greatest score + bias first, ties to the lower index, from the
+    group_picks groups whose group_best greatest sum highest; weights are the
+    scores without the bias (divided by their sum with renorm) times scale.
+    Masked experts (-inf or NaN) are never chosen; id -1, weight 0 fill up."""
+    row_stride = _rows(logits, "logits", 2)[0]
+    tokens, experts = logits.shape
+    if bias is not None:
+        _dense(bias, "bias", (experts,), torch.float32)
+    if ids is None:
+        ids = _empty((tokens, top_k), torch.int32, logits.device, stream)
+    if weights is None:
+        weights = _empty((tokens, top_k), torch.float32, logits.device, stream)
+    _dense(ids, "ids", (tokens, top_k), torch.int32)
+    _dense(weights, "weights", (tokens, top_k), torch.float32)
+    _placed(logits=logits, bias=bias, ids=ids, weights=weights)
+    _check(
+        _lib.om_route_topk(_value_type(logits, "logits"), _ptr(logits), tokens, experts, row_stride,
+                           None if bias is None else bias.data_ptr(), _score_code(score), groups, group_picks,
+                           group_best, top_k, 1 if renorm else 0, scale, _ptr(ids), _ptr(weights), _stream(stream)),
+        "om_route_topk",
+    )
+    return ids, weights
+
+
+def om_route_topk_backward(logits, ids, grad_weights, score: str = "softmax", renorm: bool = False,
+                           scale: float = 1.0, grad_logits=None, stream=None):
+    """Gradient of om_route_topk's weights by the logits (contiguous, in
+    their dtype), from its ids and the weights' gradient (float32)."""
+    row_stride = _rows(logits, "logits", 2)[0]
+    tokens, experts = logits.shape
+    if ids.dim() != 2:
+        raise ValueError("ids must have 2 dimensions")
+    top_k = ids.shape[1]
+    _dense(ids, "ids", (tokens, top_k), torch.int32)
+    _dense(grad_weights, "grad_weights", (tokens, top_k), torch.float32)
+    if grad_logits is None:
+        grad_logits = _empty((tokens, experts), logits.dtype, logits.device, stream)
+    _dense(grad_logits, "grad_logits", (tokens, experts), logits.dtype)
+    _placed(logits=logits, ids=ids, grad_weights=grad_weights, grad_logits=grad_logits)
+    _check(
+        _lib.om_route_topk_backward(_value_type(logits, "logits"), _ptr(logits), tokens, experts, row_stride,
+                                    _ptr(ids), _ptr(grad_weights), _score_code(score), top_k, 1 if renorm else 0,
+                                    scale, _ptr(grad_logits), _stream(stream)),
+        "om_route_topk_backward",
+    )
+    return grad_logits
+
+
+def om_group_by_id(ids, groups: int, offsets=None, order=None, place=None, stream=None):
+    """(offsets, order, place) of the stable grouping of ids (int32, any
+    shape, contiguous; taken flat): order[offsets[g]:offsets[g + 1]] are the
+    slots with id g in rising order, slots with an id outside [0, groups)
+    come last, and order[place[i]] == i."""
+    if ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 tensor")
+    n = ids.numel()
+    if offsets is None:
+        offsets = _empty((groups + 1,), torch.int32, ids.device, stream)
+    if order is None:
+        order = _empty((n,), torch.int32, ids.device, stream)
+    if place is None:
+        place = _empty((n,), torch.int32, ids.device, stream)
+    _dense(offsets, "offsets", (groups + 1,), torch.int32)
+    _dense(order, "order", (n,), torch.int32)
+    _dense(place, "place", (n,), torch.int32)
+    _placed(ids=ids, offsets=offsets, order=order, place=place)
+    _check(_lib.om_group_by_id(_ptr(ids), n, groups, _ptr(offsets), _ptr(order), _ptr(place), _stream(stream)),
+           "om_group_by_id")
+    return offsets, order, place
+
+
+def om_accumulate_weights(weights, score=None, lengths=None, decay: float = 1.0, kv_heads: int | None = None,
+                          out=None, stream=None):
+    """decay * score + the attention weights [batch, q_heads, queries, length]
+    summed over the queries and the query heads of each cache head, as
+    [batch, kv_heads, length] float32; zero past lengths (int32 [batch]).
+    score None starts from zero (give kv_heads then); out may be score."""
+    w_batch, w_head, w_query, _ = _rows(weights, "weights", 4)
+    batch, q_heads, queries, length = weights.shape
+    s_batch = s_head = 0
+    if score is not None:
+        s_batch, s_head, _ = _rows(score, "score", 3)
+        kv_heads = score.shape[1] if kv_heads is None else kv_heads
+        if score.dtype != torch.float32 or tuple(score.shape) != (batch, kv_heads, length):
+            raise ValueError(f"score must be float32 of shape {(batch, kv_heads, length)}")
+    if kv_heads is None:
+        raise ValueError("kv_heads is needed without a score")
+    if out is None:
+        out = _empty((batch, kv_heads, length), torch.float32, weights.device, stream)
+    o_batch, o_head, _ = _rows(out, "out", 3)
+    if out.dtype != torch.float32 or tuple(out.shape) != (batch, kv_heads, length):
+        raise ValueError(f"out must be float32 of shape {(batch, kv_heads, length)}")
+    length_ptr = _lengths(lengths, batch)
+    _placed(weights=weights, score=score, lengths=lengths, out=out)
+    _check(
+        _lib.om_accumulate_weights(_value_type(weights, "weights"), _ptr(weights), batch, q_heads, kv_heads, queries,
+                                   length, w_batch, w_head, w_query, None if score is None else _ptr(score), s_batch,
+                                   s_head, length_ptr, decay, _ptr(out), o_batch, o_head, _stream(stream)),
+        "om_accumulate_weights",
+    )
+    return out
+
+
+def om_evict_select(score, budget: int, first: int = 0, last: int = 0, lengths=None, keep=None, kept=None,
+                    stream=None):
+    """(keep, kept): the indices, rising and then -1, of the entries that each
+    row of score [batch, heads, length] (float32) keeps when cut to budget
+    (the first `first`, the last `last`, the greatest scores between, ties to
+    the lower index), and min(length, budget) per sequence."""
+    s_batch, s_head, _ = _rows(score, "score", 3)
+    if score.dtype != torch.float32:
+        raise ValueError(f"score must be float32 (got {score.dtype})")
+    batch, heads, length = score.shape
+    if keep is None:
+        keep = _empty((batch, heads, budget), torch.int32, score.device, stream)
+    if kept is None:
+        kept = _empty((batch,), torch.int32, score.device, stream)
+    _dense(keep, "keep", (batch, heads, budget), torch.int32)
+    _dense(kept, "kept", (batch,), torch.int32)
+    length_ptr = _lengths(lengths, batch)
+    _placed(score=score, lengths=lengths, keep=keep, kept=kept)
+    _check(
+        _lib.om_evict_select(_ptr(score), batch, heads, length, s_batch, s_head, length_ptr, budget, first, last,
+                             _ptr(keep), _ptr(kept), _stream(stream)),
+        "om_evict_select",
+    )
+    return keep, kept
+
+
+def _cache_entry(t, name: str, batch: int, heads: int) -> int:
+    """Bytes of one entry of a cache array [batch, heads, entries, ...] whose entries are contiguous."""
+    if t.dim() < 3 or t.shape[0] != batch or t.shape[1] != heads:
+        raise ValueError(f"{name} must be [batch, heads, entries, ...] with batch {batch} and heads {heads}")
+    inner = 1
+    for size, stride in zip(reversed(t.shape[3:]), reversed(t.stride()[3:])):
+        if size > 1 and stride != inner:
+            raise ValueError(f"the entries of {name} must be contiguous")
+        inner *= size
+    return inner * t.element_size()
+
+
+def om_evict_gather(keep, arrays, out=None, stream=None):
+    """The cache arrays (each [batch, heads, entries, ...], any element type,
+    entries contiguous) gathered to keep [batch, heads, budget]: entry j
+    becomes entry keep[j], zero where keep is -1.  Returns new arrays, or
+    `out`, which must not overlap the inputs.  One launch moves all of them."""
+    arrays = tuple(arrays)
+    if keep.dim() != 3:
+        raise ValueError("keep must have 3 dimensions")
+    batch, heads, budget = keep.shape
+    _dense(keep, "keep", (batch, heads, budget), torch.int32)
+    if not arrays:
+        raise ValueError("no arrays to gather")
+    length = arrays[0].shape[2] if arrays[0].dim() >= 3 else 0
+    if out is None:
+        out = tuple(_empty((batch, heads, budget, *t.shape[3:]), t.dtype, t.device, stream) for t in arrays)
+    out = tuple(out)
+    if len(out) != len(arrays):
+        raise ValueError("out must hold one tensor for each array")
+    _placed(keep=keep)
+    table = (CacheArray * len(arrays))()
+    for c, src, dst in zip(table, arrays, out):
+        _placed(array=src, out=dst)
+        size = _cache_entry(src, "array", batch, heads)
+        if src.shape[2] != length:
+            raise ValueError("the arrays must have as many entries each")
+        if dst.dtype != src.dtype or dst.shape[2:3] != (budget,) or dst.shape[3:] != src.shape[3:] \
+                or _cache_entry(dst, "out", batch, heads) != size:
+            raise ValueError(f"out must be {src.dtype} of shape {(batch, heads, budget, *src.shape[3:])}")
+        es = src.element_size()
+        c.src, c.dst, c.entry_bytes = src.data_ptr(), dst.data_ptr(), size
+        c.src_batch, c.src_head, c.src_entry = (s * es for s in src.stride()[:3])
+        c.dst_batch, c.dst_head, c.dst_entry = (s * es for s in dst.stride()[:3])
+    _check(_lib.om_evict_gather(_ptr(keep), batch, heads, budget, length, table, len(arrays), _stream(stream)),
+           "om_evict_gather")
+    return out
