@@ -1,6 +1,7 @@
 // om_accumulate_weights / om_evict_select / om_evict_gather: eviction from a
 // cache by accumulated attention weight.
 #include <cstdint>
+#include <mutex>
 
 #include <cuda_runtime.h>
 
@@ -28,21 +29,154 @@ __device__ __forceinline__ int64_t valid_length(const int32_t* lengths, int64_t 
     return n < 0 ? 0 : n < length ? n : length;
 }
 
-// One thread per cache entry.
-template <typename T>
-__global__ void __launch_bounds__(256) accumulate_weights_kernel(AccumulateArgs a) {
+// The two 16-bit values of a word, or the one 32-bit value, added to sums.
+__device__ __forceinline__ void add_word(float* sum, uint32_t w, float) { sum[0] += __uint_as_float(w); }
+__device__ __forceinline__ void add_word(float* sum, uint32_t w, __nv_bfloat16) {
+    sum[0] += __uint_as_float(w << 16);
+    sum[1] += __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void add_word(float* sum, uint32_t w, __half) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    sum[0] += f.x;
+    sum[1] += f.y;
+}
+
+constexpr int kAccWarps = 8;
+
+// A warp sums rows over one tile of entries, V = 16 bytes' worth per lane; the
+// rows of a tile (share * queries of them) are split over `split` warps of
+// the CTA, whose sums are then added in the order of the warps, so the result
+// depends on the shapes alone.
+//
+// Rows may start at any element (ALIGNED: all start on 16 bytes).  A lane loads
+// the aligned 16 bytes that its part of the row begins in and adds them up as
+// they lie; only when the rows' offset `skip` from that boundary changes are
+// the sums added to the tile's entries, `skip` values further left.  Rows V
+// queries apart have the same offset, so each warp walks its rows in the order
+// (query mod V, head, query), in which the offset changes least often.  The
+// tile is then 31 lanes wide, as the last lane's vector reaches past it.  A
+// vector that holds no value of the row's valid part is not loaded.
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(kAccWarps * 32) accumulate_weights_kernel(AccumulateArgs a, int split) {
+    constexpr int V = 16 / (int)sizeof(T), LANES = ALIGNED ? 32 : 31, TILE = LANES * V, U = 8;
+    __shared__ __align__(16) float s_sum[kAccWarps][32 * V];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % split;
+    const int tiles = kAccWarps / split;  // of this CTA
     const int64_t b = blockIdx.y / a.kv_heads, h = blockIdx.y % a.kv_heads;
     const int64_t n = valid_length(a.lengths, b, a.length);
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= a.length) return;
-    float total = 0.0f;
-    if (i < n) {
-        const T* w = static_cast<const T*>(a.weights) + b * a.w_batch + h * a.share * a.w_head + i;
-        for (int g = 0; g < a.share; ++g)
-            for (int q = 0; q < a.queries; ++q) total += to_float(w[g * a.w_head + q * a.w_query]);
-        if (a.score != nullptr) total += a.decay * a.score[b * a.s_batch + h * a.s_head + i];
+    const int64_t first = (int64_t)blockIdx.x * tiles * TILE;
+    const int64_t c0 = first + (warp / split) * TILE;
+    const int rows = a.share * a.queries;
+    const int r0 = (int)((int64_t)rows * part / split), r1 = (int)((int64_t)rows * (part + 1) / split);
+    // the old scores this thread will need, so that they arrive meanwhile
+    float old[V];
+    const float* score = a.score == nullptr ? nullptr : a.score + b * a.s_batch + h * a.s_head;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int j = k * kAccWarps * 32 + threadIdx.x;
+        old[k] = 0.0f;
+        if (score != nullptr && j < tiles * TILE && first + j < n) old[k] = __ldcs(score + first + j);
     }
-    a.out[b * a.o_batch + h * a.o_head + i] = total;
+    float sum[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+    if (!ALIGNED) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s_sum[warp][lane * V + v] = 0.0f;
+        __syncwarp();
+    }
+    if (c0 < n && r0 < r1) {
+        const char* base = reinterpret_cast<const char*>(static_cast<const T*>(a.weights) + b * a.w_batch +
+                                                         h * a.share * a.w_head + c0);
+        // the r0-th row of the walk: class c = query mod V, head g, query q
+        int c = 0, before = r0;
+        int in_class = (a.queries + V - 1) / V;  // queries of class c
+        while (before >= a.share * in_class) {
+            before -= a.share * in_class;
+            ++c;
+            in_class = (a.queries - c + V - 1) / V;
+        }
+        int g = before / in_class, q = c + (before - g * in_class) * V;
+        int cur = 0;  // offset, in values, of what `sum` holds
+        for (int r = r0; r < r1; r += U) {
+            uint4 w[U];
+            int skip[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                w[u] = make_uint4(0, 0, 0, 0);
+                skip[u] = -1;
+                if (r + u < r1) {
+                    const char* at = base + (g * a.w_head + q * a.w_query) * (int64_t)sizeof(T);
+                    if ((q += V) >= a.queries) {
+                        if (++g == a.share) g = 0, ++c;
+                        q = c;
+                    }
+                    skip[u] = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(at) & 15) / (int)sizeof(T);
+                    if (c0 + lane * V - skip[u] < n)
+                        w[u] = __ldcs(reinterpret_cast<const uint4*>(at - skip[u] * (int)sizeof(T)) + lane);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (!ALIGNED && skip[u] >= 0 && skip[u] != cur) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        if (lane * V + v >= cur) s_sum[warp][lane * V + v - cur] += sum[v];
+                        sum[v] = 0.0f;
+                    }
+                    __syncwarp();
+                    cur = skip[u];
+                }
+                add_word(sum, w[u].x, T{});
+                add_word(sum + V / 4, w[u].y, T{});
+                add_word(sum + V / 2, w[u].z, T{});
+                add_word(sum + 3 * V / 4, w[u].w, T{});
+            }
+        }
+        if (!ALIGNED) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (lane * V + v >= cur) s_sum[warp][lane * V + v - cur] += sum[v];
+        }
+    }
+    if (ALIGNED) {
+#pragma unroll
+        for (int v = 0; v < V; v += 4)
+            *reinterpret_cast<float4*>(&s_sum[warp][lane * V + v]) =
+                make_float4(sum[v], sum[v + 1], sum[v + 2], sum[v + 3]);
+    }
+    __syncthreads();
+    float* out = a.out + b * a.o_batch + h * a.o_head;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int j = k * kAccWarps * 32 + threadIdx.x;
+        const int64_t i = first + j;
+        if (j >= tiles * TILE || i >= a.length) break;
+        float total = 0.0f;
+        if (i < n) {
+            const int t = j / TILE, col = j - t * TILE;
+            for (int w = 0; w < split; ++w) total += s_sum[t * split + w][col];
+            if (score != nullptr) total += a.decay * old[k];
+        }
+        __stcs(out + i, total);
+    }
+}
+
+template <typename T>
+static cudaError_t launch_accumulate(const AccumulateArgs& a, int64_t batch, cudaStream_t st) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const int64_t rows = (int64_t)a.share * a.queries;
+    int split = 1;  // at least 8 rows a warp: one batch of its loads
+    while (split < kAccWarps && rows >= 16 * split) split *= 2;
+    const uint64_t low = reinterpret_cast<uintptr_t>(a.weights) / sizeof(T) | (uint64_t)a.w_batch |
+                         (uint64_t)a.w_head | (uint64_t)a.w_query;
+    const bool aligned = low % V == 0;
+    const int64_t wide = (int64_t)(kAccWarps / split) * (aligned ? 32 : 31) * V;
+    const dim3 grid((unsigned)((a.length + wide - 1) / wide), (unsigned)(batch * a.kv_heads));
+    return traced(kKindEvict, st, [&] {
+        if (aligned) accumulate_weights_kernel<T, true><<<grid, kAccWarps * 32, 0, st>>>(a, split);
+        else accumulate_weights_kernel<T, false><<<grid, kAccWarps * 32, 0, st>>>(a, split);
+    });
 }
 
 // ------------------------------------------------------------ selection --
@@ -56,16 +190,57 @@ struct EvictArgs {
     int length, heads, budget, first, last;
 };
 
-constexpr int kSelectThreads = 1024;
+constexpr int kSelectThreads = 512;
+constexpr int kSelectStep = 128;  // keys a warp takes at a time, four consecutive ones per lane
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kDigitBits = 11;
 constexpr int kDigits = 1 << kDigitBits;
+constexpr int kPasses = 3;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxCached = 48 * 1024;  // keys a CTA can hold in shared memory (192 KB)
 
 // A NaN score counts as -inf: it goes first.
 __device__ __forceinline__ uint32_t evict_key(float s) { return score_image(s == s ? s : -INFINITY); }
 
-// Sum of `mine` over the threads before, and over all of them.
-__device__ __forceinline__ int block_scan(int mine, int* s_part, int* total) {
+// The key of an entry that stays whatever its score; above that of +inf.
+constexpr uint32_t kKeyStays = 0xffffffffu;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// Every thread of every CTA of the cluster; orders their shared memory.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word, or four, of CTA `rank`'s shared memory, at the address p has in this CTA's.
+__device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
+    uint32_t at;
+    int v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ int4 peer_words(const int* p, uint32_t rank) {
+    uint32_t at;
+    int4 v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+
+// Sum of `mine` over the threads before.
+__device__ __forceinline__ int block_before(int mine, int* s_part) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int run = mine;
 #pragma unroll
@@ -73,86 +248,246 @@ __device__ __forceinline__ int block_scan(int mine, int* s_part, int* total) {
         const int up = __shfl_up_sync(0xffffffffu, run, d);
         if (lane >= d) run += up;
     }
-    __syncthreads();
     if (lane == 31) s_part[warp] = run;
     __syncthreads();
-    int w = s_part[lane];
+    int w = lane < kSelectWarps ? s_part[lane] : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int up = __shfl_up_sync(0xffffffffu, w, d);
         if (lane >= d) w += up;
     }
-    *total = __shfl_sync(0xffffffffu, w, 31);
     const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
     return (warp > 0 ? before : 0) + run - mine;
 }
 
-// One CTA per row (sequence and head).  The least key that stays is found
-// digit by digit from the top (11 + 11 + 10 bits): a histogram of the keys
-// that agree with the digits found so far gives the next one.
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictArgs a) {
-    __shared__ int s_hist[kDigits];
-    __shared__ int s_part[32];
-    __shared__ int s_digit, s_above;
-    const int64_t b = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
+struct SelectShared {
+    __align__(16) int hist[kPasses][kDigits];
+    int part[kPasses][kSelectWarps];
+    int above[kSelectWarps], equal[kSelectWarps];  // kept for sure / on the edge, in the warps before
+    int total[2];                                  // the same of the CTA
+    int digit, over;
+};
+
+// One cluster of 1 to 8 CTAs per row (sequence and head); CTA r takes the r-th
+// contiguous part of it, and warp w of the CTA the w-th part of that, so that
+// ranks in the row follow from sums over the CTAs and warps before.
+//
+// The row's least key that stays is found digit by digit from the top (11 + 11
+// + 10 bits): a histogram of the keys that agree with the digits found so far,
+// summed over the cluster, gives the next one.  Keys are read from memory
+// once and kept in shared memory (CACHED), unless the part is too long for it.
+// Places past the row's end hold key 0, which is below every score's and so
+// never reached.
+template <bool CACHED>
+__global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(EvictArgs a) {
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    SelectShared& s = *reinterpret_cast<SelectShared*>(s_raw);
+    uint32_t* s_keys = reinterpret_cast<uint32_t*>(s_raw + sizeof(SelectShared));
+    const uint32_t rank = cluster_rank(), ctas = cluster_size();
+    const int64_t row = blockIdx.x / ctas, b = row / a.heads, h = row % a.heads;
     const float* score = a.score + b * a.s_batch + h * a.s_head;
-    int32_t* keep = a.keep + (int64_t)blockIdx.x * a.budget;
+    int32_t* keep = a.keep + row * a.budget;
     const int n = (int)valid_length(a.lengths, b, a.length);
-    if (h == 0 && threadIdx.x == 0) a.kept[b] = min(n, a.budget);
-    if (n <= a.budget) {
-        for (int i = threadIdx.x; i < a.budget; i += kSelectThreads) keep[i] = i < n ? i : -1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (h == 0 && rank == 0 && threadIdx.x == 0) a.kept[b] = min(n, a.budget);
+    if (n <= a.budget) {  // the whole cluster leaves here
+        for (int i = (int)rank * kSelectThreads + threadIdx.x; i < a.budget; i += (int)ctas * kSelectThreads)
+            keep[i] = i < n ? i : -1;
         return;
     }
-    const int lo = a.first, hi = n - a.last;
-    int need = a.budget - a.first - a.last;  // still to be chosen among those that agree with `prefix`
+    for (int i = threadIdx.x; i < kPasses * kDigits / 4; i += kSelectThreads)
+        reinterpret_cast<int4*>(&s.hist[0][0])[i] = make_int4(0, 0, 0, 0);
+    const int warps = (int)ctas * kSelectWarps;
+    const int per_warp = (((n + warps - 1) / warps) + kSelectStep - 1) / kSelectStep * kSelectStep;
+    const int64_t w0 = ((int64_t)rank * kSelectWarps + warp) * per_warp;
+    const int lo = (int)min(w0, (int64_t)n), hi = (int)min(w0 + per_warp, (int64_t)n);
+    uint32_t* mine = s_keys + warp * per_warp;
+    const bool aligned = (reinterpret_cast<uintptr_t>(score) & 15) == 0;  // lo is a multiple of 4
+
+    auto fetch = [&](int i) {  // scores i .. i + 3
+        if (aligned && i + 3 < hi) return __ldg(reinterpret_cast<const float4*>(score + i));
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i < hi) x.x = __ldg(score + i);
+        if (i + 1 < hi) x.y = __ldg(score + i + 1);
+        if (i + 2 < hi) x.z = __ldg(score + i + 2);
+        if (i + 3 < hi) x.w = __ldg(score + i + 3);
+        return x;
+    };
+    auto keys_of = [&](int i, float4 x) {  // their keys
+        uint4 k = make_uint4(evict_key(x.x), evict_key(x.y), evict_key(x.z), evict_key(x.w));
+        uint32_t* p = &k.x;
+        if (i < a.first || i + 4 > n - a.last) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[j] = i + j >= hi ? 0u : i + j < a.first || i + j >= n - a.last ? kKeyStays : p[j];
+        }
+        return k;
+    };
+    auto keys_at = [&](int i0) {
+        if (CACHED) return *reinterpret_cast<const uint4*>(mine + (i0 - lo) + 4 * lane);
+        return keys_of(i0 + 4 * lane, fetch(i0 + 4 * lane));
+    };
+    __syncthreads();
+
+    int need = a.budget;  // still to be chosen among the keys that agree with `prefix`
     uint32_t prefix = 0, mask = 0;
-    if (need > 0) {
-        for (int shift = 21; shift >= -1; shift -= kDigitBits) {
-            const int down = shift < 0 ? 0 : shift;
-            const uint32_t digits = shift < 0 ? kDigits / 2 - 1 : kDigits - 1;
-            for (int i = threadIdx.x; i < kDigits; i += kSelectThreads) s_hist[i] = 0;
-            __syncthreads();
-            for (int i = lo + threadIdx.x; i < hi; i += kSelectThreads) {
-                const uint32_t k = evict_key(score[i]);
-                if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> down) & digits], 1);
+#pragma unroll
+    for (int pass = 0; pass < kPasses; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t digits = pass == 2 ? kDigits / 2 - 1 : kDigits - 1;
+        auto count = [&](uint32_t k) {
+            if (pass == 0 || (k & mask) == prefix) atomicAdd(&s.hist[pass][(k >> shift) & digits], 1);
+        };
+        if (pass == 0) {
+            constexpr int U = 4;  // loads in flight per lane
+            for (int i0 = lo; i0 < hi; i0 += kSelectStep * U) {
+                float4 x[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) x[u] = fetch(i0 + u * kSelectStep + 4 * lane);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int at = i0 + u * kSelectStep;
+                    if (at < hi) {
+                        const uint4 k = keys_of(at + 4 * lane, x[u]);
+                        if (CACHED) *reinterpret_cast<uint4*>(mine + (at - lo) + 4 * lane) = k;
+                        count(k.x), count(k.y), count(k.z), count(k.w);
+                    }
+                }
             }
-            __syncthreads();
-            // two digits a thread, from the greatest down
-            const int top = kDigits - 1 - 2 * threadIdx.x;
-            const int c0 = s_hist[top], c1 = s_hist[top - 1];
-            int total;
-            const int above = block_scan(c0 + c1, s_part, &total);
-            if (above < need && need <= above + c0) s_digit = top, s_above = above;
-            if (above + c0 < need && need <= above + c0 + c1) s_digit = top - 1, s_above = above + c0;
-            __syncthreads();
-            prefix |= (uint32_t)s_digit << down;
-            mask |= digits << down;
-            need -= s_above;
-        }
-    }
-    // in order: the first ones, those above the least key, the first `need` equal to it, the last ones
-    int done = 0, ties = 0;
-    const bool any = a.budget > a.first + a.last;
-    for (int i0 = 0; i0 < n; i0 += kSelectThreads) {
-        const int i = i0 + threadIdx.x;
-        bool sure = false, tie = false;
-        if (i < n) {
-            if (i < lo || i >= hi) {
-                sure = true;
-            } else if (any) {
-                const uint32_t k = evict_key(score[i]);
-                sure = k > prefix;
-                tie = k == prefix;
+        } else {
+            for (int i0 = lo; i0 < hi; i0 += kSelectStep) {
+                const uint4 k = keys_at(i0);
+                count(k.x), count(k.y), count(k.z), count(k.w);
             }
         }
-        int all;
-        const int tied = ties + block_scan(tie, s_part, &all);
-        const bool stays = sure || (tie && tied < need);
-        ties += all;
-        const int at = done + block_scan(stays, s_part, &all);
-        if (stays) keep[at] = i;
-        done += all;
+        cluster_sync();
+        // four digits a thread, from the greatest down, summed over the cluster
+        const int low = kDigits - 4 - 4 * threadIdx.x;
+        int4 c = make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxCluster; ++r) {
+            if (r < ctas) {
+                const int4 p = peer_words(&s.hist[pass][low], r);
+                c.x += p.x, c.y += p.y, c.z += p.z, c.w += p.w;
+            }
+        }
+        int above = block_before(c.x + c.y + c.z + c.w, s.part[pass]);
+        if (above < need && need <= above + c.x + c.y + c.z + c.w) {  // one thread
+            int digit = low + 3;
+            if (need > above + c.w) {
+                above += c.w, --digit;
+                if (need > above + c.z) {
+                    above += c.z, --digit;
+                    if (need > above + c.y) above += c.y, --digit;
+                }
+            }
+            s.digit = digit;
+            s.over = above;
+        }
+        __syncthreads();
+        prefix |= (uint32_t)s.digit << shift;
+        mask |= digits << shift;
+        need -= s.over;
     }
+
+    // how many of each warp's and each CTA's part stay: above the edge for sure, and on it
+    int above = 0, equal = 0;
+    for (int i0 = lo; i0 < hi; i0 += kSelectStep) {
+        const uint4 k = keys_at(i0);
+        above += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
+        equal += (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) s.above[warp] = above, s.equal[warp] = equal;
+    __syncthreads();
+    if (warp == 0) {
+        const int x = lane < kSelectWarps ? s.above[lane] : 0, y = lane < kSelectWarps ? s.equal[lane] : 0;
+        int rx = x, ry = y;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int ux = __shfl_up_sync(0xffffffffu, rx, d), uy = __shfl_up_sync(0xffffffffu, ry, d);
+            if (lane >= d) rx += ux, ry += uy;
+        }
+        if (lane < kSelectWarps) s.above[lane] = rx - x, s.equal[lane] = ry - y;
+        if (lane == 31) s.total[0] = rx, s.total[1] = ry;
+    }
+    cluster_sync();
+    int gone_above = s.above[warp], gone_equal = s.equal[warp];  // before this warp's part, in the row
+    for (uint32_t r = 0; r < rank; ++r) {
+        gone_above += peer_word(&s.total[0], r);
+        gone_equal += peer_word(&s.total[1], r);
+    }
+    cluster_sync();  // no CTA leaves while another reads its totals
+    for (int i0 = lo; i0 < hi; i0 += kSelectStep) {
+        const uint4 k = keys_at(i0);
+        const uint32_t* p = &k.x;
+        // a lane's counts of both kinds in one word (at most 128 each a step), summed over the lanes before
+        uint32_t both = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) both += (p[j] > prefix ? 1u : 0u) + (p[j] == prefix ? 1u << 16 : 0u);
+        uint32_t run = both;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, run, d);
+            if (lane >= d) run += up;
+        }
+        const uint32_t all = __shfl_sync(0xffffffffu, run, 31);
+        run -= both;
+        int at = gone_above + (int)(run & 0xffff), ties = gone_equal + (int)(run >> 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // of the keys on the edge the first `need` of the row stay
+            const bool tie = p[j] == prefix, sure = p[j] > prefix;
+            if (sure || (tie && ties < need)) keep[at + min(ties, need)] = i0 + 4 * lane + j;
+            at += sure;
+            ties += tie;
+        }
+        gone_above += (int)(all & 0xffff);
+        gone_equal += (int)(all >> 16);
+    }
+}
+
+// Shared memory of the selection for `keys` cached keys per CTA.
+static size_t select_smem(int64_t keys) { return sizeof(SelectShared) + (size_t)keys * 4; }
+
+// Once per device: the selection kernel's shared-memory limit.
+static om_status prepare_select(const DeviceState* d) {
+    static std::mutex mu;
+    static bool ready[128];
+    std::lock_guard<std::mutex> lk(mu);
+    if (!ready[d->dev]) {
+        for (auto* kern : {evict_select_kernel<true>, evict_select_kernel<false>})
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)select_smem(kMaxCached)) != cudaSuccess) {
+                cudaGetLastError();
+                return OM_ECUDA;
+            }
+        ready[d->dev] = true;
+    }
+    return OM_OK;
+}
+
+static cudaError_t launch_select(const EvictArgs& a, int64_t rows, int sm_count, cudaStream_t st) {
+    // As many CTAs per row as fill the SMs (two CTAs each), but at least 2048 entries a CTA.
+    int ctas = 1;
+    while (ctas < kMaxCluster && rows * ctas * 2 <= 2 * (int64_t)sm_count && a.length > ctas * 2048) ctas *= 2;
+    const int64_t warps = ctas * kSelectWarps;
+    const int64_t per_warp = (((a.length + warps - 1) / warps) + kSelectStep - 1) / kSelectStep * kSelectStep;
+    const int64_t keys = per_warp * kSelectWarps;
+    const bool cached = keys <= kMaxCached;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * ctas));
+    cfg.blockDim = dim3(kSelectThreads);
+    cfg.dynamicSmemBytes = select_smem(cached ? keys : 0);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto* kern = cached ? evict_select_kernel<true> : evict_select_kernel<false>;
+    return traced(kKindEvict, st, [&] { cudaLaunchKernelEx(&cfg, kern, a); });
 }
 
 // --------------------------------------------------------------- gather --
@@ -161,40 +496,67 @@ constexpr int kMaxArrays = 8;
 
 struct GatherArgs {
     om_cache_array arrays[kMaxArrays];
+    int first_cta[kMaxArrays];  // of each array; a row's entries are cut into tiles, one CTA each
+    int tiles[kMaxArrays], tile_entries[kMaxArrays], vector[kMaxArrays];
     const int32_t* keep;
-    int64_t slots;  // batch * heads * budget
-    int64_t budget, length;
-    int heads;
+    int64_t length;
+    int budget, heads, count;
 };
 
-// One thread per vector of a kept entry.
+constexpr int kGatherThreads = 256;
+constexpr int kGatherUnroll = 4;  // vectors in flight per thread
+
+// One tile of one row of one array: the CTA's threads take its vectors in turn.
 template <typename V>
-__device__ void gather_array(const GatherArgs& a, const om_cache_array& c) {
+__device__ __forceinline__ void gather_tile(const GatherArgs& a, const om_cache_array& c, int64_t row, int j0, int j1) {
     const int per = (int)(c.entry_bytes / (int)sizeof(V));
-    const int64_t total = a.slots * per, step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
-        const int64_t slot = i / per, piece = i % per, row = slot / a.budget, j = slot % a.budget;
-        const int64_t b = row / a.heads, h = row % a.heads;
-        const int32_t from = a.keep[slot];
-        V v{};
-        if (from >= 0 && from < a.length)
-            v = *reinterpret_cast<const V*>(static_cast<const char*>(c.src) + b * c.src_batch + h * c.src_head +
-                                            from * c.src_entry + piece * (int64_t)sizeof(V));
-        *reinterpret_cast<V*>(static_cast<char*>(c.dst) + b * c.dst_batch + h * c.dst_head + j * c.dst_entry +
-                              piece * (int64_t)sizeof(V)) = v;
+    const int64_t b = row / a.heads, h = row % a.heads;
+    const char* src = static_cast<const char*>(c.src) + b * c.src_batch + h * c.src_head;
+    char* dst = static_cast<char*>(c.dst) + b * c.dst_batch + h * c.dst_head;
+    const int32_t* keep = a.keep + row * a.budget;
+    const int total = (j1 - j0) * per;
+    for (int i0 = threadIdx.x; i0 < total; i0 += kGatherThreads * kGatherUnroll) {
+        V v[kGatherUnroll];
+        int64_t to[kGatherUnroll];
+#pragma unroll
+        for (int u = 0; u < kGatherUnroll; ++u) {
+            const int i = i0 + u * kGatherThreads;
+            v[u] = V{};
+            to[u] = -1;
+            if (i < total) {
+                const int j = i / per, piece = (i - j * per) * (int)sizeof(V);
+                const int32_t from = __ldg(keep + j0 + j);
+                to[u] = (j0 + j) * c.dst_entry + piece;
+                if (from >= 0 && from < a.length)
+                    v[u] = __ldcs(reinterpret_cast<const V*>(src + from * c.src_entry + piece));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kGatherUnroll; ++u)
+            if (to[u] >= 0) __stcs(reinterpret_cast<V*>(dst + to[u]), v[u]);
     }
 }
 
-__global__ void __launch_bounds__(256) evict_gather_kernel(GatherArgs a) {
-    const om_cache_array& c = a.arrays[blockIdx.y];
+__global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const __grid_constant__ GatherArgs a) {
+    int k = a.count - 1;
+    while (k > 0 && (int)blockIdx.x < a.first_cta[k]) --k;
+    const int t = (int)blockIdx.x - a.first_cta[k], row = t / a.tiles[k];
+    const int j0 = (t - row * a.tiles[k]) * a.tile_entries[k], j1 = min(j0 + a.tile_entries[k], a.budget);
+    switch (a.vector[k]) {
+        case 16: gather_tile<uint4>(a, a.arrays[k], row, j0, j1); break;
+        case 4: gather_tile<uint32_t>(a, a.arrays[k], row, j0, j1); break;
+        case 2: gather_tile<unsigned short>(a, a.arrays[k], row, j0, j1); break;
+        default: gather_tile<unsigned char>(a, a.arrays[k], row, j0, j1); break;
+    }
+}
+
+// Bytes of the vectors that every address of the array allows.
+static int gather_vector(const om_cache_array& c) {
     const uint64_t low = reinterpret_cast<uintptr_t>(c.src) | reinterpret_cast<uintptr_t>(c.dst) |
                          (uint64_t)c.src_batch | (uint64_t)c.src_head | (uint64_t)c.src_entry |
                          (uint64_t)c.dst_batch | (uint64_t)c.dst_head | (uint64_t)c.dst_entry |
                          (uint64_t)c.entry_bytes;
-    if ((low & 15) == 0) gather_array<uint4>(a, c);
-    else if ((low & 3) == 0) gather_array<uint32_t>(a, c);
-    else if ((low & 1) == 0) gather_array<uint16_t>(a, c);
-    else gather_array<uint8_t>(a, c);
+    return (low & 15) == 0 ? 16 : (low & 3) == 0 ? 4 : (low & 1) == 0 ? 2 : 1;
 }
 
 // Largest strides taken, so that no span of an array overflows 64 bits.
@@ -256,10 +618,8 @@ om_status om_accumulate_weights(int value_type, const void* weights, int64_t bat
     AccumulateArgs a{weights, score, lengths, out,    w_batch, w_head,        w_query, s_batch, s_head, o_batch, o_head,
                      length,  (int)kv_heads, (int)(q_heads / kv_heads), (int)queries, decay};
     cudaStream_t st = (cudaStream_t)stream;
-    const dim3 grid((unsigned)((length + 255) / 256), (unsigned)(batch * kv_heads));
-    const cudaError_t e = with_value_type(value_type, [&](auto v) {
-        return traced(kKindEvict, st, [&] { accumulate_weights_kernel<decltype(v)><<<grid, 256, 0, st>>>(a); });
-    });
+    const cudaError_t e =
+        with_value_type(value_type, [&](auto v) { return launch_accumulate<decltype(v)>(a, batch, st); });
     return e == cudaSuccess ? OM_OK : cuda_fail(e);
 }
 
@@ -270,7 +630,7 @@ om_status om_evict_select(const float* score, int64_t batch, int64_t heads, int6
         return OM_EINVAL;
     if (first > budget || last > budget - first) return OM_EINVAL;
     if (length > INT32_MAX - 65536 || budget > INT32_MAX - 65536 || heads > 65535 || batch > 32767 ||
-        s_batch > kMaxStride || s_head > kMaxStride)
+        batch * heads > (1 << 27) || s_batch > kMaxStride || s_head > kMaxStride)
         return OM_ERANGE;
     if (batch == 0) return OM_OK;
     if (keep == nullptr || kept == nullptr || (length > 0 && score == nullptr) || misaligned4(score) ||
@@ -283,9 +643,11 @@ om_status om_evict_select(const float* score, int64_t batch, int64_t heads, int6
         return OM_EINVAL;
     EvictArgs a{score, lengths, keep, kept, s_batch, s_head, (int)length, (int)heads, (int)budget, (int)first, (int)last};
     cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = traced(kKindEvict, st, [&] {
-        evict_select_kernel<<<(unsigned)(batch * heads), kSelectThreads, 0, st>>>(a);
-    });
+    DeviceState* d = nullptr;
+    om_status ds = device_state(&d);
+    if (ds == OM_OK) ds = prepare_select(d);
+    if (ds != OM_OK) return ds;
+    const cudaError_t e = launch_select(a, batch * heads, d->sm_count, st);
     return e == cudaSuccess ? OM_OK : cuda_fail(e);
 }
 
@@ -323,16 +685,26 @@ om_status om_evict_gather(const int32_t* keep, int64_t batch, int64_t heads, int
                 (i < j && overlaps(a.arrays[i].dst, spans[i], a.arrays[j].dst, spans[j], 1)))
                 return OM_EINVAL;
     a.keep = keep;
-    a.slots = slots;
-    a.budget = budget;
     a.length = length;
+    a.budget = (int)budget;
     a.heads = (int)heads;
+    a.count = count;
+    int64_t ctas = 0;
+    for (int i = 0; i < count; ++i) {
+        // tiles of about kGatherUnroll vectors per thread
+        a.vector[i] = gather_vector(a.arrays[i]);
+        const int64_t per = a.arrays[i].entry_bytes / a.vector[i];
+        int64_t entries = kGatherThreads * kGatherUnroll / per;
+        if (entries < 1) entries = 1;
+        a.tile_entries[i] = (int)entries;
+        a.tiles[i] = (int)((budget + entries - 1) / entries);
+        a.first_cta[i] = (int)ctas;
+        ctas += batch * heads * a.tiles[i];
+        if (ctas > INT32_MAX) return OM_ERANGE;
+    }
     cudaStream_t st = (cudaStream_t)stream;
-    DeviceState* d = nullptr;
-    const om_status s = device_state(&d);
-    if (s != OM_OK) return s;
-    const dim3 grid((unsigned)(d->sm_count * 8), (unsigned)count);
-    const cudaError_t e = traced(kKindEvict, st, [&] { evict_gather_kernel<<<grid, 256, 0, st>>>(a); });
+    const cudaError_t e = traced(
+        kKindEvict, st, [&] { evict_gather_kernel<<<(unsigned)ctas, kGatherThreads, 0, st>>>(a); });
     return e == cudaSuccess ? OM_OK : cuda_fail(e);
 }
 
