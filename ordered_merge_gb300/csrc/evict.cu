@@ -29,22 +29,44 @@ __device__ __forceinline__ int64_t valid_length(const int32_t* lengths, int64_t 
     return n < 0 ? 0 : n < length ? n : length;
 }
 
-// The two 16-bit values of a word, or the one 32-bit value, added to sums.
-__device__ __forceinline__ void add_word(float* sum, uint32_t w, float) { sum[0] += __uint_as_float(w); }
-__device__ __forceinline__ void add_word(float* sum, uint32_t w, __nv_bfloat16) {
-    sum[0] += __uint_as_float(w << 16);
-    sum[1] += __uint_as_float(w & 0xffff0000u);
+// Two sums in one register pair, added to at once.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
 }
-__device__ __forceinline__ void add_word(float* sum, uint32_t w, __half) {
+__device__ __forceinline__ float2 unpack2(uint64_t p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ void add2(uint64_t& sum, uint64_t x) {
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(x));
+}
+// The values of a 16-byte vector added to their sums.
+__device__ __forceinline__ void add_vector(uint64_t (&sum)[2], const uint4& w, float) {
+    add2(sum[0], pack2(__uint_as_float(w.x), __uint_as_float(w.y)));
+    add2(sum[1], pack2(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+__device__ __forceinline__ void add_word(uint64_t& sum, uint32_t w, __nv_bfloat16) {
+    add2(sum, pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
+}
+__device__ __forceinline__ void add_word(uint64_t& sum, uint32_t w, __half) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-    sum[0] += f.x;
-    sum[1] += f.y;
+    add2(sum, pack2(f.x, f.y));
+}
+template <typename T>
+__device__ __forceinline__ void add_vector(uint64_t (&sum)[4], const uint4& w, T) {
+    add_word(sum[0], w.x, T{});
+    add_word(sum[1], w.y, T{});
+    add_word(sum[2], w.z, T{});
+    add_word(sum[3], w.w, T{});
 }
 
-constexpr int kAccWarps = 8;
+constexpr int kAccMaxWarps = 8;
 
 // A warp sums rows over one tile of entries, V = 16 bytes' worth per lane; the
-// rows of a tile (share * queries of them) are split over `split` warps of
+// rows of a tile (share * queries of them) are split over 2^log_split warps of
 // the CTA, whose sums are then added in the order of the warps, so the result
 // depends on the shapes alone.
 //
@@ -56,126 +78,203 @@ constexpr int kAccWarps = 8;
 // (query mod V, head, query), in which the offset changes least often.  The
 // tile is then 31 lanes wide, as the last lane's vector reaches past it.  A
 // vector that holds no value of the row's valid part is not loaded.
-template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(kAccWarps * 32) accumulate_weights_kernel(AccumulateArgs a, int split) {
+//
+// DIRECT: one warp a tile, and aligned outputs: the lanes write their sums
+// themselves, with no turn through shared memory.
+template <typename T, bool ALIGNED, bool DIRECT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) accumulate_weights_kernel(AccumulateArgs a, int log_split) {
     constexpr int V = 16 / (int)sizeof(T), LANES = ALIGNED ? 32 : 31, TILE = LANES * V, U = 8;
-    __shared__ __align__(16) float s_sum[kAccWarps][32 * V];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % split;
-    const int tiles = kAccWarps / split;  // of this CTA
-    const int64_t b = blockIdx.y / a.kv_heads, h = blockIdx.y % a.kv_heads;
+    constexpr int STEP = ALIGNED ? 1 : V;  // queries between neighbours of the walk
+    // Entry e of a tile is at (e mod V) * PITCH + e / V: the pitch keeps both
+    // the lanes' writes and the reads of consecutive entries off each other's banks.
+    constexpr int PITCH = 32 + 32 / V;
+    __shared__ float s_sum[DIRECT ? 1 : WARPS][V * PITCH];
+    if (DIRECT) log_split = 0;
+    const int split = 1 << log_split, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp & (split - 1);
+    const int wide = (WARPS >> log_split) * TILE;  // entries of this CTA
+    const unsigned b = blockIdx.y / (unsigned)a.kv_heads, h = blockIdx.y - b * (unsigned)a.kv_heads;
     const int64_t n = valid_length(a.lengths, b, a.length);
-    const int64_t first = (int64_t)blockIdx.x * tiles * TILE;
-    const int64_t c0 = first + (warp / split) * TILE;
-    const int rows = a.share * a.queries;
-    const int r0 = (int)((int64_t)rows * part / split), r1 = (int)((int64_t)rows * (part + 1) / split);
+    const int64_t first = (int64_t)blockIdx.x * wide;
+    const int live = (int)max((int64_t)0, min(n - first, (int64_t)wide));  // valid ones among them
+    const int there = (int)min(a.length - first, (int64_t)wide);
+    const int c0 = (warp >> log_split) * TILE;  // this warp's first one
+    const int64_t rows = (int64_t)a.share * a.queries;
+    const int r0 = (int)(rows * part >> log_split), r1 = (int)(rows * (part + 1) >> log_split);
+    const float* score = a.score == nullptr ? nullptr : a.score + b * a.s_batch + h * a.s_head + first;
+    float* out = a.out + b * a.o_batch + h * a.o_head + first;
     // the old scores this thread will need, so that they arrive meanwhile
     float old[V];
-    const float* score = a.score == nullptr ? nullptr : a.score + b * a.s_batch + h * a.s_head;
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        const int j = k * kAccWarps * 32 + threadIdx.x;
-        old[k] = 0.0f;
-        if (score != nullptr && j < tiles * TILE && first + j < n) old[k] = __ldcs(score + first + j);
-    }
-    float sum[V];
+    for (int k = 0; k < V; ++k) old[k] = 0.0f;
+    if (score != nullptr) {
+        if (DIRECT) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) sum[v] = 0.0f;
-    if (!ALIGNED) {
+            for (int k = 0; k < V; k += 4) {
+                const int j = c0 + lane * V + k;
+                if (j + 3 < live) {
+                    const float4 x = __ldcs(reinterpret_cast<const float4*>(score + j));
+                    old[k] = x.x, old[k + 1] = x.y, old[k + 2] = x.z, old[k + 3] = x.w;
+                } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) s_sum[warp][lane * V + v] = 0.0f;
-        __syncwarp();
-    }
-    if (c0 < n && r0 < r1) {
-        const char* base = reinterpret_cast<const char*>(static_cast<const T*>(a.weights) + b * a.w_batch +
-                                                         h * a.share * a.w_head + c0);
-        // the r0-th row of the walk: class c = query mod V, head g, query q
-        int c = 0, before = r0;
-        int in_class = (a.queries + V - 1) / V;  // queries of class c
-        while (before >= a.share * in_class) {
-            before -= a.share * in_class;
-            ++c;
-            in_class = (a.queries - c + V - 1) / V;
+                    for (int i = 0; i < 3; ++i)
+                        if (j + i < live) old[k + i] = score[j + i];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                if (k * WARPS * 32 + (int)threadIdx.x < live) old[k] = __ldcs(score + k * WARPS * 32 + threadIdx.x);
         }
-        int g = before / in_class, q = c + (before - g * in_class) * V;
-        int cur = 0;  // offset, in values, of what `sum` holds
+    }
+    uint64_t sum[V / 2];
+#pragma unroll
+    for (int v = 0; v < V / 2; ++v) sum[v] = 0;
+    int cur = -1;  // offset, in values, of what `sum` holds
+    bool fresh = true;
+    // adds the sums to the tile's entries; entries left of it or past its end are other tiles'
+    auto settle = [&] {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = lane * V + v - cur;
+            float* at = &s_sum[warp][(e & (V - 1)) * PITCH + e / V];
+            const float2 two = unpack2(sum[v / 2]);
+            const float x = v & 1 ? two.y : two.x;
+            if (e >= 0) *at = fresh ? x : *at + x;
+        }
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) sum[v] = 0;
+        fresh = false;
+        __syncwarp();
+    };
+    if (c0 < live && r0 < r1) {
+        constexpr int64_t size = (int64_t)sizeof(T);
+        const char* base = reinterpret_cast<const char*>(static_cast<const T*>(a.weights) + b * a.w_batch +
+                                                         (int64_t)h * a.share * a.w_head + first + c0);
+        // the r0-th row of the walk: class c = query mod STEP, head g, query q
+        int c = 0, before = r0, in_class = (a.queries + STEP - 1) / STEP, g = 0, q = 0;
+        if (r0 > 0) {
+            while (before >= a.share * in_class) {
+                before -= a.share * in_class;
+                ++c;
+                in_class = (a.queries - c + STEP - 1) / STEP;
+            }
+            g = before / in_class;
+            q = c + (before - g * in_class) * STEP;
+        }
+        const char* head = base + (g * a.w_head + c * a.w_query) * size;  // query c of head g
+        const char* at = base + (g * a.w_head + q * a.w_query) * size;
+        const int64_t step = STEP * a.w_query * size;
+        const int room = (int)min(n - first - c0 - lane * V, (int64_t)1 << 20);  // valid from this lane's first on
         for (int r = r0; r < r1; r += U) {
             uint4 w[U];
-            int skip[U];
+            int skip[U], changes = 0;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 w[u] = make_uint4(0, 0, 0, 0);
-                skip[u] = -1;
+                skip[u] = u > 0 ? skip[u - 1] : 0;
                 if (r + u < r1) {
-                    const char* at = base + (g * a.w_head + q * a.w_query) * (int64_t)sizeof(T);
-                    if ((q += V) >= a.queries) {
-                        if (++g == a.share) g = 0, ++c;
-                        q = c;
-                    }
-                    skip[u] = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(at) & 15) / (int)sizeof(T);
-                    if (c0 + lane * V - skip[u] < n)
+                    if (!ALIGNED) skip[u] = (int)(reinterpret_cast<uintptr_t>(at) & 15) / (int)sizeof(T);
+                    if (room + skip[u] > 0)
                         w[u] = __ldcs(reinterpret_cast<const uint4*>(at - skip[u] * (int)sizeof(T)) + lane);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (!ALIGNED && skip[u] >= 0 && skip[u] != cur) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        if (lane * V + v >= cur) s_sum[warp][lane * V + v - cur] += sum[v];
-                        sum[v] = 0.0f;
+                    at += step;
+                    q += STEP;
+                    if (q >= a.queries) {
+                        if (ALIGNED || ++g < a.share) {
+                            head += a.w_head * size;
+                        } else {
+                            g = 0;
+                            ++c;
+                            head = base + c * a.w_query * size;
+                        }
+                        q = c;
+                        at = head;
                     }
-                    __syncwarp();
-                    cur = skip[u];
                 }
-                add_word(sum, w[u].x, T{});
-                add_word(sum + V / 4, w[u].y, T{});
-                add_word(sum + V / 2, w[u].z, T{});
-                add_word(sum + 3 * V / 4, w[u].w, T{});
+                changes |= skip[u] ^ skip[0];
+            }
+            if (!ALIGNED && cur != skip[0]) {
+                if (cur >= 0) settle();
+                cur = skip[0];
+            }
+            if (ALIGNED || changes == 0) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) add_vector(sum, w[u], T{});
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (skip[u] != cur) settle(), cur = skip[u];
+                    add_vector(sum, w[u], T{});
+                }
             }
         }
-        if (!ALIGNED) {
+    }
+    if (DIRECT) {
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (lane * V + v >= cur) s_sum[warp][lane * V + v - cur] += sum[v];
+        for (int k = 0; k < V; k += 4) {
+            const int j = c0 + lane * V + k;
+            const float2 lo = unpack2(sum[k / 2]), hi = unpack2(sum[k / 2 + 1]);
+            float x[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (score != nullptr) x[i] += a.decay * old[k + i];
+                if (j + i >= live) x[i] = 0.0f;
+            }
+            if (j + 3 < there) {
+                __stcs(reinterpret_cast<float4*>(out + j), make_float4(x[0], x[1], x[2], x[3]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    if (j + i < there) out[j + i] = x[i];
+            }
         }
+        return;
     }
-    if (ALIGNED) {
-#pragma unroll
-        for (int v = 0; v < V; v += 4)
-            *reinterpret_cast<float4*>(&s_sum[warp][lane * V + v]) =
-                make_float4(sum[v], sum[v + 1], sum[v + 2], sum[v + 3]);
-    }
+    if (cur < 0) cur = 0;
+    settle();
     __syncthreads();
-    float* out = a.out + b * a.o_batch + h * a.o_head;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        const int j = k * kAccWarps * 32 + threadIdx.x;
-        const int64_t i = first + j;
-        if (j >= tiles * TILE || i >= a.length) break;
+        const int j = k * WARPS * 32 + threadIdx.x;
+        if (j >= there) break;
         float total = 0.0f;
-        if (i < n) {
-            const int t = j / TILE, col = j - t * TILE;
-            for (int w = 0; w < split; ++w) total += s_sum[t * split + w][col];
+        if (j < live) {
+            const int t = j / TILE, e = j - t * TILE;
+            const float* p = &s_sum[t << log_split][(e & (V - 1)) * PITCH + e / V];
+            for (int w = 0; w < split; ++w) total += p[w * V * PITCH];
             if (score != nullptr) total += a.decay * old[k];
         }
-        __stcs(out + i, total);
+        __stcs(out + j, total);
     }
 }
 
+template <typename T, bool ALIGNED>
+static void launch_accumulate_split(const AccumulateArgs& a, dim3 grid, int log_split, bool direct, cudaStream_t st) {
+    if (ALIGNED && direct) accumulate_weights_kernel<T, ALIGNED, ALIGNED, 2><<<grid, 2 * 32, 0, st>>>(a, 0);
+    else if (log_split <= 1) accumulate_weights_kernel<T, ALIGNED, false, 2><<<grid, 2 * 32, 0, st>>>(a, log_split);
+    else if (log_split == 2) accumulate_weights_kernel<T, ALIGNED, false, 4><<<grid, 4 * 32, 0, st>>>(a, log_split);
+    else accumulate_weights_kernel<T, ALIGNED, false, 8><<<grid, 8 * 32, 0, st>>>(a, log_split);
+}
+
 template <typename T>
-static cudaError_t launch_accumulate(const AccumulateArgs& a, int64_t batch, cudaStream_t st) {
+static cudaError_t launch_accumulate(const AccumulateArgs& a, int64_t batch, int sm_count, cudaStream_t st) {
     constexpr int V = 16 / (int)sizeof(T);
     const int64_t rows = (int64_t)a.share * a.queries;
-    int split = 1;  // at least 8 rows a warp: one batch of its loads
-    while (split < kAccWarps && rows >= 16 * split) split *= 2;
     const uint64_t low = reinterpret_cast<uintptr_t>(a.weights) / sizeof(T) | (uint64_t)a.w_batch |
                          (uint64_t)a.w_head | (uint64_t)a.w_query;
     const bool aligned = low % V == 0;
-    const int64_t wide = (int64_t)(kAccWarps / split) * (aligned ? 32 : 31) * V;
+    const int64_t tile = (aligned ? 32 : 31) * V, tiles = (a.length + tile - 1) / tile * batch * a.kv_heads;
+    // as few warps a tile as fill the GPU with 32 warps an SM, while each has a batch of 8 rows
+    int log_split = 0;
+    while ((1 << log_split) < kAccMaxWarps && rows >= 16 << log_split && tiles << log_split < 32 * (int64_t)sm_count)
+        ++log_split;
+    uint64_t low4 = reinterpret_cast<uintptr_t>(a.out) / 4 | (uint64_t)a.o_batch | (uint64_t)a.o_head;
+    if (a.score != nullptr) low4 |= reinterpret_cast<uintptr_t>(a.score) / 4 | (uint64_t)a.s_batch | (uint64_t)a.s_head;
+    const bool direct = log_split == 0 && low4 % 4 == 0;
+    const int64_t wide = (log_split == 0 ? 2 : 1) * tile;
     const dim3 grid((unsigned)((a.length + wide - 1) / wide), (unsigned)(batch * a.kv_heads));
     return traced(kKindEvict, st, [&] {
-        if (aligned) accumulate_weights_kernel<T, true><<<grid, kAccWarps * 32, 0, st>>>(a, split);
-        else accumulate_weights_kernel<T, false><<<grid, kAccWarps * 32, 0, st>>>(a, split);
+        if (aligned) launch_accumulate_split<T, true>(a, grid, log_split, direct, st);
+        else launch_accumulate_split<T, false>(a, grid, log_split, direct, st);
     });
 }
 
@@ -195,6 +294,7 @@ constexpr int kSelectStep = 128;  // keys a warp takes at a time, four consecuti
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kDigitBits = 11;
 constexpr int kDigits = 1 << kDigitBits;
+constexpr int kCoarse = kDigits / 32;
 constexpr int kPasses = 3;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxCached = 48 * 1024;  // keys a CTA can hold in shared memory (192 KB)
@@ -219,7 +319,7 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// A word, or four, of CTA `rank`'s shared memory, at the address p has in this CTA's.
+// A word of CTA `rank`'s shared memory, at the address p has in this CTA's.
 __device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
     uint32_t at;
     int v;
@@ -228,41 +328,36 @@ __device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
     return v;
 }
 
-__device__ __forceinline__ int4 peer_words(const int* p, uint32_t rank) {
-    uint32_t at;
-    int4 v;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(at)
-                 : "memory");
-    return v;
-}
 
-// Sum of `mine` over the threads before.
-__device__ __forceinline__ int block_before(int mine, int* s_part) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Finds, among 32 * P counts held P per lane with the greatest place in lane 0's
+// first, the place at which the sum from the top reaches `need`; *over is the
+// sum above it.
+template <int P>
+__device__ __forceinline__ int place_of(const int (&c)[P], int need, int* over) {
+    const int lane = threadIdx.x & 31;
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < P; ++j) mine += c[j];
     int run = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int up = __shfl_up_sync(0xffffffffu, run, d);
         if (lane >= d) run += up;
     }
-    if (lane == 31) s_part[warp] = run;
-    __syncthreads();
-    int w = lane < kSelectWarps ? s_part[lane] : 0;
+    const int owner = __ffs(__ballot_sync(0xffffffffu, run >= need)) - 1;
+    int above = run - mine, place = lane * P;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, w, d);
-        if (lane >= d) w += up;
-    }
-    const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
-    return (warp > 0 ? before : 0) + run - mine;
+    for (int j = 0; j + 1 < P; ++j)
+        if (above + c[j] < need) above += c[j], ++place;
+        else break;
+    *over = __shfl_sync(0xffffffffu, above, owner & 31);
+    return __shfl_sync(0xffffffffu, place, owner & 31);
 }
 
 struct SelectShared {
     __align__(16) int hist[kPasses][kDigits];
-    int part[kPasses][kSelectWarps];
+    int coarse[kPasses][kCoarse];        // sums of 32 digits each
+    int peers[kMaxCluster][kCoarse];     // the cluster's
     int above[kSelectWarps], equal[kSelectWarps];  // kept for sure / on the edge, in the warps before
     int total[2];                                  // the same of the CTA
     int digit, over;
@@ -359,29 +454,30 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(EvictAr
                 count(k.x), count(k.y), count(k.z), count(k.w);
             }
         }
-        cluster_sync();
-        // four digits a thread, from the greatest down, summed over the cluster
-        const int low = kDigits - 4 - 4 * threadIdx.x;
-        int4 c = make_int4(0, 0, 0, 0);
+        __syncthreads();
 #pragma unroll
-        for (uint32_t r = 0; r < kMaxCluster; ++r) {
-            if (r < ctas) {
-                const int4 p = peer_words(&s.hist[pass][low], r);
-                c.x += p.x, c.y += p.y, c.z += p.z, c.w += p.w;
-            }
+        for (int j = 0; j < kCoarse / kSelectWarps; ++j) {
+            const int at = warp * (kCoarse / kSelectWarps) + j;
+            const int c = __reduce_add_sync(0xffffffffu, s.hist[pass][at * 32 + lane]);
+            if (lane == 0) s.coarse[pass][at] = c;
         }
-        int above = block_before(c.x + c.y + c.z + c.w, s.part[pass]);
-        if (above < need && need <= above + c.x + c.y + c.z + c.w) {  // one thread
-            int digit = low + 3;
-            if (need > above + c.w) {
-                above += c.w, --digit;
-                if (need > above + c.z) {
-                    above += c.z, --digit;
-                    if (need > above + c.y) above += c.y, --digit;
-                }
-            }
-            s.digit = digit;
-            s.over = above;
+        cluster_sync();
+        // first which 32 digits, then which of them, both summed over the cluster
+        for (int i = threadIdx.x; i < (int)ctas * kCoarse; i += kSelectThreads)
+            (&s.peers[0][0])[i] = peer_word(&s.coarse[pass][i % kCoarse], i / kCoarse);
+        __syncthreads();
+        if (warp == 0) {
+            int c[kCoarse / 32] = {}, over, more;
+            for (uint32_t r = 0; r < ctas; ++r)
+#pragma unroll
+                for (int j = 0; j < kCoarse / 32; ++j) c[j] += s.peers[r][kCoarse - 1 - (lane * (kCoarse / 32) + j)];
+            const int top = kCoarse - 1 - place_of(c, need, &over);
+            int f[1] = {0};
+#pragma unroll
+            for (uint32_t r = 0; r < kMaxCluster; ++r)
+                if (r < ctas) f[0] += peer_word(&s.hist[pass][top * 32 + 31 - lane], r);
+            const int fine = 31 - place_of(f, need - over, &more);
+            if (lane == 0) s.digit = top * 32 + fine, s.over = over + more;
         }
         __syncthreads();
         prefix |= (uint32_t)s.digit << shift;
@@ -418,32 +514,53 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(EvictAr
         gone_equal += peer_word(&s.total[1], r);
     }
     cluster_sync();  // no CTA leaves while another reads its totals
-    for (int i0 = lo; i0 < hi; i0 += kSelectStep) {
-        const uint4 k = keys_at(i0);
-        const uint32_t* p = &k.x;
-        // a lane's counts of both kinds in one word (at most 128 each a step), summed over the lanes before
-        uint32_t both = 0;
+    constexpr int U = 4;  // steps whose counts are summed together, a byte each (at most 128)
+    for (int i0 = lo; i0 < hi; i0 += kSelectStep * U) {
+        uint4 k[U];
+        uint32_t sures = 0, ties = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) both += (p[j] > prefix ? 1u : 0u) + (p[j] == prefix ? 1u << 16 : 0u);
-        uint32_t run = both;
+        for (int u = 0; u < U; ++u) {
+            const int at = i0 + u * kSelectStep;
+            k[u] = at < hi ? keys_at(at) : make_uint4(0, 0, 0, 0);
+            const uint32_t* p = &k[u].x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sures += p[j] > prefix ? 1u << (8 * u) : 0u;
+                ties += p[j] == prefix ? 1u << (8 * u) : 0u;
+            }
+        }
+        uint32_t run_s = sures, run_t = ties;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t up = __shfl_up_sync(0xffffffffu, run, d);
-            if (lane >= d) run += up;
+            const uint32_t us = __shfl_up_sync(0xffffffffu, run_s, d), ut = __shfl_up_sync(0xffffffffu, run_t, d);
+            if (lane >= d) run_s += us, run_t += ut;
         }
-        const uint32_t all = __shfl_sync(0xffffffffu, run, 31);
-        run -= both;
-        int at = gone_above + (int)(run & 0xffff), ties = gone_equal + (int)(run >> 16);
+        const uint32_t all_s = __shfl_sync(0xffffffffu, run_s, 31), all_t = __shfl_sync(0xffffffffu, run_t, 31);
+        run_s -= sures;
+        run_t -= ties;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            // of the keys on the edge the first `need` of the row stay
-            const bool tie = p[j] == prefix, sure = p[j] > prefix;
-            if (sure || (tie && ties < need)) keep[at + min(ties, need)] = i0 + 4 * lane + j;
-            at += sure;
-            ties += tie;
+        for (int u = 0; u < U; ++u) {
+            const uint32_t* p = &k[u].x;
+            const int i = i0 + u * kSelectStep + 4 * lane;
+            int at = gone_above + min(gone_equal, need) + (int)(run_s >> (8 * u) & 255);
+            if ((all_t >> (8 * u) & 255) == 0) {  // nothing on the edge in this step
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (p[j] > prefix) keep[at++] = i + j;
+            } else {
+                int tied = gone_equal + (int)(run_t >> (8 * u) & 255);
+                at += min(tied, need) - min(gone_equal, need);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // of the keys on the edge the first `need` of the row stay
+                    const bool tie = p[j] == prefix;
+                    if (p[j] > prefix || (tie && tied < need)) keep[at++] = i + j;
+                    tied += tie;
+                }
+            }
+            gone_above += (int)(all_s >> (8 * u) & 255);
+            gone_equal += (int)(all_t >> (8 * u) & 255);
         }
-        gone_above += (int)(all & 0xffff);
-        gone_equal += (int)(all >> 16);
     }
 }
 
@@ -503,7 +620,7 @@ struct GatherArgs {
     int budget, heads, count;
 };
 
-constexpr int kGatherThreads = 256;
+constexpr int kGatherThreads = 64;
 constexpr int kGatherUnroll = 4;  // vectors in flight per thread
 
 // One tile of one row of one array: the CTA's threads take its vectors in turn.
@@ -598,7 +715,8 @@ om_status om_accumulate_weights(int value_type, const void* weights, int64_t bat
         return OM_EINVAL;
     for (const int64_t s : {w_batch, w_head, w_query, s_batch, s_head, o_batch, o_head})
         if (s < 0) return OM_EINVAL;
-    if (length > INT32_MAX || queries > 65535 || q_heads > 65535 || batch > 65535 || batch * kv_heads > 65535)
+    if (length > INT32_MAX || queries > 65535 || q_heads > 65535 || batch > 65535 || batch * kv_heads > 65535 ||
+        q_heads / kv_heads * queries > INT32_MAX - 64)
         return OM_ERANGE;
     for (const int64_t s : {w_batch, w_head, w_query, s_batch, s_head, o_batch, o_head})
         if (s > kMaxStride) return OM_ERANGE;
@@ -617,9 +735,12 @@ om_status om_accumulate_weights(int value_type, const void* weights, int64_t bat
         return OM_EINVAL;
     AccumulateArgs a{weights, score, lengths, out,    w_batch, w_head,        w_query, s_batch, s_head, o_batch, o_head,
                      length,  (int)kv_heads, (int)(q_heads / kv_heads), (int)queries, decay};
+    DeviceState* d = nullptr;
+    const om_status s = device_state(&d);
+    if (s != OM_OK) return s;
     cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e =
-        with_value_type(value_type, [&](auto v) { return launch_accumulate<decltype(v)>(a, batch, st); });
+        with_value_type(value_type, [&](auto v) { return launch_accumulate<decltype(v)>(a, batch, d->sm_count, st); });
     return e == cudaSuccess ? OM_OK : cuda_fail(e);
 }
 
