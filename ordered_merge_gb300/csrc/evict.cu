@@ -63,7 +63,34 @@ __device__ __forceinline__ void add_vector(uint64_t (&sum)[4], const uint4& w, T
     add_word(sum[3], w.w, T{});
 }
 
+// The vector that starts `skip` values (of type T) into a lane's w and goes on
+// in the next lane's.  All lanes of the warp, with one skip.
+template <typename T>
+__device__ __noinline__ uint4 shifted(uint4 w, int skip) {
+    uint32_t x[5] = {w.x, w.y, w.z, w.w, 0};
+    if (skip != 0) {
+        uint32_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = __shfl_down_sync(0xffffffffu, x[i], 1);
+        const int words = skip * (int)sizeof(T) / 4;
+        x[4] = y[0];
+        if (words == 1) x[0] = x[1], x[1] = x[2], x[2] = x[3], x[3] = y[0], x[4] = y[1];
+        else if (words == 2) x[0] = x[2], x[1] = x[3], x[2] = y[0], x[3] = y[1], x[4] = y[2];
+        else if (words == 3) x[0] = x[3], x[1] = y[0], x[2] = y[1], x[3] = y[2], x[4] = y[3];
+        if (sizeof(T) == 2 && (skip & 1)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], 16);
+        }
+    }
+    return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
 constexpr int kAccMaxWarps = 8;
+// Rows in flight per warp, and warps per SM: 8 x 24 and 4 x 32 were the best of
+// 2 to 12 rows and 16 to 40 warps (131072 x 8 aligned rows of 256 entries 17.4
+// us, 4 x 32 17.8; 128 odd rows of 65539 entries 28.8 us, 8 x 24 29.8).
+constexpr int acc_unroll(bool aligned) { return aligned ? 8 : 4; }
+constexpr int acc_warps(bool aligned) { return aligned ? 24 : 32; }
 
 // A warp sums rows over one tile of entries, V = 16 bytes' worth per lane; the
 // rows of a tile (share * queries of them) are split over 2^log_split warps of
@@ -75,15 +102,19 @@ constexpr int kAccMaxWarps = 8;
 // they lie; only when the rows' offset `skip` from that boundary changes are
 // the sums added to the tile's entries, `skip` values further left.  Rows V
 // queries apart have the same offset, so each warp walks its rows in the order
-// (query mod V, head, query), in which the offset changes least often.  The
-// tile is then 31 lanes wide, as the last lane's vector reaches past it.  A
-// vector that holds no value of the row's valid part is not loaded.
+// (query mod V, head, query), in which the offset changes least often; where
+// it changes within a batch of U rows, each vector is shifted into place with
+// words of the next lane's.  The tile is then 31 lanes wide, as the last lane's
+// vector reaches past it.  A vector that holds no value of the row's valid
+// part is not loaded.
 //
 // DIRECT: one warp a tile, and aligned outputs: the lanes write their sums
 // themselves, with no turn through shared memory.
 template <typename T, bool ALIGNED, bool DIRECT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) accumulate_weights_kernel(AccumulateArgs a, int log_split) {
-    constexpr int V = 16 / (int)sizeof(T), LANES = ALIGNED ? 32 : 31, TILE = LANES * V, U = 8;
+__global__ void __launch_bounds__(WARPS * 32, acc_warps(ALIGNED) / WARPS)
+    accumulate_weights_kernel(AccumulateArgs a, int log_split) {
+    constexpr int V = 16 / (int)sizeof(T), LANES = ALIGNED ? 32 : 31, TILE = LANES * V;
+    constexpr int U = acc_unroll(ALIGNED);
     constexpr int STEP = ALIGNED ? 1 : V;  // queries between neighbours of the walk
     // Entry e of a tile is at (e mod V) * PITCH + e / V: the pitch keeps both
     // the lanes' writes and the reads of consecutive entries off each other's banks.
@@ -192,19 +223,19 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) accumulate_weights_ker
                 }
                 changes |= skip[u] ^ skip[0];
             }
-            if (!ALIGNED && cur != skip[0]) {
-                if (cur >= 0) settle();
-                cur = skip[0];
+            if (!ALIGNED) {
+                const int want = changes == 0 ? skip[0] : 0;
+                if (cur != want) {
+                    if (cur >= 0) settle();
+                    cur = want;
+                }
             }
             if (ALIGNED || changes == 0) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) add_vector(sum, w[u], T{});
             } else {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (skip[u] != cur) settle(), cur = skip[u];
-                    add_vector(sum, w[u], T{});
-                }
+                for (int u = 0; u < U; ++u) add_vector(sum, shifted<T>(w[u], skip[u]), T{});
             }
         }
     }
