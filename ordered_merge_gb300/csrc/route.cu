@@ -146,6 +146,449 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(RouteArgs 
     }
 }
 
+// ---------------------------------------------------- sorted-list kernel --
+//
+// For top_k <= 8.  L lanes share a token (32 / L tokens a warp).  A lane takes
+// its share of the row eight experts at a time: it sorts the eight by a fixed
+// network and merges them into its sorted list of the best eight (the greater
+// of a[i] and b[7 - i] for every i are the best eight of both, and bitonic, so
+// three more steps sort them).  The lanes' lists are merged the same way across
+// the lanes, log2(L) times, after which each of them has the token's best eight.
+// Nothing but minima and maxima of independent pairs, no turn through memory,
+// and no warp reduction per pick.
+//
+// PACKED: where 16-bit logits are themselves the order, a key is the
+// order-preserving image of the logit above the complement of its index, so the
+// list holds the indices, and ties go to the lower one.
+//
+// Otherwise the list holds what the experts are chosen by, as floats, and the
+// indices are found afterwards: the k-th of the list is the least that was
+// chosen; a lane looks through those of its eights whose greatest (kept in
+// shared memory) reaches it, and an expert's place is the number of listed
+// values above its own.  Equal values among the chosen, or one past the last,
+// leave places open; then the token's picks are settled one after the other.
+//
+// GROUPED: lane l's share is the contiguous part l of the row, which lies in one
+// group of experts; after the lanes' own lists are made, the groups' scores are
+// taken from their heads, and the lists of groups not picked are dropped.
+
+// What bounds it is the rate of minima and maxima (half of the issue rate): a
+// token of 128 bf16 logits takes about 50 warp instructions of them and 80 in
+// all.  Measured, 131071 tokens, top 8: 128 bf16 logits 18 us (2.3 TB/s), 128
+// f32 29 us, 256 f32 sigmoid scores with bias in 8 groups 82 us, where the
+// kernel above takes 87, 87 and 271 us.
+constexpr int kListThreads = 128;
+
+__device__ __forceinline__ uint32_t greater(uint32_t a, uint32_t b) { return max(a, b); }
+__device__ __forceinline__ uint32_t lesser(uint32_t a, uint32_t b) { return min(a, b); }
+__device__ __forceinline__ float greater(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float lesser(float a, float b) { return fminf(a, b); }
+
+template <typename K>
+__device__ __forceinline__ void order_pair(K& hi, K& lo) {
+    const K a = hi, b = lo;
+    hi = greater(a, b);
+    lo = lesser(a, b);
+}
+
+// Greatest first; a bitonic sequence of eight.
+template <typename K>
+__device__ __forceinline__ void sort_bitonic8(K (&k)[8]) {
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((i & d) == 0) order_pair(k[i], k[i + d]);
+}
+
+// Greatest first: odd-even merges of 1, 2 and 4 (19 pairs).
+template <typename K>
+__device__ __forceinline__ void sort8(K (&k)[8]) {
+    order_pair(k[0], k[1]), order_pair(k[2], k[3]), order_pair(k[4], k[5]), order_pair(k[6], k[7]);
+    order_pair(k[0], k[2]), order_pair(k[1], k[3]), order_pair(k[4], k[6]), order_pair(k[5], k[7]);
+    order_pair(k[1], k[2]), order_pair(k[5], k[6]);
+    order_pair(k[0], k[4]), order_pair(k[1], k[5]), order_pair(k[2], k[6]), order_pair(k[3], k[7]);
+    order_pair(k[2], k[4]), order_pair(k[3], k[5]);
+    order_pair(k[1], k[2]), order_pair(k[3], k[4]), order_pair(k[5], k[6]);
+}
+
+template <typename K>
+__device__ __forceinline__ void merge_best8(K (&a)[8], const K (&b)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = greater(a[i], b[7 - i]);
+    sort_bitonic8(a);
+}
+
+// Eight values of a row from e on; those at or past the end are -inf.
+template <typename T>
+struct Eight {
+    uint32_t w[8 * sizeof(T) / 4];
+};
+
+__device__ __forceinline__ uint32_t no_value(float) { return 0xff800000u; }
+__device__ __forceinline__ uint32_t no_value(__nv_bfloat16) { return 0xff80u; }
+__device__ __forceinline__ uint32_t no_value(__half) { return 0xfc00u; }
+
+template <typename T>
+__device__ __forceinline__ Eight<T> load_eight(const T* row, int e, int end, bool aligned) {
+    constexpr int W = 8 * (int)sizeof(T) / 4;
+    Eight<T> x;
+    if (aligned && e + 8 <= end) {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e) + i / 4);
+            x.w[i] = v.x, x.w[i + 1] = v.y, x.w[i + 2] = v.z, x.w[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t bits = no_value(T{});
+            if (e + i < end) {
+                if (sizeof(T) == 4) bits = __ldg(reinterpret_cast<const uint32_t*>(row) + e + i);
+                else bits = __ldg(reinterpret_cast<const unsigned short*>(row) + e + i);
+            }
+            if (sizeof(T) == 4) x.w[i] = bits;
+            else x.w[i / 2] = i & 1 ? x.w[i / 2] | bits << 16 : bits;
+        }
+    }
+    return x;
+}
+
+// Eight values written from e on, those before the end.
+template <typename T>
+__device__ __forceinline__ void store_eight(T* row, int e, int end, bool aligned, const float (&y)[8]) {
+    if (aligned && e + 8 <= end) {
+        __align__(16) T v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = from_float<T>(y[i]);
+#pragma unroll
+        for (int i = 0; i < 8 * (int)sizeof(T) / 16; ++i)
+            reinterpret_cast<uint4*>(row + e)[i] = reinterpret_cast<const uint4*>(v)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e + i < end) row[e + i] = from_float<T>(y[i]);
+    }
+}
+
+__device__ __forceinline__ float value_of(const Eight<float>& x, int i) { return __uint_as_float(x.w[i]); }
+__device__ __forceinline__ float value_of(const Eight<__nv_bfloat16>& x, int i) {
+    return __uint_as_float(i & 1 ? x.w[i / 2] & 0xffff0000u : x.w[i / 2] << 16);
+}
+__device__ __forceinline__ float value_of(const Eight<__half>& x, int i) {
+    return __half2float(__ushort_as_half((unsigned short)(i & 1 ? x.w[i / 2] >> 16 : x.w[i / 2])));
+}
+
+// The logit behind a packed key.
+template <typename T>
+__device__ __forceinline__ float logit_of(uint32_t key, T) {
+    const uint32_t image = key >> 16;
+    Eight<T> one;
+    one.w[0] = (image & 0x8000u ? image ^ 0x8000u : ~image) & 0xffffu;
+    return key == 0 ? -INFINITY : value_of(one, 0);
+}
+
+// All ones in each half of w whose top bit is set.
+__device__ __forceinline__ uint32_t half_signs(uint32_t w) {
+    uint32_t m;
+    asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(m) : "r"(w));
+    return m;
+}
+
+// Two 16-bit values with NaN made -inf and -0 made +0.
+__device__ __forceinline__ uint32_t plain_pair(uint32_t w, __nv_bfloat16) {
+    __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&w);
+    v = __hadd2(__hmax2(v, __halves2bfloat162(__ushort_as_bfloat16(0xff80), __ushort_as_bfloat16(0xff80))),
+                __halves2bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0)));
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t plain_pair(uint32_t w, __half) {
+    __half2 v = *reinterpret_cast<__half2*>(&w);
+    v = __hadd2(__hmax2(v, __halves2half2(__ushort_as_half(0xfc00), __ushort_as_half(0xfc00))),
+                __halves2half2(__ushort_as_half(0), __ushort_as_half(0)));
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t plain_pair(uint32_t, float) { return 0; }  // not used
+
+// e^(x - top) for a sum: one multiplication and the hardware's 2^x, terms below
+// 2^-126 as zero.  What the rounding of the argument costs a term falls with the
+// term itself.  x = -inf gives 0; top must be finite or +inf.
+__device__ __forceinline__ float exp_term(float x, float top) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((x - top) * 1.4426950408889634f));
+    return y;
+}
+
+// What the list is made of.
+enum ListMode {
+    kListPacked,   // 16-bit logits with their indices
+    kListLogit,    // logits
+    kListSoftmax,  // softmax scores, with a bias or summed over groups
+    kListSigmoid   // sigmoid scores, likewise
+};
+
+template <typename T, int MODE, bool GROUPED, int L>
+__global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, bool aligned) {
+    constexpr bool PACKED = MODE == kListPacked, BY_LOGIT = MODE <= kListLogit;
+    using Key = typename std::conditional<PACKED, uint32_t, float>::type;
+    constexpr unsigned kAll = 0xffffffffu;
+    const float kNone = -INFINITY;
+    extern __shared__ float4 s_choice[];       // [steps][2][kListThreads]: a lane's eights, [steps] their greatest
+    __shared__ int s_id[kListThreads / L][8];  // the picks of a token
+    const int l = threadIdx.x & (L - 1), slot = threadIdx.x / L;
+    const int64_t t = (int64_t)blockIdx.x * (kListThreads / L) + slot;
+    const bool live = t < a.tokens;
+    const T* row = static_cast<const T*>(a.logits) + (live ? t : a.tokens - 1) * a.row_stride;
+    const int steps = (a.experts + 8 * L - 1) / (8 * L);
+    const int share = a.experts / L, end = GROUPED ? (l + 1) * share : a.experts;
+    auto first_of = [&](int step) { return GROUPED ? l * share + step * 8 : (step * L + l) * 8; };
+    float* s_greatest = reinterpret_cast<float*>(s_choice + 2 * steps * kListThreads);
+
+    // softmax over the row, where it is needed
+    float top = kNone, sum = 1.0f;
+    auto top_of_row = [&] {
+        for (int step = 0; step < steps; ++step) {
+            const Eight<T> x = load_eight(row, first_of(step), end, aligned);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, value_of(x, i));
+        }
+#pragma unroll
+        for (int d = 1; d < L; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+    };
+    auto sum_of_row = [&] {
+        float part = 0.0f;
+        for (int step = 0; step < steps; ++step) {
+            const Eight<T> x = load_eight(row, first_of(step), end, aligned);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) part += exp_term(fmaxf(value_of(x, i), kNone), top > kNone ? top : 0.0f);
+        }
+#pragma unroll
+        for (int d = 1; d < L; d <<= 1) part += __shfl_xor_sync(kAll, part, d);
+        sum = part;
+    };
+    float inverse = 1.0f;
+    if (MODE == kListSoftmax) {
+        top_of_row();
+        sum_of_row();
+        inverse = 1.0f / sum;
+    }
+
+    Key best[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) best[i] = PACKED ? Key(0) : Key(kNone);
+    // one step's load is on its way while the one before is sorted
+    Eight<T> x = load_eight(row, first_of(0), end, aligned);
+#pragma unroll 1
+    for (int step = 0; step < steps; ++step) {
+        const int e = first_of(step);
+        Eight<T> next = x;
+        if (step + 1 < steps) next = load_eight(row, first_of(step + 1), end, aligned);
+        Key k[8];
+        if constexpr (PACKED) {
+            uint32_t index = (uint32_t)(0xffff - e) | (uint32_t)(0xffff - e - 1) << 16;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w = plain_pair(x.w[i], T{});
+                // negative values are complemented, others get the top bit
+                const uint32_t image = w ^ (half_signs(w) | 0x80008000u);
+                k[2 * i] = __byte_perm(index, image, 0x5410);
+                k[2 * i + 1] = __byte_perm(index, image, 0x7632);
+                index -= 0x00020002u;
+            }
+        } else {
+            // what the experts are chosen by; -inf where masked, and no -0
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float v = value_of(x, i);
+                // the hardware's 2^x: its error, below 2^-22 of the score, is that of ordering in 32 bits
+                if (MODE == kListSoftmax) k[i] = __expf(v - top) * inverse;
+                else if (MODE == kListSigmoid) k[i] = __fdividef(1.0f, 1.0f + __expf(-v));
+                else k[i] = v;
+            }
+            if (!BY_LOGIT && a.bias != nullptr) {
+                const Eight<float> bias = load_eight(a.bias, e, end, ((uintptr_t)(a.bias + e) & 15) == 0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) k[i] += value_of(bias, i);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                k[i] = fmaxf(k[i], kNone) + 0.0f;
+                if (!BY_LOGIT && !(value_of(x, i) > kNone)) k[i] = kNone;
+            }
+            s_choice[2 * step * kListThreads + threadIdx.x] = make_float4(k[0], k[1], k[2], k[3]);
+            s_choice[(2 * step + 1) * kListThreads + threadIdx.x] = make_float4(k[4], k[5], k[6], k[7]);
+        }
+        sort8(k);
+        if constexpr (!PACKED) s_greatest[step * kListThreads + threadIdx.x] = k[0];
+        merge_best8(best, k);
+        x = next;
+    }
+    bool open = true;  // this lane's share may be chosen from
+    if constexpr (GROUPED) {
+        // L / groups neighbouring lanes hold a group
+        const int wide = L / a.groups;
+        float b0, b1;
+        if constexpr (PACKED) b0 = logit_of(best[0], T{}), b1 = logit_of(best[1], T{});
+        else b0 = best[0], b1 = best[1];
+        for (int d = 1; d < wide; d <<= 1) {
+            const float o0 = __shfl_xor_sync(kAll, b0, d), o1 = __shfl_xor_sync(kAll, b1, d);
+            b1 = fmaxf(fminf(b0, o0), fmaxf(b1, o1));
+            b0 = fmaxf(b0, o0);
+        }
+        const int group = l / wide;
+        const float score = a.group_best == 2 && b1 > kNone ? b0 + b1 : b0;
+        int ahead = b0 > kNone ? 0 : a.groups;  // groups that go first; an empty one is never picked
+        for (int g = 0; g < a.groups; ++g) {
+            const float other = __shfl_sync(kAll, score, (threadIdx.x & 31 & ~(L - 1)) + g * wide);
+            ahead += other > score || (other == score && g < group);
+        }
+        open = ahead < a.group_picks;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!open) best[i] = PACKED ? Key(0) : Key(kNone);
+    }
+#pragma unroll 1
+    for (int d = 1; d < L; d <<= 1) {
+        Key other[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(kAll, best[i], d);
+        merge_best8(best, other);
+    }
+
+    if constexpr (!PACKED) {
+        // the indices behind the list
+        int valid = 0, twins = 0;  // listed values that are there; neighbours that are equal
+        float least = -3.402823466e38f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i < a.top_k && best[i] > kNone) ++valid, least = best[i];
+            if (i > 0 && i < a.top_k && best[i] > kNone) twins += best[i] == best[i - 1];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i += L)
+            if (l + i < 8) s_id[slot][l + i] = -1;
+        __syncwarp();
+        uint32_t eights = 0;  // of this lane, that reach the least chosen value
+        for (int step = 0; step < steps; ++step)
+            if (open && s_greatest[step * kListThreads + threadIdx.x] >= least) eights |= 1u << step;
+        int found = 0;
+        for (uint32_t left = eights; left != 0; left &= left - 1) {
+            const int step = __ffs(left) - 1;
+            const float4* two = s_choice + 2 * step * kListThreads + threadIdx.x;
+            const float4 lo = two[0], hi = two[kListThreads];
+            const float c[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            uint32_t chosen = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) chosen |= c[i] >= least ? 1u << i : 0u;
+            found += __popc(chosen);
+            for (; chosen != 0; chosen &= chosen - 1) {
+                const int i = __ffs(chosen) - 1;
+                const float mine = reinterpret_cast<const float*>(two + (i >> 2) * kListThreads)[i & 3];
+                int place = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) place += best[j] > mine;
+                s_id[slot][place & 7] = first_of(step) + i;
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int d = 1; d < L; d <<= 1) found += __shfl_xor_sync(kAll, found, d);
+        const bool unsettled = twins > 0 || found > valid;
+        if (__any_sync(kAll, unsettled)) {
+            // place by place: the lowest index of the place's value, above the one before if that had the same
+            int before = -1;
+            float last = INFINITY;
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+                float v = kNone;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i == j) v = best[i];
+                if (v != last) before = -1;
+                int lowest = 0x7fffffff;
+                if (unsettled && j < valid) {
+                    for (uint32_t left = eights; left != 0; left &= left - 1) {
+                        const int step = __ffs(left) - 1, e = first_of(step);
+                        const float4* two = s_choice + 2 * step * kListThreads + threadIdx.x;
+                        const float4 lo = two[0], hi = two[kListThreads];
+                        const float c[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (e + i > before && c[i] == v) lowest = min(lowest, e + i);
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int d = 1; d < L; d <<= 1) lowest = min(lowest, __shfl_xor_sync(kAll, lowest, d));
+                if (unsettled && j < valid && l == 0) s_id[slot][j] = lowest;
+                before = lowest;
+                last = v;
+            }
+            __syncwarp();
+        }
+    }
+
+    // lane l finishes the picks l * P ..
+    constexpr int P = L < 8 ? 8 / L : 1;
+    int id[P];
+    float px[P], w[P];
+    float head = kNone;  // the picks' greatest logit
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        bool there = l * P + p < a.top_k;
+        if constexpr (PACKED) {
+            Key k = 0;
+#pragma unroll
+            for (int i = 0; i < 8 / P; ++i)
+                if (l == i) k = best[i * P + p];
+            px[p] = logit_of(k, T{});
+            there = there && px[p] > kNone;
+            id[p] = there ? (int)(0xffffu - (k & 0xffffu)) : -1;
+        } else {
+            id[p] = there ? s_id[slot][l * P + p] : -1;
+            there = id[p] >= 0;
+            px[p] = there ? to_float(row[id[p]]) : kNone;
+        }
+        if (!there) px[p] = kNone;
+        head = fmaxf(head, px[p]);
+        w[p] = 0.0f;
+    }
+#pragma unroll
+    for (int d = 1; d < L; d <<= 1) head = fmaxf(head, __shfl_xor_sync(kAll, head, d));
+    if (a.renorm) {
+        float total = 0.0f;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            if (id[p] >= 0)
+                w[p] = a.score == OM_SCORE_SOFTMAX ? expf(px[p] - head) : shifted_sigmoid(px[p], fminf(head, 0.0f));
+            total += w[p];
+        }
+#pragma unroll
+        for (int d = 1; d < L; d <<= 1) total += __shfl_xor_sync(kAll, total, d);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            if (id[p] >= 0) w[p] = w[p] / total;
+    } else {
+        if (a.score == OM_SCORE_SOFTMAX && BY_LOGIT) {
+            top = head;  // without groups the first pick is the row's greatest logit
+            if (GROUPED) top_of_row();
+            sum_of_row();
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            if (id[p] >= 0) w[p] = a.score == OM_SCORE_SOFTMAX ? expf(px[p] - top) / sum : sigmoid(px[p]);
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        if (live && l * P + p < a.top_k) {
+            a.ids[t * a.top_k + l * P + p] = id[p];
+            a.weights[t * a.top_k + l * P + p] = w[p] * a.scale;
+        }
+    }
+}
+
+constexpr int kBackHeld = 4;  // steps of eight logits that a lane keeps
+
 struct RouteBackArgs {
     const void* logits;
     int64_t tokens;
@@ -157,81 +600,111 @@ struct RouteBackArgs {
     float scale;
 };
 
-// One warp per token; lane l holds the experts l, l + 32, ... and, for
-// l < top_k, the l-th pick.
-template <typename T, int R>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_topk_backward_kernel(RouteBackArgs a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const T* logits = static_cast<const T*>(a.logits);
-    T* grad = static_cast<T*>(a.grad_logits);
-    const bool dense = a.score == OM_SCORE_SOFTMAX && !a.renorm;  // every logit moves the weights
+// L lanes per token, at least as many as it has picks: lane l has the l-th.
+// Only a softmax that is not renormalised (DENSE) reads the whole row, once,
+// and keeps the terms of its sum in registers until they are written, times
+// -dot / sum.  Elsewhere the row's zeros are written while the picks' logits
+// arrive.  Rows go out in 16-byte vectors where they are aligned, and the picks
+// over them, each by its own lane.
+//
+// Bound by memory for large batches: what a row takes besides its bytes is
+// about 9 instructions per logit of DENSE, and the picked logits cost a sector
+// each.  Measured: 65536 tokens of 160 bf16, softmax, LISTED_US us
+// (45 MB); 4099 tokens of 256 f32, renormalised sigmoid, 4.4 us (4.6 MB), of
+// which 2.2 are those of a single token.
+template <typename T, bool DENSE, int L>
+__global__ void __launch_bounds__(128) route_topk_backward_kernel(RouteBackArgs a, bool aligned_in, bool aligned_out) {
+    constexpr unsigned kAll = 0xffffffffu;
     const float kNone = -INFINITY;
+    const int l = threadIdx.x & (L - 1);
+    const int64_t t = ((int64_t)blockIdx.x * 128 + threadIdx.x) / L;
+    const bool live = t < a.tokens;
+    const int64_t at = live ? t : a.tokens - 1;
+    const T* row = static_cast<const T*>(a.logits) + at * a.row_stride;
+    T* grad = static_cast<T*>(a.grad_logits) + at * a.experts;
+    const int steps = (a.experts + 8 * L - 1) / (8 * L);
+    auto reduce_max = [&](float x) {
+#pragma unroll
+        for (int d = 1; d < L; d <<= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, d));
+        return x;
+    };
+    auto reduce_sum = [&](float x) {
+#pragma unroll
+        for (int d = 1; d < L; d <<= 1) x += __shfl_xor_sync(kAll, x, d);
+        return x;
+    };
+    // this lane's pick and its part of the row: all on their way at once
+    int id = -1;
+    float g = 0.0f;
+    if (l < a.top_k) {
+        id = __ldg(a.ids + at * a.top_k + l);
+        g = __ldg(a.grad_weights + at * a.top_k + l) * a.scale;
+    }
+    constexpr int H = DENSE ? kBackHeld : 1;
+    Eight<T> x[H];
+    if (DENSE) {
+#pragma unroll
+        for (int step = 0; step < H; ++step)
+            if (step < steps) x[step] = load_eight(row, (step * L + l) * 8, a.experts, aligned_in);
+    } else if (live) {
+        const float zero[8] = {};
+        for (int step = 0; step < steps; ++step) store_eight(grad, (step * L + l) * 8, a.experts, aligned_out, zero);
+    }
+    float px = kNone;
+    if (id >= 0 && id < a.experts) px = to_float(row[id]);
+    const bool there = px > kNone;  // a masked one was no pick of the forward call
+    if (!there) g = 0.0f;
 
-    for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.tokens; t += (int64_t)gridDim.x * kRouteWarps) {
-        const T* row = logits + t * a.row_stride;
-        int id = -1;
-        float g = 0.0f, px = kNone;
-        if (lane < a.top_k) {
-            id = a.ids[t * a.top_k + lane];
-            if (id < 0 || id >= a.experts) id = -1;
-            if (id >= 0) {
-                g = a.grad_weights[t * a.top_k + lane] * a.scale;
-                px = to_float(row[id]);
-                if (!(px > kNone)) id = -1;  // masked: no pick of the forward call
+    float top = kNone, inverse = 1.0f;
+    float y[H][8];
+    if (DENSE) {
+#pragma unroll
+        for (int step = 0; step < H; ++step)
+            if (step < steps) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    y[step][i] = fmaxf(value_of(x[step], i), kNone);  // NaN to -inf
+                    top = fmaxf(top, y[step][i]);
+                }
             }
-        }
-        float s[R];
-        float top = 0.0f, sum = 1.0f;
-        if (dense) {
-            top = kNone;
+        top = reduce_max(top);
+        if (!(top > kNone)) top = 0.0f;  // nothing is there
+        float part = 0.0f;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int e = r * 32 + lane;
-                s[r] = e < a.experts ? to_float(row[e]) : kNone;
-                top = fmaxf(top, s[r]);
+        for (int step = 0; step < H; ++step)
+            if (step < steps) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) part += y[step][i] = exp_term(y[step][i], top);
             }
-            top = warp_max(top);
-            float part = 0.0f;
+        part = reduce_sum(part);
+        inverse = part == 0.0f ? 0.0f : 1.0f / part;
+    }
+    // w: the pick's weight before scale
+    float w = 0.0f, dot = 0.0f;
+    if (a.renorm) {
+        const float best = reduce_max(px);
+        if (there) w = a.score == OM_SCORE_SOFTMAX ? expf(px - best) : shifted_sigmoid(px, fminf(best, 0.0f));
+        const float total = reduce_sum(w);
+        if (there) w = w / total;
+    } else if (there) {
+        w = DENSE ? expf(px - top) * inverse : sigmoid(px);
+    }
+    if (DENSE || a.renorm) dot = reduce_sum(g * w);
+    if (DENSE) {
+        const float every = -dot * inverse;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                s[r] = s[r] > kNone ? expf(s[r] - top) : 0.0f;
-                part += s[r];
+        for (int step = 0; step < H; ++step)
+            if (step < steps) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[step][i] *= every;
+                if (live) store_eight(grad, (step * L + l) * 8, a.experts, aligned_out, y[step]);
             }
-            sum = warp_sum(part);
-        }
-        // w: the pick's weight before scale; v: its logit's gradient, less what `dense` subtracts everywhere
-        float w = 0.0f, v = 0.0f, dot = 0.0f;
-        if (a.renorm) {
-            const float best = warp_max(px);
-            const float low = fminf(best, 0.0f);
-            if (id >= 0) w = a.score == OM_SCORE_SOFTMAX ? expf(px - best) : shifted_sigmoid(px, low);
-            const float total = warp_sum(w);
-            if (id >= 0) w = w / total;
-            dot = warp_sum(id >= 0 ? g * w : 0.0f);
-            if (id >= 0) v = w * (g - dot);
-            if (id >= 0 && a.score == OM_SCORE_SIGMOID) v *= sigmoid(-px);
-        } else if (dense) {
-            if (id >= 0) w = expf(px - top) / sum;
-            dot = warp_sum(id >= 0 ? g * w : 0.0f);
-            v = w * (g - dot);
-        } else if (id >= 0) {
-            v = g * sigmoid(px) * sigmoid(-px);
-        }
-        float out[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) out[r] = dense && s[r] != 0.0f ? -(s[r] / sum) * dot : 0.0f;
-        for (int j = 0; j < a.top_k; ++j) {
-            const int pid = __shfl_sync(0xffffffffu, id, j);
-            const float pv = __shfl_sync(0xffffffffu, v, j);
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (pid == r * 32 + lane) out[r] = pv;
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int e = r * 32 + lane;
-            if (e < a.experts) grad[t * a.experts + e] = from_float<T>(out[r]);
-        }
+    }
+    __syncwarp();  // the picks are written over what another lane may have written
+    if (live && there) {
+        float v = w * (g - dot);  // dot is 0 for a plain sigmoid
+        if (a.score == OM_SCORE_SIGMOID) v *= sigmoid(-px);
+        grad[id] = from_float<T>(v);
     }
 }
 
@@ -244,6 +717,66 @@ static cudaError_t with_lane_experts(int experts, F&& f) {
     if (experts <= 256) return f(std::integral_constant<int, 8>{});
     if (experts <= 512) return f(std::integral_constant<int, 16>{});
     return f(std::integral_constant<int, 32>{});
+}
+
+template <typename T, int MODE, bool GROUPED, int L>
+static cudaError_t launch_list_lanes(const RouteArgs& a, bool aligned, cudaStream_t st) {
+    const int64_t blocks = (a.tokens + kListThreads / L - 1) / (kListThreads / L);
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    const int steps = (a.experts + 8 * L - 1) / (8 * L);
+    const size_t smem = MODE == kListPacked ? 0 : (size_t)steps * kListThreads * 9 * sizeof(float);
+    return traced(kKindRoute, st, [&] {
+        route_list_kernel<T, MODE, GROUPED, L><<<(unsigned)blocks, kListThreads, smem, st>>>(a, aligned);
+    });
+}
+
+// A token gets 32 lanes (PACKED: 16) while that gives an SM at most this many
+// threads (2432 tokens): the shorter chain wins until the SMs are busy.  2048
+// biased sigmoid tokens in 8 groups of 32 experts: 5.8 us against 6.3 with
+// 8 lanes each; 4096: 8.0 against 7.5; 131071: 140 against 82.
+constexpr int kListFewThreads = 512;
+// The most experts that 4 (grouped: twice as many for 8) lanes take, whose
+// choices then fill 36 KB of shared memory; not for PACKED, which keeps none.
+constexpr int kListMaxExperts = 256;
+
+template <typename T, int MODE>
+static cudaError_t launch_list_mode(const RouteArgs& a, bool aligned, bool few, cudaStream_t st) {
+    constexpr int kMore = MODE == kListPacked ? 16 : 32;
+    if (a.groups == 1)
+        return few ? launch_list_lanes<T, MODE, false, kMore>(a, aligned, st)
+                   : launch_list_lanes<T, MODE, false, 4>(a, aligned, st);
+    return few ? launch_list_lanes<T, MODE, true, 32>(a, aligned, st)
+               : launch_list_lanes<T, MODE, true, 8>(a, aligned, st);
+}
+
+template <typename T>
+static cudaError_t launch_list(const RouteArgs& a, bool aligned, bool few, cudaStream_t st) {
+    const bool by_logit = a.bias == nullptr && (a.groups == 1 || a.group_best == 1);
+    if constexpr (sizeof(T) == 2) {
+        if (by_logit) return launch_list_mode<T, kListPacked>(a, aligned, few, st);
+    } else {
+        if (by_logit) return launch_list_mode<T, kListLogit>(a, aligned, few, st);
+    }
+    if (a.score == OM_SCORE_SOFTMAX) return launch_list_mode<T, kListSoftmax>(a, aligned, few, st);
+    return launch_list_mode<T, kListSigmoid>(a, aligned, few, st);
+}
+
+template <typename T, bool DENSE, int L>
+static void launch_back_lanes(const RouteBackArgs& a, bool in, bool out, cudaStream_t st) {
+    const unsigned blocks = (unsigned)((a.tokens * L + 127) / 128);
+    route_topk_backward_kernel<T, DENSE, L><<<blocks, 128, 0, st>>>(a, in, out);
+}
+
+// 8 lanes a token, or 32: where there are more picks than 8, and in DENSE where
+// the row fits the registers of 32 lanes only (65536 tokens of 257 f32: 50 us,
+// 8 lanes 62) or the tokens are few (`few`; 512 of 160 bf16: 3.1 us against
+// 3.5, 65536: 31 against 17.5).
+template <typename T, bool DENSE>
+static void launch_back(const RouteBackArgs& a, bool in, bool out, bool few, cudaStream_t st) {
+    constexpr int kHeld8 = 8 * 8 * kBackHeld, kHeld32 = 8 * 32 * kBackHeld;
+    static_assert(kHeld32 >= kMaxExperts, "32 lanes hold every row");
+    if (a.top_k > 8 || (DENSE && (few || a.experts > kHeld8))) launch_back_lanes<T, DENSE, 32>(a, in, out, st);
+    else launch_back_lanes<T, DENSE, 8>(a, in, out, st);
 }
 
 static unsigned route_grid(int64_t tokens) {
@@ -259,7 +792,7 @@ static om_status route_check(int value_type, const void* logits, int64_t tokens,
     if (tokens < 0 || experts < 1 || top_k < 1 || top_k > experts) return OM_EINVAL;
     if (experts > kMaxExperts || top_k > kMaxTopK) return OM_ERANGE;
     if (tokens > 1 && row_stride < 0) return OM_EINVAL;
-    if (tokens > ((int64_t)1 << 40) || row_stride > ((int64_t)1 << 40)) return OM_ERANGE;
+    if (tokens > ((int64_t)1 << 34) || row_stride > ((int64_t)1 << 40)) return OM_ERANGE;
     if (tokens > 0 && (logits == nullptr || misaligned(logits, vb))) return OM_EINVAL;
     return OM_OK;
 }
@@ -290,6 +823,22 @@ om_status om_route_topk(int value_type, const void* logits, int64_t tokens, int6
     RouteArgs a{logits, tokens, row_stride, bias, ids, weights, (int)experts, score, groups, group_picks, group_best,
                 top_k, renorm != 0, scale};
     cudaStream_t st = (cudaStream_t)stream;
+    DeviceState* d = nullptr;
+    const om_status ds = device_state(&d);
+    if (ds != OM_OK) return ds;
+    const bool packed = vb == 2 && bias == nullptr && (groups == 1 || group_best == 1);
+    const bool few = tokens * 32 <= d->sm_count * (int64_t)kListFewThreads ||
+                     (!packed && experts > kListMaxExperts * (groups == 1 ? 1 : 2));
+    const int lanes = few ? 32 : 8;
+    // grouped: a lane's share of a row lies in one group
+    if (top_k <= 8 && (groups == 1 || (lanes % groups == 0 && experts % lanes == 0))) {
+        bool aligned = !misaligned(logits, 16) && (tokens == 1 || row_stride * vb % 16 == 0);
+        if (groups > 1) aligned = aligned && experts / lanes * vb % 16 == 0;
+        const cudaError_t e = with_value_type(value_type, [&](auto v) {
+            return launch_list<decltype(v)>(a, aligned, few, st);
+        });
+        return e == cudaSuccess ? OM_OK : cuda_fail(e);
+    }
     const cudaError_t e = with_value_type(value_type, [&](auto v) {
         return with_lane_experts((int)experts, [&](auto r) {
             return traced(kKindRoute, st, [&] {
@@ -317,12 +866,19 @@ om_status om_route_topk_backward(int value_type, const void* logits, int64_t tok
     RouteBackArgs a{logits, tokens, row_stride, ids, grad_weights, grad_logits, (int)experts, score, top_k,
                     renorm != 0, scale};
     cudaStream_t st = (cudaStream_t)stream;
+    const bool aligned_in = !misaligned(logits, 16) && (tokens == 1 || row_stride * vb % 16 == 0);
+    const bool aligned_out = !misaligned(grad_logits, 16) && (tokens == 1 || experts * vb % 16 == 0);
+    const bool dense = score == OM_SCORE_SOFTMAX && !renorm;
+    DeviceState* d = nullptr;
+    const om_status ds = device_state(&d);
+    if (ds != OM_OK) return ds;
+    const bool few = tokens * 32 <= d->sm_count * (int64_t)kListFewThreads;
+    if (tokens * 8 > (int64_t)INT32_MAX * 128) return OM_ERANGE;
     const cudaError_t e = with_value_type(value_type, [&](auto v) {
-        return with_lane_experts((int)experts, [&](auto r) {
-            return traced(kKindRoute, st, [&] {
-                route_topk_backward_kernel<decltype(v), decltype(r)::value>
-                    <<<route_grid(tokens), kRouteWarps * 32, 0, st>>>(a);
-            });
+        using T = decltype(v);
+        return traced(kKindRoute, st, [&] {
+            if (dense) launch_back<T, true>(a, aligned_in, aligned_out, few, st);
+            else launch_back<T, false>(a, aligned_in, aligned_out, few, st);
         });
     });
     return e == cudaSuccess ? OM_OK : cuda_fail(e);

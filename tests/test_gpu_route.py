@@ -70,6 +70,8 @@ SHAPES = [  # tokens, experts, k, groups, picks, best
     (1, 1, 1, 1, 1, 1), (1, 64, 6, 1, 1, 1), (3, 7, 7, 1, 1, 1), (5, 33, 4, 1, 1, 1), (70, 32, 2, 4, 2, 1),
     (9, 160, 8, 8, 3, 2), (33, 256, 8, 8, 4, 2), (4, 257, 5, 1, 1, 1), (6, 96, 32, 32, 16, 2), (3, 1024, 32, 16, 4, 2),
     (2, 513, 1, 1, 1, 1), (300, 48, 5, 3, 2, 2), (2, 12, 3, 12, 3, 2),
+    (17, 128, 4, 2, 1, 1), (9, 192, 6, 4, 2, 2), (5, 1024, 8, 8, 2, 1), (40, 64, 3, 8, 5, 2), (6, 320, 7, 1, 1, 1),
+    (11, 1000, 8, 1, 1, 1),
 ]
 
 
