@@ -312,7 +312,7 @@ om_status om_merge_sort_keys(int key_type, int order, void *keys,
  * What a language model orders: the experts of a token by their scores, the
  * tokens by their experts, the entries of a cache by the attention they have
  * drawn.  As in the merges, ties go to the earlier (lower) index.  All calls
- * are asynchronous on `stream`; all but om_group_by_id allocate nothing.
+ * are asynchronous on `stream` and allocate nothing.
  * These calls do not need sorted input.
  */
 
@@ -383,9 +383,8 @@ om_status om_route_topk_backward(int value_type, const void *logits,
  * offsets[g] (groups + 1 values) is where id g starts in it, offsets[groups]
  * where the ids outside do; place is the inverse, order[place[i]] = i.
  * What om_merge_sort_u32 on (id, slot) pairs gives, for few distinct ids, in
- * a constant number of passes, with the offsets.  n <= 2^31 - 1 and
- * groups <= 1024, else OM_ERANGE.  Larger calls take stream-ordered scratch
- * from the library's pool (4 bytes per group and CTA).
+ * one launch (a cooperative one when it takes several CTAs), with the offsets.
+ * n <= 2^31 - 1 and groups <= 1024, else OM_ERANGE.
  */
 om_status om_group_by_id(const int32_t *ids, int64_t n, int64_t groups,
                          int32_t *offsets, int32_t *order, int32_t *place,

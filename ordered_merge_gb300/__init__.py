@@ -104,7 +104,7 @@ def _load():
     lib.om_accumulate_weights.restype = I32
     lib.om_evict_select.argtypes = [P, I64, I64, I64, I64, I64, P, I64, I64, I64, P, P, P]
     lib.om_evict_select.restype = I32
-    lib.om_evict_gather.argtypes = [P, I64, I64, I64, I64, ctypes.POINTER(CacheArray), I32, P]
+    lib.om_evict_gather.argtypes = [P, I64, I64, I64, I64, P, I32, P]
     lib.om_evict_gather.restype = I32
     return lib
 

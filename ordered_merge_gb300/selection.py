@@ -9,12 +9,20 @@ in; those not passed are allocated.
 """
 from __future__ import annotations
 
+import functools
+import struct
+
 import torch
 
-from . import CacheArray, _check, _lib, _stream
+from . import _check, _lib, _stream
 
 VALUE_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+# The current stream's handle without building a Stream object, where this
+# torch has the call (3 us less a call on the measured host).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _ptr(t):
@@ -31,22 +39,27 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _placed(**tensors):
-    """Every tensor is on the current device (the one the library launches on)."""
-    device = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if device is None:
-            device = torch.cuda.current_device()
-        if t.get_device() != device:
-            raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{device}")
+def _launch_stream(stream, names, *tensors):
+    """The handle of `stream`, or of the current one, on the current device,
+    where every tensor (None: not given) has to be."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{_named(names, tensors, t)} must be a CUDA tensor")
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{_named(names, tensors, t)} is on {t.device}, but the current device is cuda:{device}")
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream(stream)
+
+
+def _named(names, tensors, t):
+    return names.split()[next(i for i, x in enumerate(tensors) if x is t)]
 
 
 def _dense(t, name: str, shape, dtype):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
                          f"(got {t.dtype}, {tuple(t.shape)})")
 
@@ -97,11 +110,11 @@ def om_route_topk(logits, top_k: int, score: str = "softmax", bias=None, groups:
         weights = _empty((tokens, top_k), torch.float32, logits.device, stream)
     _dense(ids, "ids", (tokens, top_k), torch.int32)
     _dense(weights, "weights", (tokens, top_k), torch.float32)
-    _placed(logits=logits, bias=bias, ids=ids, weights=weights)
+    handle = _launch_stream(stream, "logits bias ids weights", logits, bias, ids, weights)
     _check(
         _lib.om_route_topk(_value_type(logits, "logits"), _ptr(logits), tokens, experts, row_stride,
                            None if bias is None else bias.data_ptr(), _score_code(score), groups, group_picks,
-                           group_best, top_k, 1 if renorm else 0, scale, _ptr(ids), _ptr(weights), _stream(stream)),
+                           group_best, top_k, 1 if renorm else 0, scale, _ptr(ids), _ptr(weights), handle),
         "om_route_topk",
     )
     return ids, weights
@@ -121,11 +134,11 @@ def om_route_topk_backward(logits, ids, grad_weights, score: str = "softmax", re
     if grad_logits is None:
         grad_logits = _empty((tokens, experts), logits.dtype, logits.device, stream)
     _dense(grad_logits, "grad_logits", (tokens, experts), logits.dtype)
-    _placed(logits=logits, ids=ids, grad_weights=grad_weights, grad_logits=grad_logits)
+    handle = _launch_stream(stream, "logits ids grad_weights grad_logits", logits, ids, grad_weights, grad_logits)
     _check(
         _lib.om_route_topk_backward(_value_type(logits, "logits"), _ptr(logits), tokens, experts, row_stride,
                                     _ptr(ids), _ptr(grad_weights), _score_code(score), top_k, 1 if renorm else 0,
-                                    scale, _ptr(grad_logits), _stream(stream)),
+                                    scale, _ptr(grad_logits), handle),
         "om_route_topk_backward",
     )
     return grad_logits
@@ -148,8 +161,8 @@ def om_group_by_id(ids, groups: int, offsets=None, order=None, place=None, strea
     _dense(offsets, "offsets", (groups + 1,), torch.int32)
     _dense(order, "order", (n,), torch.int32)
     _dense(place, "place", (n,), torch.int32)
-    _placed(ids=ids, offsets=offsets, order=order, place=place)
-    _check(_lib.om_group_by_id(_ptr(ids), n, groups, _ptr(offsets), _ptr(order), _ptr(place), _stream(stream)),
+    handle = _launch_stream(stream, "ids offsets order place", ids, offsets, order, place)
+    _check(_lib.om_group_by_id(_ptr(ids), n, groups, _ptr(offsets), _ptr(order), _ptr(place), handle),
            "om_group_by_id")
     return offsets, order, place
 
@@ -176,11 +189,11 @@ def om_accumulate_weights(weights, score=None, lengths=None, decay: float = 1.0,
     if out.dtype != torch.float32 or tuple(out.shape) != (batch, kv_heads, length):
         raise ValueError(f"out must be float32 of shape {(batch, kv_heads, length)}")
     length_ptr = _lengths(lengths, batch)
-    _placed(weights=weights, score=score, lengths=lengths, out=out)
+    handle = _launch_stream(stream, "weights score lengths out", weights, score, lengths, out)
     _check(
         _lib.om_accumulate_weights(_value_type(weights, "weights"), _ptr(weights), batch, q_heads, kv_heads, queries,
                                    length, w_batch, w_head, w_query, None if score is None else _ptr(score), s_batch,
-                                   s_head, length_ptr, decay, _ptr(out), o_batch, o_head, _stream(stream)),
+                                   s_head, length_ptr, decay, _ptr(out), o_batch, o_head, handle),
         "om_accumulate_weights",
     )
     return out
@@ -203,25 +216,38 @@ def om_evict_select(score, budget: int, first: int = 0, last: int = 0, lengths=N
     _dense(keep, "keep", (batch, heads, budget), torch.int32)
     _dense(kept, "kept", (batch,), torch.int32)
     length_ptr = _lengths(lengths, batch)
-    _placed(score=score, lengths=lengths, keep=keep, kept=kept)
+    handle = _launch_stream(stream, "score lengths keep kept", score, lengths, keep, kept)
     _check(
         _lib.om_evict_select(_ptr(score), batch, heads, length, s_batch, s_head, length_ptr, budget, first, last,
-                             _ptr(keep), _ptr(kept), _stream(stream)),
+                             _ptr(keep), _ptr(kept), handle),
         "om_evict_select",
     )
     return keep, kept
 
 
-def _cache_entry(t, name: str, batch: int, heads: int) -> int:
-    """Bytes of one entry of a cache array [batch, heads, entries, ...] whose entries are contiguous."""
-    if t.dim() < 3 or t.shape[0] != batch or t.shape[1] != heads:
+def _cache_entry(shape, strides, name: str, batch: int, heads: int) -> int:
+    """Elements of one entry of a cache array [batch, heads, entries, ...] whose entries are contiguous."""
+    if len(shape) < 3 or shape[0] != batch or shape[1] != heads:
         raise ValueError(f"{name} must be [batch, heads, entries, ...] with batch {batch} and heads {heads}")
     inner = 1
-    for size, stride in zip(reversed(t.shape[3:]), reversed(t.stride()[3:])):
-        if size > 1 and stride != inner:
+    for d in range(len(shape) - 1, 2, -1):
+        if shape[d] != 1 and strides[d] != inner:
             raise ValueError(f"the entries of {name} must be contiguous")
-        inner *= size
-    return inner * t.element_size()
+        inner *= shape[d]
+    return inner
+
+
+@functools.lru_cache(maxsize=256)
+def _gather_geometry(keep_shape, size: int, src_shape, src_strides, dst_shape, dst_strides):
+    """Checks one array's shapes and strides (of elements of `size` bytes) and
+    returns what om_cache_array says of them: bytes per entry and the strides
+    in bytes.  Of the shapes alone, so it is kept from call to call."""
+    batch, heads, budget = keep_shape
+    inner = _cache_entry(src_shape, src_strides, "array", batch, heads)
+    want = (*keep_shape, *src_shape[3:])
+    if dst_shape != want or _cache_entry(dst_shape, dst_strides, "out", batch, heads) != inner:
+        raise ValueError(f"out must have shape {want} (got {tuple(dst_shape)})")
+    return (inner * size, *(s * size for s in src_strides[:3]), *(s * size for s in dst_strides[:3]))
 
 
 def om_evict_gather(keep, arrays, out=None, stream=None):
@@ -230,32 +256,28 @@ def om_evict_gather(keep, arrays, out=None, stream=None):
     becomes entry keep[j], zero where keep is -1.  Returns new arrays, or
     `out`, which must not overlap the inputs.  One launch moves all of them."""
     arrays = tuple(arrays)
-    if keep.dim() != 3:
+    shape = keep.shape
+    if len(shape) != 3:
         raise ValueError("keep must have 3 dimensions")
-    batch, heads, budget = keep.shape
-    _dense(keep, "keep", (batch, heads, budget), torch.int32)
-    if not arrays:
-        raise ValueError("no arrays to gather")
-    length = arrays[0].shape[2] if arrays[0].dim() >= 3 else 0
+    _dense(keep, "keep", shape, torch.int32)
+    if not arrays or arrays[0].dim() < 3:
+        raise ValueError("arrays must hold tensors [batch, heads, entries, ...]")
+    length = arrays[0].shape[2]
     if out is None:
-        out = tuple(_empty((batch, heads, budget, *t.shape[3:]), t.dtype, t.device, stream) for t in arrays)
+        out = tuple(_empty((*shape, *t.shape[3:]), t.dtype, t.device, stream) for t in arrays)
     out = tuple(out)
     if len(out) != len(arrays):
         raise ValueError("out must hold one tensor for each array")
-    _placed(keep=keep)
-    table = (CacheArray * len(arrays))()
-    for c, src, dst in zip(table, arrays, out):
-        _placed(array=src, out=dst)
-        size = _cache_entry(src, "array", batch, heads)
+    handle = _launch_stream(stream, "keep" + " array" * len(arrays) + " out" * len(out), keep, *arrays, *out)
+    table = []
+    for src, dst in zip(arrays, out):
+        if dst.dtype != src.dtype:
+            raise ValueError(f"out must be {src.dtype} (got {dst.dtype})")
+        geometry = _gather_geometry(shape, src.element_size(), src.shape, src.stride(), dst.shape, dst.stride())
         if src.shape[2] != length:
             raise ValueError("the arrays must have as many entries each")
-        if dst.dtype != src.dtype or dst.shape[2:3] != (budget,) or dst.shape[3:] != src.shape[3:] \
-                or _cache_entry(dst, "out", batch, heads) != size:
-            raise ValueError(f"out must be {src.dtype} of shape {(batch, heads, budget, *src.shape[3:])}")
-        es = src.element_size()
-        c.src, c.dst, c.entry_bytes = src.data_ptr(), dst.data_ptr(), size
-        c.src_batch, c.src_head, c.src_entry = (s * es for s in src.stride()[:3])
-        c.dst_batch, c.dst_head, c.dst_entry = (s * es for s in dst.stride()[:3])
-    _check(_lib.om_evict_gather(_ptr(keep), batch, heads, budget, length, table, len(arrays), _stream(stream)),
+        table += (src.data_ptr(), dst.data_ptr(), *geometry)
+    # om_cache_array: nine 64-bit words
+    _check(_lib.om_evict_gather(_ptr(keep), *shape, length, struct.pack(f"{len(table)}q", *table), len(arrays), handle),
            "om_evict_gather")
     return out
