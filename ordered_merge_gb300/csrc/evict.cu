@@ -336,30 +336,6 @@ __device__ __forceinline__ uint32_t evict_key(float s) { return score_image(s ==
 // The key of an entry that stays whatever its score; above that of +inf.
 constexpr uint32_t kKeyStays = 0xffffffffu;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-// Every thread of every CTA of the cluster; orders their shared memory.
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A word of CTA `rank`'s shared memory, at the address p has in this CTA's.
-__device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
-    uint32_t at;
-    int v;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    return v;
-}
-
-
 // Finds, among 32 * P counts held P per lane with the greatest place in lane 0's
 // first, the place at which the sum from the top reaches `need`; *over is the
 // sum above it.

@@ -13,6 +13,7 @@ namespace om {
 constexpr int kMaxGroups = 1024;
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupWarps = kGroupThreads / 32;
+constexpr unsigned kGroupCluster8 = 8;  // CTAs of a cluster at most
 
 // Ids outside [0, groups) form one more group after the others.
 __device__ __forceinline__ int group_of(int32_t id, int groups) {
@@ -34,21 +35,42 @@ struct GroupArgs {
     }
 };
 
+// Every thread of the cooperative grid.  A function of its own, because inlined
+// the thread that waits for the other CTAs stayed apart from its warp
+// afterwards, and the warp ran everything twice.
+__device__ __noinline__ void grid_barrier() { cooperative_groups::this_grid().sync(); }
+
+// How the CTAs of a call learn of each other's counts.
+enum GroupWay {
+    kGroupLone,     // one CTA
+    kGroupCluster,  // a cluster of 2 to 8: from each other's shared memory
+    kGroupGrid      // a cooperative grid: through the chunks of `place`
+};
+
 // A slot's place is the sum of: the slots of lower groups, those of its own in
 // the chunks of the CTAs before, in the parts of the warps before, and before
 // it in its own warp's part.  Chunks and parts are contiguous, so equal ids
 // keep their order.
 //
-// One CTA, or a cooperative grid whose CTAs exchange their counts through the
-// start of their own chunk of `place` (2 * (groups + 1) words), which they
-// overwrite only at the end: no scratch memory.  CTA c leaves its counts there;
-// one warp per group turns the column of a group into the sums over the CTAs
-// before, and leaves the group's total beside each; then every CTA needs its
-// own chunk only.  (Every CTA reading every other's counts took 12 us more.)
+// kGroupGrid takes no scratch memory: CTA c leaves its counts at the start of
+// its own chunk of `place` (2 * (groups + 1) words); one warp per group turns
+// the column of a group into the sums over the CTAs before, and leaves the
+// group's total beside each; then every CTA needs its own chunk only, which it
+// overwrites at the end.
+//
+// What bounds it: for few slots the chain of loads and barriers, 4 us of which
+// one CTA needs for its first loads; for many the two grid barriers (1.4 us
+// each) and the ranking, about 130 instructions per 32 slots.  Measured, times
+// of the kernel: 512 slots of 256 groups 5.3 us, 32768 9.3 us, 1.05 M of 128
+// 16.4 us.  Writing `order` from a chunk put in order in shared memory first,
+// in runs, was no faster (16.5 us).
+template <int WAY>
 __global__ void __launch_bounds__(kGroupThreads) group_by_id_kernel(GroupArgs a) {
-    extern __shared__ int s_next[];  // [warps][groups + 1]: counts, then the next place
+    extern __shared__ int s_next[];  // [warps][E]: a warp's counts, then its next place less the CTA's first
     __shared__ int s_part[kGroupWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, E = a.groups + 1;
+    int* s_count = s_next + warps * E;  // [E]: the CTA's counts
+    int* s_first = s_count + E;         // [E]: the CTA's first place of each group
     const unsigned ctas = gridDim.x;
     const int64_t lo = a.start(blockIdx.x), hi = a.start(blockIdx.x + 1);
     // each warp's part of the chunk, in steps of 32 slots
@@ -67,18 +89,27 @@ __global__ void __launch_bounds__(kGroupThreads) group_by_id_kernel(GroupArgs a)
             if (i0 + 32 * u < whi) atomicAdd(&next[group_of(id[u], a.groups)], 1);
     }
     __syncthreads();
-
-    int32_t* mine = a.place + lo;  // this CTA's words of the exchange
-    if (ctas > 1) {
-        for (int g = threadIdx.x; g < E; g += blockDim.x) {
-            int count = 0;
-#pragma unroll 8
-            for (int w = 0; w < warps; ++w) count += s_next[w * E + g];
-            __stcg(mine + g, count);
+    // counts to sums over the warps before
+    for (int g = threadIdx.x; g < E; g += blockDim.x) {
+        int run = 0;
+        for (int w0 = 0; w0 < warps; w0 += 8) {
+            int c[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) c[k] = w0 + k < warps ? s_next[(w0 + k) * E + g] : 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (w0 + k < warps) s_next[(w0 + k) * E + g] = run;
+                run += c[k];
+            }
         }
-        cooperative_groups::this_grid().sync();
+        s_count[g] = run;
+        if (WAY == kGroupGrid) __stcg(a.place + lo + g, run);
+    }
+    if (WAY == kGroupCluster) cluster_sync();
+    if (WAY == kGroupGrid) {
+        grid_barrier();
         for (int g = warp * (int)ctas + (int)blockIdx.x; g < E; g += warps * (int)ctas) {
-            constexpr int R = 4;  // loads of a column in flight per lane
+            constexpr int R = 5;  // 160 CTAs at a time
             int before = 0;
             for (unsigned c0 = 0; c0 < ctas; c0 += 32 * R) {
                 int count[R];
@@ -102,21 +133,27 @@ __global__ void __launch_bounds__(kGroupThreads) group_by_id_kernel(GroupArgs a)
             }
             for (unsigned c = lane; c < ctas; c += 32) __stcg(a.place + a.start(c) + E + g, before);
         }
-        cooperative_groups::this_grid().sync();
+        grid_barrier();
     }
 
-    // where each group starts, then where each warp's slots of it do
+    // where each group starts, and the CTA's slots of it
     int start = 0;
     for (int g0 = 0; g0 < E; g0 += blockDim.x) {
         const int g = g0 + threadIdx.x;
         int total = 0, before = 0;
         if (g < E) {
-            if (ctas > 1) {
-                before = __ldcg(mine + g);
-                total = __ldcg(mine + E + g);
+            if (WAY == kGroupGrid) {
+                before = __ldcg(a.place + lo + g);
+                total = __ldcg(a.place + lo + E + g);
+            } else if (WAY == kGroupCluster) {
+#pragma unroll
+                for (unsigned r = 0; r < kGroupCluster8; ++r) {
+                    const int count = r < ctas ? peer_word(s_count + g, r) : 0;
+                    total += count;
+                    before += r < blockIdx.x ? count : 0;
+                }
             } else {
-#pragma unroll 8
-                for (int w = 0; w < warps; ++w) total += s_next[w * E + g];
+                total = s_count[g];
             }
         }
         int run = total;
@@ -138,43 +175,46 @@ __global__ void __launch_bounds__(kGroupThreads) group_by_id_kernel(GroupArgs a)
         start += __shfl_sync(0xffffffffu, sums, 31);
         if (g < E) {
             if (blockIdx.x == 0) a.offsets[g] = first;  // the last one, of the ids outside, ends the others
-            int at = first + before;
-#pragma unroll 8
-            for (int w = 0; w < warps; ++w) {
-                const int c = s_next[w * E + g];
-                s_next[w * E + g] = at;
-                at += c;
-            }
+            s_first[g] = first + before;
         }
         __syncthreads();
     }
+    if (WAY == kGroupCluster) cluster_sync();  // no CTA leaves, or writes, while another reads its counts
+
     const int bits = 32 - __clz(a.groups);  // of the greatest group, `groups` itself
-    for (int64_t i0 = wlo; i0 < whi; i0 += 32 * U) {
+    const int32_t* ids = a.ids + lo;
+    int32_t* place = a.place + lo;
+    const int r1 = (int)(whi - lo);
+    const unsigned before_me = (1u << lane) - 1;
+    for (int r0 = (int)(wlo - lo) + lane; r0 - lane < r1; r0 += 32 * U) {
         int32_t id[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) id[u] = i0 + 32 * u + lane < whi ? __ldg(a.ids + i0 + 32 * u + lane) : 0;
+        for (int u = 0; u < U; ++u) id[u] = r0 + 32 * u < r1 ? __ldg(ids + r0 + 32 * u) : 0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (i0 + 32 * u >= whi) break;
-            const int64_t i = i0 + 32 * u + lane;
-            const bool live = i < whi;
-            const int g = live ? group_of(id[u], a.groups) : 0;
-            // the lanes with the same group, one bit of it at a time (a vote each; the
-            // hardware's match of whole words takes far longer: 7.5 us of 1 M slots' 22)
+            const int r = r0 + 32 * u;
+            if (r - lane >= r1) break;
+            const bool live = r < r1;
+            const int g = group_of(id[u], a.groups);
+            // the lanes with the same group, one bit of it at a time: a vote each (the
+            // hardware's match of whole words made the whole call a tenth longer)
             unsigned same = __ballot_sync(0xffffffffu, live);
-            for (int bit = 0; bit < bits; ++bit) {
-                const bool one = g >> bit & 1;
-                const unsigned ones = __ballot_sync(0xffffffffu, one);
-                same &= one ? ones : ~ones;
+#pragma unroll
+            for (int bit = 0; bit < 11; ++bit) {
+                if (bit < bits) {
+                    const bool one = g & (1 << bit);
+                    same &= __ballot_sync(0xffffffffu, one) ^ (one ? 0u : 0xffffffffu);
+                }
             }
-            int at = 0;
-            if (live) at = next[g] + __popc(same & ((1u << lane) - 1));
+            const int rank = __popc(same & before_me);
+            int at = next[g] + rank;
             __syncwarp();
-            if (live && lane == __ffs(same) - 1) next[g] += __popc(same);
+            if (live && rank == 0) next[g] = at + __popc(same);
             __syncwarp();
             if (live) {
-                a.order[at] = (int32_t)i;
-                a.place[i] = at;
+                at += s_first[g];
+                a.order[at] = (int32_t)(lo + r);
+                place[r] = at;
             }
         }
     }
@@ -186,21 +226,25 @@ static om_status prepare_group(const DeviceState* d) {
     static bool ready[128];
     std::lock_guard<std::mutex> lk(mu);
     if (!ready[d->dev]) {
-        if (cudaFuncSetAttribute(group_by_id_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kGroupWarps * (kMaxGroups + 1) * 4) != cudaSuccess) {
-            cudaGetLastError();
-            return OM_ECUDA;
-        }
+        for (auto* kern : {group_by_id_kernel<kGroupLone>, group_by_id_kernel<kGroupCluster>,
+                           group_by_id_kernel<kGroupGrid>})
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (kGroupWarps + 2) * (kMaxGroups + 1) * 4) != cudaSuccess) {
+                cudaGetLastError();
+                return OM_ECUDA;
+            }
         ready[d->dev] = true;
     }
     return OM_OK;
 }
 
-// Least slots of a CTA of several; and the slots up to which one CTA does the
-// call alone, without the exchange: 4096 slots of 256 groups 7.2 us (two CTAs
-// 14), 8192 of 128 10.3 (four 10.8).
-constexpr int64_t kGroupLeastChunk = 2048;
-constexpr int64_t kGroupLone = 8192;
+// Slots up to which one CTA, and one cluster, does the call: 2048 slots of 64
+// groups 5.2 us alone, 6.0 in a cluster; 8192 of 128 11.1 and 6.3; 32768 of 256
+// 9.3 us in a cluster, 11.5 in a grid; 65536 of 256 13.4 and 10.4.
+constexpr int64_t kGroupLoneSlots = 2048;
+constexpr int64_t kGroupClusterSlots = 49152;
+// Least slots of a CTA of several (8192 slots in 8 CTAs 6.3 us, in 4 7.1).
+constexpr int64_t kGroupLeastChunk = 1024;
 
 }  // namespace om
 
@@ -223,29 +267,41 @@ om_status om_group_by_id(const int32_t* ids, int64_t n, int64_t groups, int32_t*
     om_status s = device_state(&d);
     if (s == OM_OK) s = prepare_group(d);
     if (s != OM_OK) return s;
-    // a chunk holds at least the two words per group that its CTA exchanges
-    int64_t least = 2 * (groups + 1);
-    if (least < kGroupLeastChunk) least = kGroupLeastChunk;
-    int64_t ctas = n / least;
-    if (ctas > d->sm_count) ctas = d->sm_count;
-    if (n < kGroupLone) ctas = 1;
-    if (ctas < 1) ctas = 1;
+    int way = kGroupLone, warps = kGroupWarps;
+    int64_t ctas = 1;
+    if (n <= kGroupLoneSlots) {
+        if (n <= 128 * (kGroupWarps - 1)) warps = (int)(n / 128) + 1;  // a warp per 128 slots
+    } else if (n <= kGroupClusterSlots) {
+        way = kGroupCluster;
+        for (ctas = 2; ctas < kGroupCluster8 && ctas * kGroupLeastChunk < n; ctas *= 2) {}
+    } else {
+        // a chunk holds at least the two words per group that its CTA exchanges
+        way = kGroupGrid;
+        ctas = n / (2 * (groups + 1) > kGroupLeastChunk ? 2 * (groups + 1) : kGroupLeastChunk);
+        if (ctas > d->sm_count) ctas = d->sm_count;
+    }
     GroupArgs a{ids, n, (int)groups, offsets, order, place, (int)(n / ctas), (int)(n % ctas)};
-    // a lone CTA takes a warp per 128 slots
-    int warps = kGroupWarps;
-    if (ctas == 1 && n <= 128 * (kGroupWarps - 1)) warps = (int)(n / 128) + 1;
     cudaStream_t st = (cudaStream_t)stream;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(warps * 32);
-    cfg.dynamicSmemBytes = (size_t)warps * (groups + 1) * 4;
+    cfg.dynamicSmemBytes = (size_t)(warps + 2) * (groups + 1) * 4;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
+    if (way == kGroupGrid) {
+        attr[0].id = cudaLaunchAttributeCooperative;
+        attr[0].val.cooperative = 1;
+    } else {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)ctas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = ctas > 1 ? 1 : 0;
-    const cudaError_t e = traced(kKindGroup, st, [&] { cudaLaunchKernelEx(&cfg, group_by_id_kernel, a); });
+    cfg.numAttrs = way == kGroupLone ? 0 : 1;
+    auto* kern = way == kGroupLone      ? group_by_id_kernel<kGroupLone>
+                 : way == kGroupCluster ? group_by_id_kernel<kGroupCluster>
+                                        : group_by_id_kernel<kGroupGrid>;
+    const cudaError_t e = traced(kKindGroup, st, [&] { cudaLaunchKernelEx(&cfg, kern, a); });
     return e == cudaSuccess ? OM_OK : cuda_fail(e);
 }
 
