@@ -157,9 +157,9 @@ om_status om_device_error(void *stream, uint32_t *detail);
  * With tracing on, every kernel launch is bracketed by two CUDA events on its
  * stream.  om_trace_read synchronises those events and returns, for kernel
  * kind `kind` (0 = partition, 1 = tile merge, 2 = block sort, 3 = co-rank
- * batch, 4 = the comparison merges below, 5 = one-pass merge, 6 = routing,
- * 7 = grouping, 8 = accumulation and eviction), the number of launches and
- * their summed duration in milliseconds since the last om_trace_reset.
+ * batch, 4 = the comparison merges below, 5 = one-pass merge), the number of
+ * launches and their summed duration in milliseconds since the last
+ * om_trace_reset.
  */
 om_status om_trace_enable(int on);
 om_status om_trace_reset(void);
@@ -313,7 +313,8 @@ om_status om_merge_sort_keys(int key_type, int order, void *keys,
  * tokens by their experts, the entries of a cache by the attention they have
  * drawn.  As in the merges, ties go to the earlier (lower) index.  All calls
  * are asynchronous on `stream` and allocate nothing.
- * These calls do not need sorted input.
+ * These calls do not need sorted input.  Their launches are in
+ * om_launch_count, but om_trace_read has no kind for them.
  */
 
 /* Value types of logits and attention weights. */

@@ -99,10 +99,7 @@ enum KernelKind {
     kKindCorank = 3,
     kKindBaseline = 4,
     kKindOnePass = 5,
-    kKindRoute = 6,
-    kKindGroup = 7,
-    kKindEvict = 8,
-    kNumKinds = 9
+    kNumKinds = 6
 };
 
 // ------------------------------------------------------------ device state --

@@ -303,7 +303,7 @@ static cudaError_t launch_accumulate(const AccumulateArgs& a, int64_t batch, int
     const bool direct = log_split == 0 && low4 % 4 == 0;
     const int64_t wide = (log_split == 0 ? 2 : 1) * tile;
     const dim3 grid((unsigned)((a.length + wide - 1) / wide), (unsigned)(batch * a.kv_heads));
-    return traced(kKindEvict, st, [&] {
+    return counted([&] {
         if (aligned) launch_accumulate_split<T, true>(a, grid, log_split, direct, st);
         else launch_accumulate_split<T, false>(a, grid, log_split, direct, st);
     });
@@ -611,7 +611,7 @@ static cudaError_t launch_select(const EvictArgs& a, int64_t rows, int sm_count,
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     auto* kern = cached ? evict_select_kernel<true> : evict_select_kernel<false>;
-    return traced(kKindEvict, st, [&] { cudaLaunchKernelEx(&cfg, kern, a); });
+    return counted([&] { cudaLaunchKernelEx(&cfg, kern, a); });
 }
 
 // --------------------------------------------------------------- gather --
@@ -831,8 +831,7 @@ om_status om_evict_gather(const int32_t* keep, int64_t batch, int64_t heads, int
         if (ctas > INT32_MAX) return OM_ERANGE;
     }
     cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = traced(
-        kKindEvict, st, [&] { evict_gather_kernel<<<(unsigned)ctas, kGatherThreads, 0, st>>>(a); });
+    const cudaError_t e = counted([&] { evict_gather_kernel<<<(unsigned)ctas, kGatherThreads, 0, st>>>(a); });
     return e == cudaSuccess ? OM_OK : cuda_fail(e);
 }
 

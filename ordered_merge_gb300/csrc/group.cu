@@ -301,7 +301,7 @@ om_status om_group_by_id(const int32_t* ids, int64_t n, int64_t groups, int32_t*
     auto* kern = way == kGroupLone      ? group_by_id_kernel<kGroupLone>
                  : way == kGroupCluster ? group_by_id_kernel<kGroupCluster>
                                         : group_by_id_kernel<kGroupGrid>;
-    const cudaError_t e = traced(kKindGroup, st, [&] { cudaLaunchKernelEx(&cfg, kern, a); });
+    const cudaError_t e = counted([&] { cudaLaunchKernelEx(&cfg, kern, a); });
     return e == cudaSuccess ? OM_OK : cuda_fail(e);
 }
 

@@ -725,7 +725,7 @@ static cudaError_t launch_list_lanes(const RouteArgs& a, bool aligned, cudaStrea
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     const int steps = (a.experts + 8 * L - 1) / (8 * L);
     const size_t smem = MODE == kListPacked ? 0 : (size_t)steps * kListThreads * 9 * sizeof(float);
-    return traced(kKindRoute, st, [&] {
+    return counted([&] {
         route_list_kernel<T, MODE, GROUPED, L><<<(unsigned)blocks, kListThreads, smem, st>>>(a, aligned);
     });
 }
@@ -841,7 +841,7 @@ om_status om_route_topk(int value_type, const void* logits, int64_t tokens, int6
     }
     const cudaError_t e = with_value_type(value_type, [&](auto v) {
         return with_lane_experts((int)experts, [&](auto r) {
-            return traced(kKindRoute, st, [&] {
+            return counted([&] {
                 route_topk_kernel<decltype(v), decltype(r)::value><<<route_grid(tokens), kRouteWarps * 32, 0, st>>>(a);
             });
         });
@@ -876,7 +876,7 @@ om_status om_route_topk_backward(int value_type, const void* logits, int64_t tok
     if (tokens * 8 > (int64_t)INT32_MAX * 128) return OM_ERANGE;
     const cudaError_t e = with_value_type(value_type, [&](auto v) {
         using T = decltype(v);
-        return traced(kKindRoute, st, [&] {
+        return counted([&] {
             if (dense) launch_back<T, true>(a, aligned_in, aligned_out, few, st);
             else launch_back<T, false>(a, aligned_in, aligned_out, few, st);
         });

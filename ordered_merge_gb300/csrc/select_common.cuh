@@ -10,7 +10,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include "om_ptx.cuh"
+#include "api_internal.cuh"
 #include "ordmerge.h"
 
 namespace om {
@@ -72,6 +72,14 @@ __device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
     return v;
+}
+
+// Launches through `launch` (a callable issuing exactly one kernel) and counts
+// it for om_launch_count; om_trace_* keep no kind for these kernels.
+template <typename F>
+cudaError_t counted(F&& launch) {
+    launch();
+    return trace_end(TraceRec{0, nullptr, nullptr}, false, nullptr);
 }
 
 inline int value_bytes(int value_type) {
