@@ -363,8 +363,7 @@ __device__ __forceinline__ int place_of(const int (&c)[P], int need, int* over) 
 
 struct SelectShared {
     __align__(16) int hist[kPasses][kDigits];
-    int coarse[kPasses][kCoarse];        // sums of 32 digits each
-    int peers[kMaxCluster][kCoarse];     // the cluster's
+    int coarse[kPasses][kCoarse];  // sums of 32 digits each
     int above[kSelectWarps], equal[kSelectWarps];  // kept for sure / on the edge, in the warps before
     int total[2];                                  // the same of the CTA
     int digit, over;
@@ -440,7 +439,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(EvictAr
             if (pass == 0 || (k & mask) == prefix) atomicAdd(&s.hist[pass][(k >> shift) & digits], 1);
         };
         if (pass == 0) {
-            constexpr int U = 4;  // loads in flight per lane
+            constexpr int U = 8;  // loads in flight per lane
             for (int i0 = lo; i0 < hi; i0 += kSelectStep * U) {
                 float4 x[U];
 #pragma unroll
@@ -470,16 +469,16 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(EvictAr
         }
         cluster_sync();
         // first which 32 digits, then which of them, both summed over the cluster
-        for (int i = threadIdx.x; i < (int)ctas * kCoarse; i += kSelectThreads)
-            (&s.peers[0][0])[i] = peer_word(&s.coarse[pass][i % kCoarse], i / kCoarse);
-        __syncthreads();
         if (warp == 0) {
-            int c[kCoarse / 32] = {}, over, more;
-            for (uint32_t r = 0; r < ctas; ++r)
+            constexpr int C = kCoarse / 32;
+            int c[C] = {}, f[1] = {0}, over, more;
 #pragma unroll
-                for (int j = 0; j < kCoarse / 32; ++j) c[j] += s.peers[r][kCoarse - 1 - (lane * (kCoarse / 32) + j)];
+            for (uint32_t r = 0; r < kMaxCluster; ++r)
+                if (r < ctas) {
+#pragma unroll
+                    for (int j = 0; j < C; ++j) c[j] += peer_word(&s.coarse[pass][kCoarse - 1 - (lane * C + j)], r);
+                }
             const int top = kCoarse - 1 - place_of(c, need, &over);
-            int f[1] = {0};
 #pragma unroll
             for (uint32_t r = 0; r < kMaxCluster; ++r)
                 if (r < ctas) f[0] += peer_word(&s.hist[pass][top * 32 + 31 - lane], r);
@@ -532,36 +531,46 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(EvictAr
             const uint32_t* p = &k[u].x;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                sures += p[j] > prefix ? 1u << (8 * u) : 0u;
-                ties += p[j] == prefix ? 1u << (8 * u) : 0u;
+                if (p[j] > prefix) sures += 1u << (8 * u);
+                if (p[j] == prefix) ties += 1u << (8 * u);
             }
         }
-        uint32_t run_s = sures, run_t = ties;
+        uint32_t run_s = sures, run_t = ties, all_t = 0;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t us = __shfl_up_sync(0xffffffffu, run_s, d), ut = __shfl_up_sync(0xffffffffu, run_t, d);
-            if (lane >= d) run_s += us, run_t += ut;
+            const uint32_t up = __shfl_up_sync(0xffffffffu, run_s, d);
+            if (lane >= d) run_s += up;
         }
-        const uint32_t all_s = __shfl_sync(0xffffffffu, run_s, 31), all_t = __shfl_sync(0xffffffffu, run_t, 31);
+        const uint32_t all_s = __shfl_sync(0xffffffffu, run_s, 31);
         run_s -= sures;
-        run_t -= ties;
+        if (__any_sync(0xffffffffu, ties != 0)) {
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t up = __shfl_up_sync(0xffffffffu, run_t, d);
+                if (lane >= d) run_t += up;
+            }
+            all_t = __shfl_sync(0xffffffffu, run_t, 31);
+            run_t -= ties;
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t* p = &k[u].x;
             const int i = i0 + u * kSelectStep + 4 * lane;
-            int at = gone_above + min(gone_equal, need) + (int)(run_s >> (8 * u) & 255);
+            int32_t* out = keep + (gone_above + min(gone_equal, need) + (int)(run_s >> (8 * u) & 255));
             if ((all_t >> (8 * u) & 255) == 0) {  // nothing on the edge in this step
+                if ((sures >> (8 * u) & 255) != 0) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (p[j] > prefix) keep[at++] = i + j;
+                    for (int j = 0; j < 4; ++j)
+                        if (p[j] > prefix) *out++ = i + j;
+                }
             } else {
                 int tied = gone_equal + (int)(run_t >> (8 * u) & 255);
-                at += min(tied, need) - min(gone_equal, need);
+                out += min(tied, need) - min(gone_equal, need);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     // of the keys on the edge the first `need` of the row stay
                     const bool tie = p[j] == prefix;
-                    if (p[j] > prefix || (tie && tied < need)) keep[at++] = i + j;
+                    if (p[j] > prefix || (tie && tied < need)) *out++ = i + j;
                     tied += tie;
                 }
             }

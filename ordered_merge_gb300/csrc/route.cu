@@ -420,7 +420,12 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
         }
         sort8(k);
         if constexpr (!PACKED) s_greatest[step * kListThreads + threadIdx.x] = k[0];
-        merge_best8(best, k);
+        if (step > 0) {
+            merge_best8(best, k);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) best[i] = k[i];
+        }
         x = next;
     }
     bool open = true;  // this lane's share may be chosen from
