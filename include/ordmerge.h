@@ -344,13 +344,14 @@ typedef enum {
  * group_best = 1 (or one group) the order is taken from the logits
  * themselves, which the rounding of exp cannot tie.
  *  - An expert whose logit is -inf or NaN has no score (softmax does not
- *    count it); that one, and one whose bias is -inf or NaN, is never chosen.
+ *    count it); that one, and one whose c is -inf or NaN, is never chosen.
  *    A token with fewer than top_k experts left gets id -1 and weight 0 in
  *    the slots left over, a wholly masked one in all of them.
  *  - The renormalised weights come from shifted exponentials: they stay
  *    right when every s underflows.
  *  - 1 <= top_k <= group_picks * (experts / groups), groups divides experts.
- *    At most 1024 experts, 32 groups and top_k 32, else OM_ERANGE.
+ *    At most 1024 experts, 32 groups, top_k 32 and 2^32 tokens, else
+ *    OM_ERANGE.
  */
 om_status om_route_topk(int value_type, const void *logits, int64_t tokens,
                         int64_t experts, int64_t row_stride,

@@ -24,7 +24,7 @@ def test_route_refusals(om):
                 dict(vt=1, x=0x10001), dict(ids=0x90001), dict(bias=0x20002), dict(stride=-1), dict(w=0x90008),
                 dict(ids=0x10040), dict(bias=0x90010), dict(w=0x10000 - 16)):
         assert _route(L, **bad) == om.OM_EINVAL, bad
-    for bad in (dict(e=1025, stride=1025), dict(k=33), dict(groups=64, picks=64), dict(t=1 << 41), dict(stride=1 << 41)):
+    for bad in (dict(e=1025, stride=1025), dict(k=33), dict(groups=64, picks=64), dict(t=1 << 33), dict(t=1 << 32, stride=1 << 40), dict(stride=1 << 57)):
         assert _route(L, **bad) == om.OM_ERANGE, bad
     assert _route(L, t=0, x=None, ids=None, w=None) == om.OM_OK
 
