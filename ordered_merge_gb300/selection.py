@@ -23,6 +23,7 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 # The current stream's handle without building a Stream object, where this
 # torch has the call (3 us less a call on the measured host).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device, _cuda_ready = torch.cuda.current_device, torch.cuda.is_initialized
 
 
 def _ptr(t):
@@ -42,20 +43,17 @@ def _empty(shape, dtype, device, stream):
 def _launch_stream(stream, names, *tensors):
     """The handle of `stream`, or of the current one, on the current device,
     where every tensor (None: not given) has to be."""
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"{_named(names, tensors, t)} must be a CUDA tensor")
-    device = torch.cuda.current_device()
+    device = _current_device() if _cuda_ready() else -2
     for t in tensors:
         if t is not None and t.get_device() != device:
-            raise ValueError(f"{_named(names, tensors, t)} is on {t.device}, but the current device is cuda:{device}")
+            i = next(i for i, x in enumerate(tensors) if x is t)
+            name = names.split()[min(i, names.count(" "))]
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
     if stream is None and _raw_stream is not None:
         return _raw_stream(device)
     return _stream(stream)
-
-
-def _named(names, tensors, t):
-    return names.split()[next(i for i, x in enumerate(tensors) if x is t)]
 
 
 def _dense(t, name: str, shape, dtype):
@@ -238,16 +236,23 @@ def _cache_entry(shape, strides, name: str, batch: int, heads: int) -> int:
 
 
 @functools.lru_cache(maxsize=256)
-def _gather_geometry(keep_shape, size: int, src_shape, src_strides, dst_shape, dst_strides):
-    """Checks one array's shapes and strides (of elements of `size` bytes) and
-    returns what om_cache_array says of them: bytes per entry and the strides
-    in bytes.  Of the shapes alone, so it is kept from call to call."""
+def _gather_geometry(keep_shape, *arrays):
+    """Checks the arrays' shapes and strides (each array: element size, then
+    shape and strides of source and output) and returns, as om_cache_array
+    wants them, every array's bytes per entry and strides in bytes, and the
+    number of entries.  Of the shapes alone, so it is kept from call to call."""
     batch, heads, budget = keep_shape
-    inner = _cache_entry(src_shape, src_strides, "array", batch, heads)
-    want = (*keep_shape, *src_shape[3:])
-    if dst_shape != want or _cache_entry(dst_shape, dst_strides, "out", batch, heads) != inner:
-        raise ValueError(f"out must have shape {want} (got {tuple(dst_shape)})")
-    return (inner * size, *(s * size for s in src_strides[:3]), *(s * size for s in dst_strides[:3]))
+    words, length = [], None
+    for size, src_shape, src_strides, dst_shape, dst_strides in zip(*[iter(arrays)] * 5):
+        inner = _cache_entry(src_shape, src_strides, "array", batch, heads)
+        want = (*keep_shape, *src_shape[3:])
+        if dst_shape != want or _cache_entry(dst_shape, dst_strides, "out", batch, heads) != inner:
+            raise ValueError(f"out must have shape {want} (got {tuple(dst_shape)})")
+        if length is not None and src_shape[2] != length:
+            raise ValueError("the arrays must have as many entries each")
+        length = src_shape[2]
+        words.append((inner * size, *(s * size for s in src_strides[:3]), *(s * size for s in dst_strides[:3])))
+    return words, length, struct.Struct(f"{9 * len(words)}q").pack
 
 
 def om_evict_gather(keep, arrays, out=None, stream=None):
@@ -260,24 +265,23 @@ def om_evict_gather(keep, arrays, out=None, stream=None):
     if len(shape) != 3:
         raise ValueError("keep must have 3 dimensions")
     _dense(keep, "keep", shape, torch.int32)
-    if not arrays or arrays[0].dim() < 3:
-        raise ValueError("arrays must hold tensors [batch, heads, entries, ...]")
-    length = arrays[0].shape[2]
+    if not arrays:
+        raise ValueError("no arrays to gather")
     if out is None:
         out = tuple(_empty((*shape, *t.shape[3:]), t.dtype, t.device, stream) for t in arrays)
     out = tuple(out)
     if len(out) != len(arrays):
         raise ValueError("out must hold one tensor for each array")
-    handle = _launch_stream(stream, "keep" + " array" * len(arrays) + " out" * len(out), keep, *arrays, *out)
-    table = []
+    handle = _launch_stream(stream, "keep array", keep, *arrays, *out)
+    key = []
     for src, dst in zip(arrays, out):
         if dst.dtype != src.dtype:
             raise ValueError(f"out must be {src.dtype} (got {dst.dtype})")
-        geometry = _gather_geometry(shape, src.element_size(), src.shape, src.stride(), dst.shape, dst.stride())
-        if src.shape[2] != length:
-            raise ValueError("the arrays must have as many entries each")
-        table += (src.data_ptr(), dst.data_ptr(), *geometry)
+        key += (src.element_size(), src.shape, src.stride(), dst.shape, dst.stride())
+    words, length, pack = _gather_geometry(shape, *key)
+    table = []
+    for src, dst, fixed in zip(arrays, out, words):
+        table += (src.data_ptr(), dst.data_ptr(), *fixed)
     # om_cache_array: nine 64-bit words
-    _check(_lib.om_evict_gather(_ptr(keep), *shape, length, struct.pack(f"{len(table)}q", *table), len(arrays), handle),
-           "om_evict_gather")
+    _check(_lib.om_evict_gather(_ptr(keep), *shape, length, pack(*table), len(arrays), handle), "om_evict_gather")
     return out
