@@ -175,9 +175,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(RouteArgs 
 // What bounds it is the rate of minima and maxima (half of the issue rate): a
 // token of 128 bf16 logits takes about 50 warp instructions of them and 80 in
 // all.  Measured, 131071 tokens, top 8: 128 bf16 logits 18 us (2.3 TB/s), 128
-// f32 29 us, 256 f32 sigmoid scores with bias in 8 groups 82 us, where the
+// f32 29 us, 256 f32 sigmoid scores with bias in 8 groups 66 us, where the
 // kernel above takes 87, 87 and 271 us.
 constexpr int kListThreads = 128;
+constexpr int kListPitch = kListThreads + 1;  // of the rows of choices: neighbouring rows start on other banks
 
 __device__ __forceinline__ uint32_t greater(uint32_t a, uint32_t b) { return max(a, b); }
 __device__ __forceinline__ uint32_t lesser(uint32_t a, uint32_t b) { return min(a, b); }
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
     using Key = typename std::conditional<PACKED, uint32_t, float>::type;
     constexpr unsigned kAll = 0xffffffffu;
     const float kNone = -INFINITY;
-    extern __shared__ float4 s_choice[];       // [steps][2][kListThreads]: a lane's eights, [steps] their greatest
+    extern __shared__ float4 s_choice[];       // [steps][2][kListPitch]: a lane's eights; [steps]: their greatest
     __shared__ int s_id[kListThreads / L][8];  // the picks of a token
     const int l = threadIdx.x & (L - 1), slot = threadIdx.x / L;
     const int64_t t = (int64_t)blockIdx.x * (kListThreads / L) + slot;
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
     const int steps = (a.experts + 8 * L - 1) / (8 * L);
     const int share = a.experts / L, end = GROUPED ? (l + 1) * share : a.experts;
     auto first_of = [&](int step) { return GROUPED ? l * share + step * 8 : (step * L + l) * 8; };
-    float* s_greatest = reinterpret_cast<float*>(s_choice + 2 * steps * kListThreads);
+    float* s_greatest = reinterpret_cast<float*>(s_choice + 2 * steps * kListPitch);
 
     // softmax over the row, where it is needed
     float top = kNone, sum = 1.0f;
@@ -376,48 +377,32 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
     Key best[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) best[i] = PACKED ? Key(0) : Key(kNone);
-    // one step's load is on its way while the one before is sorted
-    Eight<T> x = load_eight(row, first_of(0), end, aligned);
-#pragma unroll 1
-    for (int step = 0; step < steps; ++step) {
-        const int e = first_of(step);
-        Eight<T> next = x;
-        if (step + 1 < steps) next = load_eight(row, first_of(step + 1), end, aligned);
-        Key k[8];
-        if constexpr (PACKED) {
-            uint32_t index = (uint32_t)(0xffff - e) | (uint32_t)(0xffff - e - 1) << 16;
+    // what the eight experts from e on, with logits x, are chosen by; -inf where masked, and no -0
+    auto choose = [&](const Eight<T>& x, int e, int end, float (&k)[8]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t w = plain_pair(x.w[i], T{});
-                // negative values are complemented, others get the top bit
-                const uint32_t image = w ^ (half_signs(w) | 0x80008000u);
-                k[2 * i] = __byte_perm(index, image, 0x5410);
-                k[2 * i + 1] = __byte_perm(index, image, 0x7632);
-                index -= 0x00020002u;
-            }
-        } else {
-            // what the experts are chosen by; -inf where masked, and no -0
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float v = value_of(x, i);
-                // the hardware's 2^x: its error, below 2^-22 of the score, is that of ordering in 32 bits
-                if (MODE == kListSoftmax) k[i] = __expf(v - top) * inverse;
-                else if (MODE == kListSigmoid) k[i] = __fdividef(1.0f, 1.0f + __expf(-v));
-                else k[i] = v;
-            }
-            if (!BY_LOGIT && a.bias != nullptr) {
-                const Eight<float> bias = load_eight(a.bias, e, end, ((uintptr_t)(a.bias + e) & 15) == 0);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) k[i] += value_of(bias, i);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                k[i] = fmaxf(k[i], kNone) + 0.0f;
-                if (!BY_LOGIT && !(value_of(x, i) > kNone)) k[i] = kNone;
-            }
-            s_choice[2 * step * kListThreads + threadIdx.x] = make_float4(k[0], k[1], k[2], k[3]);
-            s_choice[(2 * step + 1) * kListThreads + threadIdx.x] = make_float4(k[4], k[5], k[6], k[7]);
+        for (int i = 0; i < 8; ++i) {
+            const float v = value_of(x, i);
+            // the hardware's 2^x: its error, below 2^-22 of the score, is that of ordering in 32 bits
+            if (MODE == kListSoftmax) k[i] = __expf(v - top) * inverse;
+            else if (MODE == kListSigmoid) k[i] = __fdividef(1.0f, 1.0f + __expf(-v));
+            else k[i] = v;
         }
+        if (!BY_LOGIT && a.bias != nullptr) {
+            const Eight<float> bias = load_eight(a.bias, e, end, ((uintptr_t)(a.bias + e) & 15) == 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) k[i] += value_of(bias, i);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            k[i] = fmaxf(k[i], kNone) + 0.0f;
+            if (!BY_LOGIT && !(value_of(x, i) > kNone)) k[i] = kNone;
+        }
+    };
+    auto keep_choices = [&](int step, int thread, const float (&k)[8]) {
+        s_choice[2 * step * kListPitch + thread] = make_float4(k[0], k[1], k[2], k[3]);
+        s_choice[(2 * step + 1) * kListPitch + thread] = make_float4(k[4], k[5], k[6], k[7]);
+    };
+    auto list = [&](int step, Key (&k)[8]) {
         sort8(k);
         if constexpr (!PACKED) s_greatest[step * kListThreads + threadIdx.x] = k[0];
         if (step > 0) {
@@ -426,7 +411,63 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
 #pragma unroll
             for (int i = 0; i < 8; ++i) best[i] = k[i];
         }
-        x = next;
+    };
+    if (GROUPED && !PACKED && sizeof(T) == 4 && share >= 32 && share % 8 == 0) {
+        // The lanes' shares lie a line or more apart, so the row is read across the
+        // lanes, and the choices handed to the lanes whose they are through shared
+        // memory.  (Loads of their own shares touched 32 lines each and filled 72 %
+        // of the load path: 131071 tokens of 256 f32 took 82 us, this way 66; shares
+        // of 16 f32 52 and 53, of 32 bf16 65 both ways.)
+        if constexpr (!PACKED) {
+            const int own = share / 8;  // eights of a lane
+            Eight<T> x = load_eight(row, l * 8, a.experts, aligned);
+#pragma unroll 1
+            for (int step = 0; step < own; ++step) {
+                const int eight = step * L + l;
+                Eight<T> next = x;
+                if (step + 1 < own) next = load_eight(row, (eight + L) * 8, a.experts, aligned);
+                float k[8];
+                choose(x, eight * 8, a.experts, k);
+                const int owner = eight / own;
+                keep_choices(eight - owner * own, (int)threadIdx.x - l + owner, k);
+                x = next;
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int step = 0; step < own; ++step) {
+                const float4* two = s_choice + 2 * step * kListPitch + threadIdx.x;
+                const float4 lo = two[0], hi = two[kListPitch];
+                Key k[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                list(step, k);
+            }
+        }
+    } else {
+        // one step's load is on its way while the one before is sorted
+        Eight<T> x = load_eight(row, first_of(0), end, aligned);
+#pragma unroll 1
+        for (int step = 0; step < steps; ++step) {
+            const int e = first_of(step);
+            Eight<T> next = x;
+            if (step + 1 < steps) next = load_eight(row, first_of(step + 1), end, aligned);
+            Key k[8];
+            if constexpr (PACKED) {
+                uint32_t index = (uint32_t)(0xffff - e) | (uint32_t)(0xffff - e - 1) << 16;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w = plain_pair(x.w[i], T{});
+                    // negative values are complemented, others get the top bit
+                    const uint32_t image = w ^ (half_signs(w) | 0x80008000u);
+                    k[2 * i] = __byte_perm(index, image, 0x5410);
+                    k[2 * i + 1] = __byte_perm(index, image, 0x7632);
+                    index -= 0x00020002u;
+                }
+            } else {
+                choose(x, e, end, k);
+                keep_choices(step, threadIdx.x, k);
+            }
+            list(step, k);
+            x = next;
+        }
     }
     bool open = true;  // this lane's share may be chosen from
     if constexpr (GROUPED) {
@@ -479,8 +520,8 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
         int found = 0;
         for (uint32_t left = eights; left != 0; left &= left - 1) {
             const int step = __ffs(left) - 1;
-            const float4* two = s_choice + 2 * step * kListThreads + threadIdx.x;
-            const float4 lo = two[0], hi = two[kListThreads];
+            const float4* two = s_choice + 2 * step * kListPitch + threadIdx.x;
+            const float4 lo = two[0], hi = two[kListPitch];
             const float c[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             uint32_t chosen = 0;
 #pragma unroll
@@ -488,7 +529,7 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
             found += __popc(chosen);
             for (; chosen != 0; chosen &= chosen - 1) {
                 const int i = __ffs(chosen) - 1;
-                const float mine = reinterpret_cast<const float*>(two + (i >> 2) * kListThreads)[i & 3];
+                const float mine = reinterpret_cast<const float*>(two + (i >> 2) * kListPitch)[i & 3];
                 int place = 0;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) place += best[j] > mine;
@@ -514,8 +555,8 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
                 if (unsettled && j < valid) {
                     for (uint32_t left = eights; left != 0; left &= left - 1) {
                         const int step = __ffs(left) - 1, e = first_of(step);
-                        const float4* two = s_choice + 2 * step * kListThreads + threadIdx.x;
-                        const float4 lo = two[0], hi = two[kListThreads];
+                        const float4* two = s_choice + 2 * step * kListPitch + threadIdx.x;
+                        const float4 lo = two[0], hi = two[kListPitch];
                         const float c[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -728,7 +769,7 @@ template <typename T, int MODE, bool GROUPED, int L>
 static cudaError_t launch_list_lanes(const RouteArgs& a, bool aligned, cudaStream_t st) {
     const int64_t blocks = (a.tokens + kListThreads / L - 1) / (kListThreads / L);
     const int steps = (a.experts + 8 * L - 1) / (8 * L);
-    const size_t smem = MODE == kListPacked ? 0 : (size_t)steps * kListThreads * 9 * sizeof(float);
+    const size_t smem = MODE == kListPacked ? 0 : (size_t)steps * (2 * kListPitch * sizeof(float4) + kListThreads * sizeof(float));
     return counted([&] {
         route_list_kernel<T, MODE, GROUPED, L><<<(unsigned)blocks, kListThreads, smem, st>>>(a, aligned);
     });
@@ -737,7 +778,7 @@ static cudaError_t launch_list_lanes(const RouteArgs& a, bool aligned, cudaStrea
 // A token gets 32 lanes (PACKED: 16) while that gives an SM at most this many
 // threads (2432 tokens): the shorter chain wins until the SMs are busy.  2048
 // biased sigmoid tokens in 8 groups of 32 experts: 5.8 us against 6.3 with
-// 8 lanes each; 4096: 8.0 against 7.5; 131071: 140 against 82.
+// 8 lanes each; 4096: 7.8 against 7.6; 131071: 140 against 66.
 constexpr int kListFewThreads = 512;
 // The most experts that 4 (grouped: twice as many for 8) lanes take, whose
 // choices then fill 36 KB of shared memory; not for PACKED, which keeps none.
