@@ -237,3 +237,82 @@ def test_route_backward_strided_logits(gpu):
     ids, w = gpu.route_topk(view, 6)
     g = torch.randn_like(w)
     assert torch.equal(gpu.route_topk_backward(view, ids, g), gpu.route_topk_backward(view.contiguous(), ids, g))
+
+
+# ------------------------------------------- enough tokens for fewer lanes each --
+
+MANY = 2600  # above the number up to which a token gets most lanes
+
+
+def _route_all(x, k, score, bias, groups, picks, best, renorm, scale):
+    """The reference for many rows at once: no masks, no NaN."""
+    s = ref.scores(x, score)
+    by_logit = bias is None and (groups == 1 or best == 1)
+    c = x.copy() if by_logit else s + (0.0 if bias is None else bias)
+    rows = np.arange(len(x))[:, None]
+    if groups > 1:
+        total = -np.sort(-c.reshape(len(x), groups, -1), 2)[:, :, :best].sum(2)
+        out = np.argsort(-total, 1, kind="stable")[:, picks:]
+        c.reshape(len(x), groups, -1)[rows, out] = -np.inf
+    ids = np.argsort(-c, 1, kind="stable")[:, :k]
+    w = s[rows, ids]
+    return ids, (w / w.sum(1, keepdims=True) if renorm else w) * scale
+
+
+@pytest.mark.parametrize("shape", [(64, 6, 1, 1, 1), (128, 8, 1, 1, 1), (160, 8, 8, 3, 2), (256, 8, 8, 4, 2), (256, 8, 8, 4, 1),
+                                   (256, 5, 2, 1, 2), (257, 3, 1, 1, 1), (512, 8, 4, 2, 2), (72, 8, 4, 3, 2), (40, 1, 1, 1, 1),
+                                   (96, 12, 1, 1, 1)], ids=str)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_route_many_tokens(gpu, shape, score, dtype):
+    experts, k, groups, picks, best = shape
+    rng = np.random.default_rng(experts + k)
+    for biased in (False, True):
+        bias = rng.normal(size=experts).astype(np.float32).astype(np.float64) * (0.1 if score == "sigmoid" else 0.01) if biased else None
+        x = _logits(experts * 7 + biased, MANY, experts, dtype, k, score, bias, groups, picks, best)
+        b = None if bias is None else torch.from_numpy(bias).float().cuda()
+        for renorm in (False, True):
+            ids, w = gpu.route_topk(x.cuda(), k, score=score, bias=b, groups=groups, group_picks=picks, group_best=best,
+                                    renorm=renorm, scale=1.5)
+            want_ids, want_w = _route_all(f64(x), k, score, None if b is None else f64(b), groups, picks, best, renorm, 1.5)
+            assert np.array_equal(ids.cpu().numpy(), want_ids)
+            assert np.all(np.abs(f64(w) - want_w) <= WEIGHT_TOL * np.abs(want_w))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("experts,groups,picks", [(64, 1, 1), (130, 1, 1), (256, 8, 3)])
+def test_route_many_tokens_ties_and_masks(gpu, dtype, experts, groups, picks):
+    """A few values only, so most choices tie; some rows and experts masked."""
+    rng = np.random.default_rng(experts)
+    x = torch.from_numpy(rng.integers(-2, 2, (MANY, experts))).to(DTYPES[dtype])
+    x[::7, ::3] = -float("inf")
+    x[5::11, 1] = float("nan")
+    x[13] = -float("inf")
+    x[MANY - 1, 3:] = -float("inf")
+    for score in ("softmax", "sigmoid"):
+        for bias in (None, torch.zeros(experts, device="cuda")):
+            ids, w = gpu.route_topk(x.cuda(), 8, score=score, bias=bias, groups=groups, group_picks=picks, renorm=True)
+            rows = [*range(0, MANY, 97), 5, 13, 16, MANY - 1]
+            want_ids, want_w = ref.route(f64(x[rows]), 8, score, None if bias is None else f64(bias), groups, picks, 1, True)
+            assert np.array_equal(ids.cpu().numpy()[rows], want_ids)
+            assert np.all(np.abs(f64(w)[rows] - want_w) <= WEIGHT_TOL * want_w)
+
+
+@pytest.mark.parametrize("experts,k", [(64, 6), (160, 8), (257, 3), (1000, 8), (48, 1), (96, 20)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_route_backward_many_tokens(gpu, experts, k, score, renorm, dtype):
+    gen = torch.Generator().manual_seed(experts + k)
+    x = (torch.randn(MANY, experts, generator=gen) * 2).clamp(-12, 12).to(DTYPES[dtype])
+    x[3, 2:] = -float("inf")
+    x[4] = -float("inf")
+    x[5, ::5] = float("nan")
+    ids = torch.where(x.isnan(), torch.finfo(torch.float32).min, x.float()).topk(k, 1).indices.to(torch.int32)
+    ids[MANY - 1, 0] = -1
+    grad = torch.randn(MANY, k, generator=gen)
+    got = gpu.route_topk_backward(x.cuda(), ids.cuda(), grad.cuda(), score=score, renorm=renorm, scale=2.5)
+    rows = [0, 1, 3, 4, 5, *range(60, MANY, 101), MANY - 1]
+    clean = torch.where(x.isnan(), -float("inf"), x.float())[rows]
+    want = ref.route_backward(f64(clean), ids.numpy()[rows], f64(grad)[rows], score, renorm, 2.5)
+    assert _grad_close(got[rows], want, f64(grad)[rows], 2.5, k)
