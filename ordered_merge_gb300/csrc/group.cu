@@ -64,7 +64,8 @@ enum GroupWay {
 // of the kernel: 512 slots of 256 groups 5.3 us, 32768 9.3 us, 1.05 M of 128
 // 16.4 us.  Writing `order` from a chunk put in order in shared memory first,
 // in runs, was no faster (16.5 us).
-template <int WAY>
+// BITS: of the greatest group, `groups` itself.
+template <int WAY, int BITS>
 __global__ void __launch_bounds__(kGroupThreads) group_by_id_kernel(GroupArgs a) {
     extern __shared__ int s_next[];  // [warps][E]: a warp's counts, then its next place less the CTA's first
     __shared__ int s_part[kGroupWarps];
@@ -181,7 +182,6 @@ __global__ void __launch_bounds__(kGroupThreads) group_by_id_kernel(GroupArgs a)
     }
     if (WAY == kGroupCluster) cluster_sync();  // no CTA leaves, or writes, while another reads its counts
 
-    const int bits = 32 - __clz(a.groups);  // of the greatest group, `groups` itself
     const int32_t* ids = a.ids + lo;
     int32_t* place = a.place + lo;
     const int r1 = (int)(whi - lo);
@@ -200,11 +200,9 @@ __global__ void __launch_bounds__(kGroupThreads) group_by_id_kernel(GroupArgs a)
             // hardware's match of whole words made the whole call a tenth longer)
             unsigned same = __ballot_sync(0xffffffffu, live);
 #pragma unroll
-            for (int bit = 0; bit < 11; ++bit) {
-                if (bit < bits) {
-                    const bool one = g & (1 << bit);
-                    same &= __ballot_sync(0xffffffffu, one) ^ (one ? 0u : 0xffffffffu);
-                }
+            for (int bit = 0; bit < BITS; ++bit) {
+                const bool one = g & (1 << bit);
+                same &= __ballot_sync(0xffffffffu, one) ^ (one ? 0u : 0xffffffffu);
             }
             const int rank = __popc(same & before_me);
             int at = next[g] + rank;
@@ -220,14 +218,22 @@ __global__ void __launch_bounds__(kGroupThreads) group_by_id_kernel(GroupArgs a)
     }
 }
 
+template <int BITS>
+static auto group_kernel(int way) {
+    return way == kGroupLone      ? group_by_id_kernel<kGroupLone, BITS>
+           : way == kGroupCluster ? group_by_id_kernel<kGroupCluster, BITS>
+                                  : group_by_id_kernel<kGroupGrid, BITS>;
+}
+
 // Once per device: the kernel's shared-memory limit.
 static om_status prepare_group(const DeviceState* d) {
     static std::mutex mu;
     static bool ready[128];
     std::lock_guard<std::mutex> lk(mu);
     if (!ready[d->dev]) {
-        for (auto* kern : {group_by_id_kernel<kGroupLone>, group_by_id_kernel<kGroupCluster>,
-                           group_by_id_kernel<kGroupGrid>})
+        for (auto* kern : {group_by_id_kernel<kGroupLone, 8>, group_by_id_kernel<kGroupLone, 11>,
+                           group_by_id_kernel<kGroupCluster, 8>, group_by_id_kernel<kGroupCluster, 11>,
+                           group_by_id_kernel<kGroupGrid, 8>, group_by_id_kernel<kGroupGrid, 11>})
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (kGroupWarps + 2) * (kMaxGroups + 1) * 4) != cudaSuccess) {
                 cudaGetLastError();
@@ -298,9 +304,8 @@ om_status om_group_by_id(const int32_t* ids, int64_t n, int64_t groups, int32_t*
     }
     cfg.attrs = attr;
     cfg.numAttrs = way == kGroupLone ? 0 : 1;
-    auto* kern = way == kGroupLone      ? group_by_id_kernel<kGroupLone>
-                 : way == kGroupCluster ? group_by_id_kernel<kGroupCluster>
-                                        : group_by_id_kernel<kGroupGrid>;
+    auto* kern = group_kernel<8>(way);
+    if (groups >= 256) kern = group_kernel<11>(way);
     const cudaError_t e = counted([&] { cudaLaunchKernelEx(&cfg, kern, a); });
     return e == cudaSuccess ? OM_OK : cuda_fail(e);
 }
