@@ -320,9 +320,7 @@ struct EvictArgs {
     int length, heads, budget, first, last;
 };
 
-constexpr int kSelectThreads = 512;
 constexpr int kSelectStep = 128;  // keys a warp takes at a time, four consecutive ones per lane
-constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kDigitBits = 11;
 constexpr int kDigits = 1 << kDigitBits;
 constexpr int kCoarse = kDigits / 32;
@@ -361,10 +359,11 @@ __device__ __forceinline__ int place_of(const int (&c)[P], int need, int* over) 
     return __shfl_sync(0xffffffffu, place, owner & 31);
 }
 
+template <int WARPS>
 struct SelectShared {
     __align__(16) int hist[kPasses][kDigits];
     int coarse[kPasses][kCoarse];  // sums of 32 digits each
-    int above[kSelectWarps], equal[kSelectWarps];  // kept for sure / on the edge, in the warps before
+    int above[WARPS], equal[WARPS];  // kept for sure / on the edge, in the warps before
     int total[2];                                  // the same of the CTA
     int digit, over;
 };
@@ -379,12 +378,20 @@ struct SelectShared {
 // once and kept in shared memory (CACHED), unless the part is too long for it.
 // Places past the row's end hold key 0, which is below every score's and so
 // never reached.
-template <bool CACHED>
-__global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(EvictArgs a) {
+template <bool CACHED, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) evict_select_kernel(EvictArgs a) {
+    using Shared = SelectShared<WARPS>;
+    constexpr int kThreads = WARPS * 32;
     extern __shared__ __align__(16) unsigned char s_raw[];
-    SelectShared& s = *reinterpret_cast<SelectShared*>(s_raw);
-    uint32_t* s_keys = reinterpret_cast<uint32_t*>(s_raw + sizeof(SelectShared));
+    Shared& s = *reinterpret_cast<Shared*>(s_raw);
+    uint32_t* s_keys = reinterpret_cast<uint32_t*>(s_raw + sizeof(Shared));
     const uint32_t rank = cluster_rank(), ctas = cluster_size();
+    // with one CTA its own barrier and loads do, which are shorter
+    auto meet = [&] {
+        if (ctas > 1) cluster_sync();
+        else __syncthreads();
+    };
+    auto word_of = [&](const int* p, uint32_t r) { return ctas > 1 ? peer_word(p, r) : *p; };
     const int64_t row = blockIdx.x / ctas, b = row / a.heads, h = row % a.heads;
     const float* score = a.score + b * a.s_batch + h * a.s_head;
     int32_t* keep = a.keep + row * a.budget;
@@ -392,15 +399,15 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(EvictAr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (h == 0 && rank == 0 && threadIdx.x == 0) a.kept[b] = min(n, a.budget);
     if (n <= a.budget) {  // the whole cluster leaves here
-        for (int i = (int)rank * kSelectThreads + threadIdx.x; i < a.budget; i += (int)ctas * kSelectThreads)
+        for (int i = (int)rank * kThreads + threadIdx.x; i < a.budget; i += (int)ctas * kThreads)
             keep[i] = i < n ? i : -1;
         return;
     }
-    for (int i = threadIdx.x; i < kPasses * kDigits / 4; i += kSelectThreads)
+    for (int i = threadIdx.x; i < kPasses * kDigits / 4; i += kThreads)
         reinterpret_cast<int4*>(&s.hist[0][0])[i] = make_int4(0, 0, 0, 0);
-    const int warps = (int)ctas * kSelectWarps;
+    const int warps = (int)ctas * WARPS;
     const int per_warp = (((n + warps - 1) / warps) + kSelectStep - 1) / kSelectStep * kSelectStep;
-    const int64_t w0 = ((int64_t)rank * kSelectWarps + warp) * per_warp;
+    const int64_t w0 = ((int64_t)rank * WARPS + warp) * per_warp;
     const int lo = (int)min(w0, (int64_t)n), hi = (int)min(w0 + per_warp, (int64_t)n);
     uint32_t* mine = s_keys + warp * per_warp;
     const bool aligned = (reinterpret_cast<uintptr_t>(score) & 15) == 0;  // lo is a multiple of 4
@@ -462,12 +469,12 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(EvictAr
         }
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kCoarse / kSelectWarps; ++j) {
-            const int at = warp * (kCoarse / kSelectWarps) + j;
+        for (int j = 0; j < kCoarse / WARPS; ++j) {
+            const int at = warp * (kCoarse / WARPS) + j;
             const int c = __reduce_add_sync(0xffffffffu, s.hist[pass][at * 32 + lane]);
             if (lane == 0) s.coarse[pass][at] = c;
         }
-        cluster_sync();
+        meet();
         // first which 32 digits, then which of them, both summed over the cluster
         if (warp == 0) {
             constexpr int C = kCoarse / 32;
@@ -476,12 +483,12 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(EvictAr
             for (uint32_t r = 0; r < kMaxCluster; ++r)
                 if (r < ctas) {
 #pragma unroll
-                    for (int j = 0; j < C; ++j) c[j] += peer_word(&s.coarse[pass][kCoarse - 1 - (lane * C + j)], r);
+                    for (int j = 0; j < C; ++j) c[j] += word_of(&s.coarse[pass][kCoarse - 1 - (lane * C + j)], r);
                 }
             const int top = kCoarse - 1 - place_of(c, need, &over);
 #pragma unroll
             for (uint32_t r = 0; r < kMaxCluster; ++r)
-                if (r < ctas) f[0] += peer_word(&s.hist[pass][top * 32 + 31 - lane], r);
+                if (r < ctas) f[0] += word_of(&s.hist[pass][top * 32 + 31 - lane], r);
             const int fine = 31 - place_of(f, need - over, &more);
             if (lane == 0) s.digit = top * 32 + fine, s.over = over + more;
         }
@@ -503,23 +510,23 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(EvictAr
     if (lane == 0) s.above[warp] = above, s.equal[warp] = equal;
     __syncthreads();
     if (warp == 0) {
-        const int x = lane < kSelectWarps ? s.above[lane] : 0, y = lane < kSelectWarps ? s.equal[lane] : 0;
+        const int x = lane < WARPS ? s.above[lane] : 0, y = lane < WARPS ? s.equal[lane] : 0;
         int rx = x, ry = y;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int ux = __shfl_up_sync(0xffffffffu, rx, d), uy = __shfl_up_sync(0xffffffffu, ry, d);
             if (lane >= d) rx += ux, ry += uy;
         }
-        if (lane < kSelectWarps) s.above[lane] = rx - x, s.equal[lane] = ry - y;
+        if (lane < WARPS) s.above[lane] = rx - x, s.equal[lane] = ry - y;
         if (lane == 31) s.total[0] = rx, s.total[1] = ry;
     }
-    cluster_sync();
+    meet();
     int gone_above = s.above[warp], gone_equal = s.equal[warp];  // before this warp's part, in the row
     for (uint32_t r = 0; r < rank; ++r) {
         gone_above += peer_word(&s.total[0], r);
         gone_equal += peer_word(&s.total[1], r);
     }
-    cluster_sync();  // no CTA leaves while another reads its totals
+    if (ctas > 1) cluster_sync();  // no CTA leaves while another reads its totals
     constexpr int U = 4;  // steps whose counts are summed together, a byte each (at most 128)
     for (int i0 = lo; i0 < hi; i0 += kSelectStep * U) {
         uint4 k[U];
@@ -581,17 +588,25 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(EvictAr
 }
 
 // Shared memory of the selection for `keys` cached keys per CTA.
-static size_t select_smem(int64_t keys) { return sizeof(SelectShared) + (size_t)keys * 4; }
+template <int WARPS>
+static size_t select_smem(int64_t keys) {
+    return sizeof(SelectShared<WARPS>) + (size_t)keys * 4;
+}
 
-// Once per device: the selection kernel's shared-memory limit.
+// Entries up to which a row's CTA has 8 warps instead of 16 where there are more
+// rows than SMs: 1024 rows of 2048 entries 17 us against 29, of 4096 21 against
+// 32, but 512 of 8192 24 against 21, and 8 of 4096 9.4 against 9.0.
+constexpr int64_t kSelectShort = 4096;
+
+// Once per device: the selection kernels' shared-memory limit.
 static om_status prepare_select(const DeviceState* d) {
     static std::mutex mu;
     static bool ready[128];
     std::lock_guard<std::mutex> lk(mu);
     if (!ready[d->dev]) {
-        for (auto* kern : {evict_select_kernel<true>, evict_select_kernel<false>})
+        for (auto* kern : {evict_select_kernel<true, 16>, evict_select_kernel<false, 16>, evict_select_kernel<true, 8>})
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)select_smem(kMaxCached)) != cudaSuccess) {
+                                     (int)select_smem<16>(kMaxCached)) != cudaSuccess) {
                 cudaGetLastError();
                 return OM_ECUDA;
             }
@@ -600,18 +615,20 @@ static om_status prepare_select(const DeviceState* d) {
     return OM_OK;
 }
 
-static cudaError_t launch_select(const EvictArgs& a, int64_t rows, int sm_count, cudaStream_t st) {
-    // As many CTAs per row as fill the SMs (two CTAs each), but at least 2048 entries a CTA.
+template <int WARPS>
+static cudaError_t launch_select_warps(const EvictArgs& a, int64_t rows, int sm_count, cudaStream_t st) {
+    // As many CTAs per row as fill the SMs (two CTAs each), but at least 8192 entries
+    // a CTA: 8 rows of 16384 10.3 us, with 2048 11.5; of 4096 7.8, with 2048 9.0.
     int ctas = 1;
-    while (ctas < kMaxCluster && rows * ctas * 2 <= 2 * (int64_t)sm_count && a.length > ctas * 2048) ctas *= 2;
-    const int64_t warps = ctas * kSelectWarps;
+    while (ctas < kMaxCluster && rows * ctas * 2 <= 2 * (int64_t)sm_count && a.length > ctas * 8192) ctas *= 2;
+    const int64_t warps = ctas * WARPS;
     const int64_t per_warp = (((a.length + warps - 1) / warps) + kSelectStep - 1) / kSelectStep * kSelectStep;
-    const int64_t keys = per_warp * kSelectWarps;
+    const int64_t keys = per_warp * WARPS;
     const bool cached = keys <= kMaxCached;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * ctas));
-    cfg.blockDim = dim3(kSelectThreads);
-    cfg.dynamicSmemBytes = select_smem(cached ? keys : 0);
+    cfg.blockDim = dim3(WARPS * 32);
+    cfg.dynamicSmemBytes = select_smem<WARPS>(cached ? keys : 0);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -619,8 +636,16 @@ static cudaError_t launch_select(const EvictArgs& a, int64_t rows, int sm_count,
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto* kern = cached ? evict_select_kernel<true> : evict_select_kernel<false>;
+    auto* kern = evict_select_kernel<true, WARPS>;
+    if constexpr (WARPS == 16) {
+        if (!cached) kern = evict_select_kernel<false, WARPS>;
+    }
     return counted([&] { cudaLaunchKernelEx(&cfg, kern, a); });
+}
+
+static cudaError_t launch_select(const EvictArgs& a, int64_t rows, int sm_count, cudaStream_t st) {
+    return a.length <= kSelectShort && rows > sm_count ? launch_select_warps<8>(a, rows, sm_count, st)
+                                    : launch_select_warps<16>(a, rows, sm_count, st);
 }
 
 // --------------------------------------------------------------- gather --

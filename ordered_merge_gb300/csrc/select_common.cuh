@@ -61,9 +61,10 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-// Every thread of every CTA of the cluster; orders their shared memory.
+// Every thread of every CTA of the cluster; orders their shared memory.  Not the
+// .aligned form: nothing promises that a warp is whole where this is inlined.
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 // A word of CTA `rank`'s shared memory, at the address p has in this CTA's.
 __device__ __forceinline__ int peer_word(const int* p, uint32_t rank) {

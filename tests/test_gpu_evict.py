@@ -133,7 +133,7 @@ def test_select_long_row_and_strides(gpu):
     assert torch.equal(_select_check(gpu, view, 1000, 1, 5), gpu.evict_select(view.contiguous(), 1000, 1, 5)[0])
 
 
-@pytest.mark.parametrize("rows", [(1, 8, 40000), (40, 8, 9000), (2, 2, 200000)], ids=str)
+@pytest.mark.parametrize("rows", [(1, 8, 40000), (40, 8, 9000), (2, 2, 200000), (40, 8, 1500), (25, 8, 4096), (3, 1, 16385)], ids=str)
 def test_select_many_shapes_of_work(gpu, rows):
     """Few long rows, many short ones: whatever the work is split into."""
     score = torch.rand(rows, device="cuda") ** 8
