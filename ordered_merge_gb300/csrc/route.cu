@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(RouteArgs 
 // What bounds it is the rate of minima and maxima (half of the issue rate): a
 // token of 128 bf16 logits takes about 50 warp instructions of them and 80 in
 // all.  Measured, 131071 tokens, top 8: 128 bf16 logits 18 us (2.3 TB/s), 128
-// f32 29 us, 256 f32 sigmoid scores with bias in 8 groups 66 us, where the
+// f32 29 us, 256 f32 sigmoid scores with bias in 8 groups 71 us, where the
 // kernel above takes 87, 87 and 271 us.
 constexpr int kListThreads = 128;
 constexpr int kListPitch = kListThreads + 1;  // of the rows of choices: neighbouring rows start on other banks
@@ -382,9 +382,10 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float v = value_of(x, i);
-            // the hardware's 2^x: its error, below 2^-22 of the score, is that of ordering in 32 bits
-            if (MODE == kListSoftmax) k[i] = __expf(v - top) * inverse;
-            else if (MODE == kListSigmoid) k[i] = __fdividef(1.0f, 1.0f + __expf(-v));
+            // scores to a few units in the last place: ordered as 32 bits can order them (the
+            // hardware's 2^x alone, whose error grows with |v|, would take 7 % off the largest calls)
+            if (MODE == kListSoftmax) k[i] = expf(v - top) * inverse;
+            else if (MODE == kListSigmoid) k[i] = __fdividef(1.0f, 1.0f + expf(-v));
             else k[i] = v;
         }
         if (!BY_LOGIT && a.bias != nullptr) {
@@ -416,8 +417,8 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
         // The lanes' shares lie a line or more apart, so the row is read across the
         // lanes, and the choices handed to the lanes whose they are through shared
         // memory.  (Loads of their own shares touched 32 lines each and filled 72 %
-        // of the load path: 131071 tokens of 256 f32 took 82 us, this way 66; shares
-        // of 16 f32 52 and 53, of 32 bf16 65 both ways.)
+        // of the load path: 131071 tokens of 256 f32 took 16 us more; shares of 16
+        // f32 and of 32 bf16 gain nothing.)
         if constexpr (!PACKED) {
             const int own = share / 8;  // eights of a lane
             Eight<T> x = load_eight(row, l * 8, a.experts, aligned);
@@ -778,7 +779,7 @@ static cudaError_t launch_list_lanes(const RouteArgs& a, bool aligned, cudaStrea
 // A token gets 32 lanes (PACKED: 16) while that gives an SM at most this many
 // threads (2432 tokens): the shorter chain wins until the SMs are busy.  2048
 // biased sigmoid tokens in 8 groups of 32 experts: 5.8 us against 6.3 with
-// 8 lanes each; 4096: 7.8 against 7.6; 131071: 140 against 66.
+// 8 lanes each; 4096: 7.8 against 7.6; 131071: 140 against 71.
 constexpr int kListFewThreads = 512;
 // The most experts that 4 (grouped: twice as many for 8) lanes take, whose
 // choices then fill 36 KB of shared memory; not for PACKED, which keeps none.
