@@ -119,6 +119,7 @@ constexpr int acc_warps(bool aligned) { return aligned ? 24 : 32; }
 template <typename T, bool ALIGNED, bool DIRECT, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, acc_warps(ALIGNED) / WARPS)
     accumulate_weights_kernel(AccumulateArgs a, int log_split) {
+    wait_for_stream();
     constexpr int V = 16 / (int)sizeof(T), LANES = ALIGNED ? 32 : 31, TILE = LANES * V;
     constexpr int U = acc_unroll(ALIGNED);
     constexpr int STEP = ALIGNED ? 1 : V;  // queries between neighbours of the walk
@@ -286,10 +287,10 @@ __global__ void __launch_bounds__(WARPS * 32, acc_warps(ALIGNED) / WARPS)
 
 template <typename T, bool ALIGNED>
 static void launch_accumulate_split(const AccumulateArgs& a, dim3 grid, int log_split, bool direct, cudaStream_t st) {
-    if (ALIGNED && direct) accumulate_weights_kernel<T, ALIGNED, ALIGNED, 2><<<grid, 2 * 32, 0, st>>>(a, 0);
-    else if (log_split <= 1) accumulate_weights_kernel<T, ALIGNED, false, 2><<<grid, 2 * 32, 0, st>>>(a, log_split);
-    else if (log_split == 2) accumulate_weights_kernel<T, ALIGNED, false, 4><<<grid, 4 * 32, 0, st>>>(a, log_split);
-    else accumulate_weights_kernel<T, ALIGNED, false, 8><<<grid, 8 * 32, 0, st>>>(a, log_split);
+    if (ALIGNED && direct) launch_early(accumulate_weights_kernel<T, ALIGNED, ALIGNED, 2>, grid, 2 * 32, 0, st, a, 0);
+    else if (log_split <= 1) launch_early(accumulate_weights_kernel<T, ALIGNED, false, 2>, grid, 2 * 32, 0, st, a, log_split);
+    else if (log_split == 2) launch_early(accumulate_weights_kernel<T, ALIGNED, false, 4>, grid, 4 * 32, 0, st, a, log_split);
+    else launch_early(accumulate_weights_kernel<T, ALIGNED, false, 8>, grid, 8 * 32, 0, st, a, log_split);
 }
 
 template <typename T>
@@ -390,6 +391,7 @@ struct SelectShared {
 // take 21 us, 8 rows of 4096 8.0; the bytes alone would take 2.5 and 0.02.
 template <bool CACHED, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) evict_select_kernel(EvictArgs a) {
+    wait_for_stream();
     using Shared = SelectShared<WARPS>;
     constexpr int kThreads = WARPS * 32;
     extern __shared__ __align__(16) unsigned char s_raw[];
@@ -640,12 +642,12 @@ static cudaError_t launch_select_warps(const EvictArgs& a, int64_t rows, int sm_
     cfg.blockDim = dim3(WARPS * 32);
     cfg.dynamicSmemBytes = select_smem<WARPS>(cached ? keys : 0);
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2] = {early_attribute()};
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     auto* kern = evict_select_kernel<true, WARPS>;
     if constexpr (WARPS == 16) {
         if (!cached) kern = evict_select_kernel<false, WARPS>;
@@ -708,6 +710,7 @@ __device__ __forceinline__ void gather_tile(const GatherArgs& a, const om_cache_
 }
 
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const __grid_constant__ GatherArgs a) {
+    wait_for_stream();
     int k = a.count - 1;
     while (k > 0 && (int)blockIdx.x < a.first_cta[k]) --k;
     const int t = (int)blockIdx.x - a.first_cta[k], row = t / a.tiles[k];
@@ -877,7 +880,7 @@ om_status om_evict_gather(const int32_t* keep, int64_t batch, int64_t heads, int
         if (ctas > INT32_MAX) return OM_ERANGE;
     }
     cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = counted([&] { evict_gather_kernel<<<(unsigned)ctas, kGatherThreads, 0, st>>>(a); });
+    const cudaError_t e = counted([&] { launch_early(evict_gather_kernel, (unsigned)ctas, kGatherThreads, 0, st, a); });
     return e == cudaSuccess ? OM_OK : cuda_fail(e);
 }
 

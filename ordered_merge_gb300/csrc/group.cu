@@ -67,6 +67,7 @@ enum GroupWay {
 // BITS: of the greatest group, `groups` itself.
 template <int WAY, int BITS>
 __global__ void __launch_bounds__(kGroupThreads) group_by_id_kernel(GroupArgs a) {
+    wait_for_stream();
     extern __shared__ int s_next[];  // [warps][E]: a warp's counts, then its next place less the CTA's first
     __shared__ int s_part[kGroupWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, E = a.groups + 1;
@@ -293,17 +294,18 @@ om_status om_group_by_id(const int32_t* ids, int64_t n, int64_t groups, int32_t*
     cfg.blockDim = dim3(warps * 32);
     cfg.dynamicSmemBytes = (size_t)(warps + 2) * (groups + 1) * 4;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2] = {};
     if (way == kGroupGrid) {
         attr[0].id = cudaLaunchAttributeCooperative;
         attr[0].val.cooperative = 1;
     } else {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)ctas;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[0] = early_attribute();
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)ctas;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     }
     cfg.attrs = attr;
-    cfg.numAttrs = way == kGroupLone ? 0 : 1;
+    cfg.numAttrs = way == kGroupCluster ? 2 : 1;
     auto* kern = group_kernel<8>(way);
     if (groups >= 256) kern = group_kernel<11>(way);
     const cudaError_t e = counted([&] { cudaLaunchKernelEx(&cfg, kern, a); });

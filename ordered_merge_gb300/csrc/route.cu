@@ -40,6 +40,7 @@ __device__ __forceinline__ float sigmoid(float x) {
 // One warp per token; lane l holds the experts l, l + 32, ...
 template <typename T, int R>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(RouteArgs a) {
+    wait_for_stream();
     __shared__ float s_choice[kRouteWarps][R * 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const T* logits = static_cast<const T*>(a.logits);
@@ -330,6 +331,7 @@ enum ListMode {
 
 template <typename T, int MODE, bool GROUPED, int L>
 __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, bool aligned) {
+    wait_for_stream();
     constexpr bool PACKED = MODE == kListPacked, BY_LOGIT = MODE <= kListLogit;
     using Key = typename std::conditional<PACKED, uint32_t, float>::type;
     constexpr unsigned kAll = 0xffffffffu;
@@ -661,6 +663,7 @@ struct RouteBackArgs {
 // which 2.2 are those of a single token.
 template <typename T, bool DENSE, int L>
 __global__ void __launch_bounds__(128) route_topk_backward_kernel(RouteBackArgs a, bool aligned_in, bool aligned_out) {
+    wait_for_stream();
     constexpr unsigned kAll = 0xffffffffu;
     const float kNone = -INFINITY;
     const int l = threadIdx.x & (L - 1);
@@ -772,7 +775,7 @@ static cudaError_t launch_list_lanes(const RouteArgs& a, bool aligned, cudaStrea
     const int steps = (a.experts + 8 * L - 1) / (8 * L);
     const size_t smem = MODE == kListPacked ? 0 : (size_t)steps * (2 * kListPitch * sizeof(float4) + kListThreads * sizeof(float));
     return counted([&] {
-        route_list_kernel<T, MODE, GROUPED, L><<<(unsigned)blocks, kListThreads, smem, st>>>(a, aligned);
+        launch_early(route_list_kernel<T, MODE, GROUPED, L>, (unsigned)blocks, kListThreads, smem, st, a, aligned);
     });
 }
 
@@ -810,7 +813,7 @@ static cudaError_t launch_list(const RouteArgs& a, bool aligned, bool few, cudaS
 template <typename T, bool DENSE, int L>
 static void launch_back_lanes(const RouteBackArgs& a, bool in, bool out, cudaStream_t st) {
     const unsigned blocks = (unsigned)((a.tokens * L + 127) / 128);
-    route_topk_backward_kernel<T, DENSE, L><<<blocks, 128, 0, st>>>(a, in, out);
+    launch_early(route_topk_backward_kernel<T, DENSE, L>, blocks, 128, 0, st, a, in, out);
 }
 
 // 8 lanes a token, or 32: where there are more picks than 8, and in DENSE where
@@ -889,7 +892,7 @@ om_status om_route_topk(int value_type, const void* logits, int64_t tokens, int6
     const cudaError_t e = with_value_type(value_type, [&](auto v) {
         return with_lane_experts((int)experts, [&](auto r) {
             return counted([&] {
-                route_topk_kernel<decltype(v), decltype(r)::value><<<route_grid(tokens), kRouteWarps * 32, 0, st>>>(a);
+                launch_early(route_topk_kernel<decltype(v), decltype(r)::value>, route_grid(tokens), kRouteWarps * 32, 0, st, a);
             });
         });
     });

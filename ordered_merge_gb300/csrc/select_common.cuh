@@ -83,6 +83,38 @@ cudaError_t counted(F&& launch) {
     return trace_end(TraceRec{0, nullptr, nullptr}, false, nullptr);
 }
 
+// ---- launches that overlap the end of the stream's work
+//
+// A kernel launched by launch_early may be given to the SMs while the kernel
+// before it in the stream still drains; wait_for_stream, its first statement,
+// holds it back until that one has ended and its writes are visible.  Then it
+// lets the next such kernel come, which waits in its turn.
+
+__device__ __forceinline__ void wait_for_stream() {
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The attribute of such a launch.
+inline cudaLaunchAttribute early_attribute() {
+    cudaLaunchAttribute a = {};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    return a;
+}
+
+template <typename... Ps, typename... As>
+void launch_early(void (*kern)(Ps...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, As... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = early_attribute();
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 inline int value_bytes(int value_type) {
     switch (value_type) {
         case OM_VALUE_F32: return 4;
