@@ -877,11 +877,14 @@ om_status om_route_topk(int value_type, const void* logits, int64_t tokens, int6
     const om_status ds = device_state(&d);
     if (ds != OM_OK) return ds;
     const bool packed = vb == 2 && bias == nullptr && (groups == 1 || group_best == 1);
-    const bool few = tokens * 32 <= d->sm_count * (int64_t)kListFewThreads ||
-                     (!packed && experts > kListMaxExperts * (groups == 1 ? 1 : 2));
+    // grouped: a lane's share of a row has to lie in one group
+    auto fits = [&](int lanes) { return groups == 1 || (lanes % groups == 0 && experts % lanes == 0); };
+    const bool most = packed || experts <= kListMaxExperts * (groups == 1 ? 1 : 2);  // 4 or 8 lanes can
+    bool few = tokens * 32 <= d->sm_count * (int64_t)kListFewThreads || !most;
+    // the other number of lanes where only that one fits: still half the time of a warp reduction per pick
+    if (!fits(few ? 32 : 8) && fits(few ? 8 : 32) && (!few || most)) few = !few;
     const int lanes = few ? 32 : 8;
-    // grouped: a lane's share of a row lies in one group
-    if (top_k <= 8 && (groups == 1 || (lanes % groups == 0 && experts % lanes == 0))) {
+    if (top_k <= 8 && fits(lanes)) {
         bool aligned = !misaligned(logits, 16) && (tokens == 1 || row_stride * vb % 16 == 0);
         if (groups > 1) aligned = aligned && experts / lanes * vb % 16 == 0;
         const cudaError_t e = with_value_type(value_type, [&](auto v) {

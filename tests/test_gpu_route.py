@@ -72,6 +72,7 @@ SHAPES = [  # tokens, experts, k, groups, picks, best
     (2, 513, 1, 1, 1, 1), (300, 48, 5, 3, 2, 2), (2, 12, 3, 12, 3, 2),
     (17, 128, 4, 2, 1, 1), (9, 192, 6, 4, 2, 2), (5, 1024, 8, 8, 2, 1), (40, 64, 3, 8, 5, 2), (6, 320, 7, 1, 1, 1),
     (11, 1000, 8, 1, 1, 1),
+    (21, 72, 4, 4, 2, 2), (7, 200, 8, 2, 1, 2), (6, 96, 6, 16, 4, 2), (5, 256, 8, 32, 8, 1), (4, 640, 8, 8, 2, 2),
 ]
 
 
@@ -261,7 +262,8 @@ def _route_all(x, k, score, bias, groups, picks, best, renorm, scale):
 
 @pytest.mark.parametrize("shape", [(64, 6, 1, 1, 1), (128, 8, 1, 1, 1), (160, 8, 8, 3, 2), (256, 8, 8, 4, 2), (256, 8, 8, 4, 1),
                                    (256, 5, 2, 1, 2), (257, 3, 1, 1, 1), (512, 8, 4, 2, 2), (72, 8, 4, 3, 2), (40, 1, 1, 1, 1),
-                                   (96, 12, 1, 1, 1)], ids=str)
+                                   (96, 12, 1, 1, 1), (96, 6, 16, 4, 2), (256, 8, 32, 8, 1), (200, 8, 4, 2, 2), (90, 5, 3, 2, 2)],
+                         ids=str)
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_route_many_tokens(gpu, shape, score, dtype):
