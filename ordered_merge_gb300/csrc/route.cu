@@ -149,12 +149,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(RouteArgs 
 
 // ---------------------------------------------------- sorted-list kernel --
 //
-// For top_k <= 8.  L lanes share a token (32 / L tokens a warp).  A lane takes
+// For top_k <= 16.  L lanes share a token (32 / L tokens a warp).  A lane takes
 // its share of the row eight experts at a time: it sorts the eight by a fixed
-// network and merges them into its sorted list of the best eight (the greater
-// of a[i] and b[7 - i] for every i are the best eight of both, and bitonic, so
-// three more steps sort them).  The lanes' lists are merged the same way across
-// the lanes, log2(L) times, after which each of them has the token's best eight.
+// network and merges them into its sorted list of the best LIST, 8 or 16 (with
+// 8, the greater of a[i] and b[7 - i] for every i are the best eight of both, and
+// bitonic, so three more steps sort them).  The lanes' lists are merged the same
+// way across the lanes, log2(L) times, after which each of them has the token's
+// best.
 // Nothing but minima and maxima of independent pairs, no turn through memory,
 // and no warp reduction per pick.
 //
@@ -193,13 +194,13 @@ __device__ __forceinline__ void order_pair(K& hi, K& lo) {
     lo = lesser(a, b);
 }
 
-// Greatest first; a bitonic sequence of eight.
-template <typename K>
-__device__ __forceinline__ void sort_bitonic8(K (&k)[8]) {
+// Greatest first; a bitonic sequence.
+template <typename K, int N>
+__device__ __forceinline__ void sort_bitonic(K (&k)[N]) {
 #pragma unroll
-    for (int d = 4; d > 0; d >>= 1)
+    for (int d = N / 2; d > 0; d >>= 1)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < N; ++i)
             if ((i & d) == 0) order_pair(k[i], k[i + d]);
 }
 
@@ -214,11 +215,12 @@ __device__ __forceinline__ void sort8(K (&k)[8]) {
     order_pair(k[1], k[2]), order_pair(k[3], k[4]), order_pair(k[5], k[6]);
 }
 
-template <typename K>
-__device__ __forceinline__ void merge_best8(K (&a)[8], const K (&b)[8]) {
+// The best N of a's N and b's M, both greatest first.
+template <typename K, int N, int M>
+__device__ __forceinline__ void merge_best(K (&a)[N], const K (&b)[M]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = greater(a[i], b[7 - i]);
-    sort_bitonic8(a);
+    for (int i = 0; i < M; ++i) a[N - M + i] = greater(a[N - M + i], b[M - 1 - i]);
+    sort_bitonic(a);
 }
 
 // Eight values of a row from e on; those at or past the end are -inf.
@@ -329,7 +331,7 @@ enum ListMode {
     kListSigmoid   // sigmoid scores, likewise
 };
 
-template <typename T, int MODE, bool GROUPED, int L>
+template <typename T, int MODE, bool GROUPED, int L, int LIST>
 __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, bool aligned) {
     wait_for_stream();
     constexpr bool PACKED = MODE == kListPacked, BY_LOGIT = MODE <= kListLogit;
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
     constexpr unsigned kAll = 0xffffffffu;
     const float kNone = -INFINITY;
     extern __shared__ float4 s_choice[];       // [steps][2][kListPitch]: a lane's eights; [steps]: their greatest
-    __shared__ int s_id[kListThreads / L][8];  // the picks of a token
+    __shared__ int s_id[kListThreads / L][LIST];  // the picks of a token
     const int l = threadIdx.x & (L - 1), slot = threadIdx.x / L;
     const int64_t t = (int64_t)blockIdx.x * (kListThreads / L) + slot;
     const bool live = t < a.tokens;
@@ -376,9 +378,9 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
         inverse = 1.0f / sum;
     }
 
-    Key best[8];
+    Key best[LIST];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) best[i] = PACKED ? Key(0) : Key(kNone);
+    for (int i = 0; i < LIST; ++i) best[i] = PACKED ? Key(0) : Key(kNone);
     // what the eight experts from e on, with logits x, are chosen by; -inf where masked, and no -0
     auto choose = [&](const Eight<T>& x, int e, int end, float (&k)[8]) {
 #pragma unroll
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
         sort8(k);
         if constexpr (!PACKED) s_greatest[step * kListThreads + threadIdx.x] = k[0];
         if (step > 0) {
-            merge_best8(best, k);
+            merge_best(best, k);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) best[i] = k[i];
@@ -493,15 +495,15 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
         }
         open = ahead < a.group_picks;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < LIST; ++i)
             if (!open) best[i] = PACKED ? Key(0) : Key(kNone);
     }
 #pragma unroll 1
     for (int d = 1; d < L; d <<= 1) {
-        Key other[8];
+        Key other[LIST];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(kAll, best[i], d);
-        merge_best8(best, other);
+        for (int i = 0; i < LIST; ++i) other[i] = __shfl_xor_sync(kAll, best[i], d);
+        merge_best(best, other);
     }
 
     if constexpr (!PACKED) {
@@ -509,13 +511,13 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
         int valid = 0, twins = 0;  // listed values that are there; neighbours that are equal
         float least = -3.402823466e38f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < LIST; ++i) {
             if (i < a.top_k && best[i] > kNone) ++valid, least = best[i];
             if (i > 0 && i < a.top_k && best[i] > kNone) twins += best[i] == best[i - 1];
         }
 #pragma unroll
-        for (int i = 0; i < 8; i += L)
-            if (l + i < 8) s_id[slot][l + i] = -1;
+        for (int i = 0; i < LIST; i += L)
+            if (l + i < LIST) s_id[slot][l + i] = -1;
         __syncwarp();
         uint32_t eights = 0;  // of this lane, that reach the least chosen value
         for (int step = 0; step < steps; ++step)
@@ -535,8 +537,8 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
                 const float mine = reinterpret_cast<const float*>(two + (i >> 2) * kListPitch)[i & 3];
                 int place = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) place += best[j] > mine;
-                s_id[slot][place & 7] = first_of(step) + i;
+                for (int j = 0; j < LIST; ++j) place += best[j] > mine;
+                s_id[slot][place & (LIST - 1)] = first_of(step) + i;
             }
         }
         __syncwarp();
@@ -548,10 +550,10 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
             int before = -1;
             float last = INFINITY;
 #pragma unroll 1
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < LIST; ++j) {
                 float v = kNone;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < LIST; ++i)
                     if (i == j) v = best[i];
                 if (v != last) before = -1;
                 int lowest = 0x7fffffff;
@@ -578,7 +580,7 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
     }
 
     // lane l finishes the picks l * P ..
-    constexpr int P = L < 8 ? 8 / L : 1;
+    constexpr int P = L < LIST ? LIST / L : 1;
     int id[P];
     float px[P], w[P];
     float head = kNone;  // the picks' greatest logit
@@ -588,7 +590,7 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
         if constexpr (PACKED) {
             Key k = 0;
 #pragma unroll
-            for (int i = 0; i < 8 / P; ++i)
+            for (int i = 0; i < LIST / P; ++i)
                 if (l == i) k = best[i * P + p];
             px[p] = logit_of(k, T{});
             there = there && px[p] > kNone;
@@ -769,13 +771,15 @@ static cudaError_t with_lane_experts(int experts, F&& f) {
     return f(std::integral_constant<int, 32>{});
 }
 
-template <typename T, int MODE, bool GROUPED, int L>
+template <typename T, int MODE, bool GROUPED, int L, int LIST>
 static cudaError_t launch_list_lanes(const RouteArgs& a, bool aligned, cudaStream_t st) {
     const int64_t blocks = (a.tokens + kListThreads / L - 1) / (kListThreads / L);
     const int steps = (a.experts + 8 * L - 1) / (8 * L);
-    const size_t smem = MODE == kListPacked ? 0 : (size_t)steps * (2 * kListPitch * sizeof(float4) + kListThreads * sizeof(float));
+    const size_t smem =
+        MODE == kListPacked ? 0 : (size_t)steps * (2 * kListPitch * sizeof(float4) + kListThreads * sizeof(float));
     return counted([&] {
-        launch_early(route_list_kernel<T, MODE, GROUPED, L>, (unsigned)blocks, kListThreads, smem, st, a, aligned);
+        launch_early(route_list_kernel<T, MODE, GROUPED, L, LIST>, (unsigned)blocks, kListThreads, smem, st, a,
+                     aligned);
     });
 }
 
@@ -785,17 +789,20 @@ static cudaError_t launch_list_lanes(const RouteArgs& a, bool aligned, cudaStrea
 // 8 lanes each; 4096: 7.8 against 7.6; 131071: 140 against 71.
 constexpr int kListFewThreads = 512;
 // The most experts that 4 (grouped: twice as many for 8) lanes take, whose
-// choices then fill 36 KB of shared memory; not for PACKED, which keeps none.
+// choices then fill 37 KB of shared memory; not for PACKED, which keeps none.
 constexpr int kListMaxExperts = 256;
 
 template <typename T, int MODE>
 static cudaError_t launch_list_mode(const RouteArgs& a, bool aligned, bool few, cudaStream_t st) {
     constexpr int kMore = MODE == kListPacked ? 16 : 32;
+    if (a.top_k > 8)
+        return a.groups == 1 ? launch_list_lanes<T, MODE, false, 8, 16>(a, aligned, st)
+                             : launch_list_lanes<T, MODE, true, 8, 16>(a, aligned, st);
     if (a.groups == 1)
-        return few ? launch_list_lanes<T, MODE, false, kMore>(a, aligned, st)
-                   : launch_list_lanes<T, MODE, false, 4>(a, aligned, st);
-    return few ? launch_list_lanes<T, MODE, true, 32>(a, aligned, st)
-               : launch_list_lanes<T, MODE, true, 8>(a, aligned, st);
+        return few ? launch_list_lanes<T, MODE, false, kMore, 8>(a, aligned, st)
+                   : launch_list_lanes<T, MODE, false, 4, 8>(a, aligned, st);
+    return few ? launch_list_lanes<T, MODE, true, 32, 8>(a, aligned, st)
+               : launch_list_lanes<T, MODE, true, 8, 8>(a, aligned, st);
 }
 
 template <typename T>
@@ -879,12 +886,21 @@ om_status om_route_topk(int value_type, const void* logits, int64_t tokens, int6
     const bool packed = vb == 2 && bias == nullptr && (groups == 1 || group_best == 1);
     // grouped: a lane's share of a row has to lie in one group
     auto fits = [&](int lanes) { return groups == 1 || (lanes % groups == 0 && experts % lanes == 0); };
-    const bool most = packed || experts <= kListMaxExperts * (groups == 1 ? 1 : 2);  // 4 or 8 lanes can
-    bool few = tokens * 32 <= d->sm_count * (int64_t)kListFewThreads || !most;
-    // the other number of lanes where only that one fits: still half the time of a warp reduction per pick
-    if (!fits(few ? 32 : 8) && fits(few ? 8 : 32) && (!few || most)) few = !few;
-    const int lanes = few ? 32 : 8;
-    if (top_k <= 8 && fits(lanes)) {
+    const bool room = packed || experts <= kListMaxExperts * (groups == 1 && top_k <= 8 ? 1 : 2);  // for 4 or 8 lanes
+    const bool some = tokens * 32 <= d->sm_count * (int64_t)kListFewThreads;
+    bool listed, few = false;
+    if (top_k <= 8) {
+        few = some || !room;
+        // the other number of lanes where only that one fits: still half the time of a warp reduction per pick
+        if (!fits(few ? 32 : 8) && fits(few ? 8 : 32) && (!few || room)) few = !few;
+        listed = fits(few ? 32 : 8);
+    } else {
+        // 8 lanes and lists of 16; a few tokens' f32 logits are as well off with a warp each (512 of 128, top 10:
+        // 3.6 us against 4.9; of 256 with bias, top 12: 10.7 against 8.4; 131071 of 160 bf16, top 16: 225 against 42)
+        listed = top_k <= 16 && room && fits(8) && !(some && vb == 4 && bias == nullptr && groups == 1);
+    }
+    if (listed) {
+        const int lanes = few ? 32 : 8;
         bool aligned = !misaligned(logits, 16) && (tokens == 1 || row_stride * vb % 16 == 0);
         if (groups > 1) aligned = aligned && experts / lanes * vb % 16 == 0;
         const cudaError_t e = with_value_type(value_type, [&](auto v) {

@@ -262,7 +262,8 @@ def _route_all(x, k, score, bias, groups, picks, best, renorm, scale):
 
 @pytest.mark.parametrize("shape", [(64, 6, 1, 1, 1), (128, 8, 1, 1, 1), (160, 8, 8, 3, 2), (256, 8, 8, 4, 2), (256, 8, 8, 4, 1),
                                    (256, 5, 2, 1, 2), (257, 3, 1, 1, 1), (512, 8, 4, 2, 2), (72, 8, 4, 3, 2), (40, 1, 1, 1, 1),
-                                   (96, 12, 1, 1, 1), (96, 6, 16, 4, 2), (256, 8, 32, 8, 1), (200, 8, 4, 2, 2), (90, 5, 3, 2, 2)],
+                                   (96, 12, 1, 1, 1), (96, 6, 16, 4, 2), (256, 8, 32, 8, 1), (200, 8, 4, 2, 2), (90, 5, 3, 2, 2),
+                                   (160, 16, 1, 1, 1), (256, 12, 8, 4, 2), (512, 9, 4, 3, 1), (67, 13, 1, 1, 1), (16, 16, 2, 2, 1)],
                          ids=str)
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
@@ -283,7 +284,8 @@ def test_route_many_tokens(gpu, shape, score, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("experts,groups,picks", [(64, 1, 1), (130, 1, 1), (256, 8, 3)])
-def test_route_many_tokens_ties_and_masks(gpu, dtype, experts, groups, picks):
+@pytest.mark.parametrize("k", [8, 15])
+def test_route_many_tokens_ties_and_masks(gpu, dtype, experts, groups, picks, k):
     """A few values only, so most choices tie; some rows and experts masked."""
     rng = np.random.default_rng(experts)
     x = torch.from_numpy(rng.integers(-2, 2, (MANY, experts))).to(DTYPES[dtype])
@@ -293,9 +295,9 @@ def test_route_many_tokens_ties_and_masks(gpu, dtype, experts, groups, picks):
     x[MANY - 1, 3:] = -float("inf")
     for score in ("softmax", "sigmoid"):
         for bias in (None, torch.zeros(experts, device="cuda")):
-            ids, w = gpu.route_topk(x.cuda(), 8, score=score, bias=bias, groups=groups, group_picks=picks, renorm=True)
+            ids, w = gpu.route_topk(x.cuda(), k, score=score, bias=bias, groups=groups, group_picks=picks, renorm=True)
             rows = [*range(0, MANY, 97), 5, 13, 16, MANY - 1]
-            want_ids, want_w = ref.route(f64(x[rows]), 8, score, None if bias is None else f64(bias), groups, picks, 1, True)
+            want_ids, want_w = ref.route(f64(x[rows]), k, score, None if bias is None else f64(bias), groups, picks, 1, True)
             assert np.array_equal(ids.cpu().numpy()[rows], want_ids)
             assert np.all(np.abs(f64(w)[rows] - want_w) <= WEIGHT_TOL * want_w)
 
