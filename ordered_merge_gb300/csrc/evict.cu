@@ -113,9 +113,9 @@ constexpr int acc_warps(bool aligned) { return aligned ? 24 : 32; }
 // themselves, with no turn through shared memory.
 //
 // Bound by memory: every weight is read once.  64 x 8 cache heads of 8192 bf16
-// entries, eight query heads each (90 MB): 14.6 us a pass, 91 % of the copy rate;
+// entries, eight query heads each (90 MB): 13.2 us a pass, the copy rate;
 // 8 cache heads of 65539 f16 entries, 128 rows each, on odd addresses (138 MB):
-// 27.8 us, where each 16-byte vector of a warp also costs 67 instructions.
+// 25.9 us, where each 16-byte vector of a warp also costs 67 instructions.
 template <typename T, bool ALIGNED, bool DIRECT, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, acc_warps(ALIGNED) / WARPS)
     accumulate_weights_kernel(AccumulateArgs a, int log_split) {

@@ -175,10 +175,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(RouteArgs 
 // taken from their heads, and the lists of groups not picked are dropped.
 
 // What bounds it is the rate of minima and maxima (half of the issue rate): a
-// token of 128 bf16 logits takes about 50 warp instructions of them and 80 in
-// all.  Measured, 131071 tokens, top 8: 128 bf16 logits 18 us (2.3 TB/s), 128
+// token of 128 bf16 logits takes about 40 warp instructions of them and 94 in
+// all, 64 of them in that pipe.  Measured, 131071 tokens, top 8: 128 bf16 logits 18 us (2.3 TB/s), 128
 // f32 29 us, 256 f32 sigmoid scores with bias in 8 groups 71 us, where the
-// kernel above takes 87, 87 and 271 us.
+// kernel above takes 87, 87 and 271 us; top 16 of 160 bf16 42 us against 225.
 constexpr int kListThreads = 128;
 constexpr int kListPitch = kListThreads + 1;  // of the rows of choices: neighbouring rows start on other banks
 
