@@ -63,10 +63,9 @@ class BoundedCache:
     def evict(self):
         score = self.score[:, :, :self.used]
         keep, kept = om.evict_select(score, self.budget, self.first, self.last, self.lengths)
-        moved = om.evict_gather(keep, (self.keys[:, :, :self.used], self.values[:, :, :self.used], score))
+        arrays = [x[:, :, :self.used] for x in (self.keys, self.values, self.score)]
         self.used = min(self.used, self.budget)
-        for mine, new in zip((self.keys, self.values, self.score), moved):
-            mine[:, :, :self.used] = new[:, :, :self.used]
+        om.evict_gather(keep, arrays, out=[x[:, :, :self.budget] for x in (self.keys, self.values, self.score)])
         self.lengths = kept
 
 

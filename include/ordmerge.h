@@ -452,8 +452,12 @@ typedef struct {
  * for j < budget, zero bytes where keep is outside [0, length).  `arrays` is
  * a host array, read before the call returns.  No dst may overlap a src,
  * another dst or keep (compared by the span from the first to the last entry),
- * nor share bytes between its own entries.  Vectors of 16 bytes where every
- * address allows them.  Entry strides are at most 2^30 bytes, others 2^40.
+ * nor share bytes between its own entries.
+ * In place: all arrays together may have dst = src, with the same strides;
+ * keep has to rise then, as om_evict_select's does (values are lost
+ * otherwise), and entries past the budget keep what they held.
+ * Vectors of 16 bytes where every address allows them.  Entry strides are at
+ * most 2^30 bytes, others 2^40.
  */
 om_status om_evict_gather(const int32_t *keep, int64_t batch, int64_t heads,
                           int64_t budget, int64_t length,

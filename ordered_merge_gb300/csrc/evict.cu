@@ -723,6 +723,84 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const __gr
     }
 }
 
+// ---- in place
+//
+// keep rises, so entry j comes from entry keep[j] >= j: a CTA, or a cluster of
+// them, that walks a row from its start, storing a chunk only when all of it has
+// been loaded, never overwrites what a later chunk needs, and may load the next
+// chunk meanwhile.  Where there are few rows, entries are cut into `slices`
+// columns of at least 64 bytes, and clusters of up to 8 CTAs take a column's
+// chunks together.  An entry that stays where it is is not touched.
+//
+// Bound by the meetings between loading and storing, on cold inputs: 32 rows of
+// 16384 kept of 131072 entries (keys and values of 256 bytes, a score) 142 us,
+// 2 rows of 65536 72 us (369 with one CTA to a column).  Into other memory these
+// take 93 and 29 us, before anything is brought back.
+
+constexpr int kInPlaceThreads = 512;
+
+template <typename V>
+__device__ __forceinline__ void gather_row_in_place(const GatherArgs& a, const om_cache_array& c, int64_t row,
+                                                    int slice, int slices) {
+    constexpr int U = kGatherUnroll;
+    const unsigned per = (unsigned)(c.entry_bytes / (int)sizeof(V)) / (unsigned)slices;  // vectors of an entry here
+    const int64_t b = row / a.heads, h = row % a.heads;
+    char* base = static_cast<char*>(c.dst) + b * c.dst_batch + h * c.dst_head + (int64_t)slice * per * sizeof(V);
+    const int32_t* keep = a.keep + row * a.budget;
+    const unsigned total = (unsigned)a.budget * per, ctas = cluster_size();
+    const unsigned first = cluster_rank() * kInPlaceThreads + threadIdx.x, stride = ctas * kInPlaceThreads;
+    struct Chunk {
+        V v[U];
+        int64_t to[U];
+    };
+    auto load = [&](unsigned i0, Chunk& x) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const unsigned i = i0 + u * stride + first;
+            x.v[u] = V{};
+            x.to[u] = -1;
+            if (i < total) {
+                const unsigned j = i / per, piece = (i - j * per) * (unsigned)sizeof(V);
+                const int32_t from = __ldg(keep + j);
+                if (from != (int32_t)j) {
+                    x.to[u] = j * c.dst_entry + piece;
+                    if (from >= 0 && from < a.length)
+                        x.v[u] = *reinterpret_cast<const V*>(base + from * c.dst_entry + piece);
+                }
+            }
+        }
+    };
+    Chunk now, next;
+    load(0, now);
+    for (unsigned i0 = 0; i0 < total; i0 += U * stride) {
+        const bool more = total - i0 > U * stride;
+        if (more) load(i0 + U * stride, next);
+        // the whole of `now` has been loaded
+        if (ctas > 1) cluster_sync();
+        else __syncthreads();
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (now.to[u] >= 0) *reinterpret_cast<V*>(base + now.to[u]) = now.v[u];
+        if (more) now = next;
+        else break;
+    }
+}
+
+// first_cta, tiles: as for the other kernel, for clusters, a tile being a slice of a row.
+__global__ void __launch_bounds__(kInPlaceThreads) evict_gather_in_place_kernel(const __grid_constant__ GatherArgs a) {
+    wait_for_stream();
+    const int cluster = (int)(blockIdx.x / cluster_size());
+    int k = a.count - 1;
+    while (k > 0 && cluster < a.first_cta[k]) --k;
+    const int t = cluster - a.first_cta[k], row = t / a.tiles[k], slice = t - row * a.tiles[k];
+    switch (a.vector[k]) {
+        case 16: gather_row_in_place<uint4>(a, a.arrays[k], row, slice, a.tiles[k]); break;
+        case 4: gather_row_in_place<uint32_t>(a, a.arrays[k], row, slice, a.tiles[k]); break;
+        case 2: gather_row_in_place<unsigned short>(a, a.arrays[k], row, slice, a.tiles[k]); break;
+        default: gather_row_in_place<unsigned char>(a, a.arrays[k], row, slice, a.tiles[k]); break;
+    }
+}
+
 // Bytes of the vectors that every address of the array allows.
 static int gather_vector(const om_cache_array& c) {
     const uint64_t low = reinterpret_cast<uintptr_t>(c.src) | reinterpret_cast<uintptr_t>(c.dst) |
@@ -838,6 +916,7 @@ om_status om_evict_gather(const int32_t* keep, int64_t batch, int64_t heads, int
     GatherArgs a{};
     const int64_t slots = batch * heads * budget;
     int64_t spans[kMaxArrays], src_spans[kMaxArrays];
+    int in_place = 0;
     for (int i = 0; i < count; ++i) {
         const om_cache_array& c = arrays[i];
         if (c.entry_bytes < 1 || c.dst == nullptr || (length > 0 && c.src == nullptr)) return OM_EINVAL;
@@ -847,18 +926,23 @@ om_status om_evict_gather(const int32_t* keep, int64_t batch, int64_t heads, int
         if (c.src_batch > kMaxStride || c.src_head > kMaxStride || c.dst_batch > kMaxStride ||
             c.dst_head > kMaxStride || c.src_entry > kMaxEntryStride || c.dst_entry > kMaxEntryStride)
             return OM_ERANGE;
-        bool shared = false, ignored = false;
+        bool shared = false, src_shared = false;
         spans[i] = strided_span(c.entry_bytes, {batch, heads, budget}, {c.dst_batch, c.dst_head, c.dst_entry}, &shared);
         if (shared) return OM_EINVAL;
         src_spans[i] = length > 0 ? strided_span(c.entry_bytes, {batch, heads, length},
-                                                 {c.src_batch, c.src_head, c.src_entry}, &ignored)
+                                                 {c.src_batch, c.src_head, c.src_entry}, &src_shared)
                                   : 0;
         if (overlaps(c.dst, spans[i], keep, slots * 4, 1)) return OM_EINVAL;
+        if (c.src == c.dst && c.src_batch == c.dst_batch && c.src_head == c.dst_head && c.src_entry == c.dst_entry) {
+            if (src_shared) return OM_EINVAL;  // rows would write into each other's entries
+            ++in_place;
+        }
         a.arrays[i] = c;
     }
+    if (in_place != 0 && in_place != count) return OM_EINVAL;
     for (int i = 0; i < count; ++i)
         for (int j = 0; j < count; ++j)
-            if (overlaps(a.arrays[i].dst, spans[i], a.arrays[j].src, src_spans[j], 1) ||
+            if ((!(in_place && i == j) && overlaps(a.arrays[i].dst, spans[i], a.arrays[j].src, src_spans[j], 1)) ||
                 (i < j && overlaps(a.arrays[i].dst, spans[i], a.arrays[j].dst, spans[j], 1)))
                 return OM_EINVAL;
     a.keep = keep;
@@ -866,21 +950,54 @@ om_status om_evict_gather(const int32_t* keep, int64_t batch, int64_t heads, int
     a.budget = (int)budget;
     a.heads = (int)heads;
     a.count = count;
+    DeviceState* d = nullptr;
+    const om_status s = device_state(&d);
+    if (s != OM_OK) return s;
     int64_t ctas = 0;
     for (int i = 0; i < count; ++i) {
-        // tiles of about kGatherUnroll vectors per thread
         a.vector[i] = gather_vector(a.arrays[i]);
         const int64_t per = a.arrays[i].entry_bytes / a.vector[i];
-        int64_t entries = kGatherThreads * kGatherUnroll / per;
-        if (entries < 1) entries = 1;
-        a.tile_entries[i] = (int)entries;
-        a.tiles[i] = (int)((budget + entries - 1) / entries);
+        if (in_place) {
+            // columns of at least 64 bytes until there are two CTAs an SM
+            int64_t slices = 1;
+            while (batch * heads * count * slices < 2 * d->sm_count && per % (2 * slices) == 0 &&
+                   per / (2 * slices) * a.vector[i] >= 64)
+                slices *= 2;
+            if (budget * per / slices > INT32_MAX) return OM_ERANGE;  // with a chunk more still 32 bits
+            a.tiles[i] = (int)slices;
+        } else {
+            // tiles of about kGatherUnroll vectors per thread
+            int64_t entries = kGatherThreads * kGatherUnroll / per;
+            if (entries < 1) entries = 1;
+            a.tile_entries[i] = (int)entries;
+            a.tiles[i] = (int)((budget + entries - 1) / entries);
+        }
         a.first_cta[i] = (int)ctas;
         ctas += batch * heads * a.tiles[i];
         if (ctas > INT32_MAX) return OM_ERANGE;
     }
     cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = counted([&] { launch_early(evict_gather_kernel, (unsigned)ctas, kGatherThreads, 0, st, a); });
+    unsigned cluster = 1;  // in place: CTAs to each column of a row
+    while (in_place && cluster < kMaxCluster && ctas * cluster * 2 <= 2 * d->sm_count &&
+           budget > (int64_t)cluster * kInPlaceThreads)
+        cluster *= 2;
+    const cudaError_t e = counted([&] {
+        if (!in_place) {
+            launch_early(evict_gather_kernel, (unsigned)ctas, kGatherThreads, 0, st, a);
+            return;
+        }
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)ctas * cluster);
+        cfg.blockDim = dim3(kInPlaceThreads);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2] = {early_attribute()};
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        cudaLaunchKernelEx(&cfg, evict_gather_in_place_kernel, a);
+    });
     return e == cudaSuccess ? OM_OK : cuda_fail(e);
 }
 

@@ -203,3 +203,36 @@ def test_select_then_gather_on_another_stream(gpu):
     got, = gpu.evict_gather(k2, (mine,), stream=side)
     side.synchronize()
     assert torch.equal(k2, keep) and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("rows", [(1, 2), (3, 5), (40, 8)], ids=str)
+@pytest.mark.parametrize("width,dtype", [(128, torch.bfloat16), (80, torch.float16), (64, torch.uint8), (3, torch.float32),
+                                         (1, torch.uint8), (576, torch.float32)])
+def test_gather_in_place(gpu, rows, width, dtype):
+    """The first budget entries of the arrays themselves: what a copy would hold, and the rest as it was."""
+    b, h = rows
+    s, n = (900, 333) if b * h > 100 else (7001, 3000)
+    gen = torch.Generator(device="cuda").manual_seed(width)
+    cache = torch.randint(0, 100, (2, b, h, s + 3, width), generator=gen, device="cuda").to(dtype)
+    keys, values = cache[0][:, :, :s], cache[1][:, :, 2:2 + s]
+    score = torch.rand(b, h, s, generator=gen, device="cuda")
+    lengths = torch.tensor([[s, n - 40, n + 1][i % 3] for i in range(b)], dtype=torch.int32, device="cuda")
+    keep, _ = gpu.evict_select(score, n, 5, 17, lengths)
+    want = [_gather_plain(keep, x) for x in (keys, values, score)]
+    rest = [x[:, :, n:].clone() for x in (keys, values, score)]
+    edge = cache[1][:, :, :2].clone(), cache[0][:, :, s:].clone()
+    gpu.evict_gather(keep, (keys, values, score), out=tuple(x[:, :, :n] for x in (keys, values, score)))
+    for x, w, r in zip((keys, values, score), want, rest):
+        assert torch.equal(x[:, :, :n], w) and torch.equal(x[:, :, n:], r)
+    assert torch.equal(cache[1][:, :, :2], edge[0]) and torch.equal(cache[0][:, :, s:], edge[1])
+
+
+def test_gather_in_place_of_the_whole_cache(gpu):
+    """Nothing moves, or everything by one."""
+    x = torch.randn(2, 3, 5000, 64, device="cuda")
+    was = x.clone()
+    same = torch.arange(5000, dtype=torch.int32, device="cuda").expand(2, 3, 5000).contiguous()
+    gpu.evict_gather(same, (x,), out=(x,))
+    assert torch.equal(x, was)
+    gpu.evict_gather(torch.where(same < 4999, same + 1, -1), (x,), out=(x,))
+    assert torch.equal(x[:, :, :-1], was[:, :, 1:]) and not x[:, :, -1].any()

@@ -107,6 +107,10 @@ def test_gather_refusals(om):
                 dict(dst_entry=32), dict(dst_head=256), dict(dst=0x10000), dict(dst=0x10800), dict(dst=0x1000),
                 dict(dst_entry=0)):
         assert call(**bad) == om.OM_EINVAL, bad
+    # in place: rows that reach into each other's entries; one array of two; two arrays in one place
+    same = dict(dst=0x10000, dst_batch=4096, dst_entry=64)
+    assert call(**same, src_head=1024, dst_head=1024) == om.OM_EINVAL
+    assert call(**same, dst_head=2048, count=2) == om.OM_EINVAL
     for bad in (dict(count=9), dict(b=1 << 16), dict(src_entry=1 << 31), dict(dst_batch=1 << 41), dict(entry_bytes=1 << 25)):
         assert call(**bad) == om.OM_ERANGE, bad
     assert call(b=0, keep=None) == om.OM_OK
