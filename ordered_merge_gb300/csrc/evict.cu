@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(WARPS * 32, acc_warps(ALIGNED) / WARPS)
             for (int k = 0; k < V; k += 4) {
                 const int j = c0 + lane * V + k;
                 if (j + 3 < live) {
-                    const float4 x = __ldcs(reinterpret_cast<const float4*>(score + j));
+                    const float4 x = load_once(reinterpret_cast<const float4*>(score + j));
                     old[k] = x.x, old[k + 1] = x.y, old[k + 2] = x.z, old[k + 3] = x.w;
                 } else {
 #pragma unroll
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(WARPS * 32, acc_warps(ALIGNED) / WARPS)
         } else {
 #pragma unroll
             for (int k = 0; k < V; ++k)
-                if (k * WARPS * 32 + (int)threadIdx.x < live) old[k] = __ldcs(score + k * WARPS * 32 + threadIdx.x);
+                if (k * WARPS * 32 + (int)threadIdx.x < live) old[k] = load_once(score + k * WARPS * 32 + threadIdx.x);
         }
     }
     uint64_t sum[V / 2];
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(WARPS * 32, acc_warps(ALIGNED) / WARPS)
                 if (r + u < r1) {
                     if (!ALIGNED) skip[u] = (int)(reinterpret_cast<uintptr_t>(at) & 15) / (int)sizeof(T);
                     if (room + skip[u] > 0)
-                        w[u] = __ldcs(reinterpret_cast<const uint4*>(at - skip[u] * (int)sizeof(T)) + lane);
+                        w[u] = load_once(reinterpret_cast<const uint4*>(at - skip[u] * (int)sizeof(T)) + lane);
                     at += step;
                     q += STEP;
                     if (q >= a.queries) {
@@ -425,12 +425,12 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) evict_select_kernel(Ev
     const bool aligned = (reinterpret_cast<uintptr_t>(score) & 15) == 0;  // lo is a multiple of 4
 
     auto fetch = [&](int i) {  // scores i .. i + 3
-        if (aligned && i + 3 < hi) return __ldg(reinterpret_cast<const float4*>(score + i));
+        if (aligned && i + 3 < hi) return *reinterpret_cast<const float4*>(score + i);
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (i < hi) x.x = __ldg(score + i);
-        if (i + 1 < hi) x.y = __ldg(score + i + 1);
-        if (i + 2 < hi) x.z = __ldg(score + i + 2);
-        if (i + 3 < hi) x.w = __ldg(score + i + 3);
+        if (i < hi) x.x = score[i];
+        if (i + 1 < hi) x.y = score[i + 1];
+        if (i + 2 < hi) x.z = score[i + 2];
+        if (i + 3 < hi) x.w = score[i + 3];
         return x;
     };
     auto keys_of = [&](int i, float4 x) {  // their keys
@@ -690,18 +690,21 @@ __device__ __forceinline__ void gather_tile(const GatherArgs& a, const om_cache_
     for (int i0 = threadIdx.x; i0 < total; i0 += kGatherThreads * kGatherUnroll) {
         V v[kGatherUnroll];
         int64_t to[kGatherUnroll];
+        int32_t from[kGatherUnroll];
+        int piece[kGatherUnroll];
+        // all indices first, then all vectors: two trips to memory, not two for each vector
 #pragma unroll
         for (int u = 0; u < kGatherUnroll; ++u) {
-            const int i = i0 + u * kGatherThreads;
+            const int i = i0 + u * kGatherThreads, j = i / per;
+            from[u] = i < total ? keep[j0 + j] : -1;
+            piece[u] = (i - j * per) * (int)sizeof(V);
+            to[u] = i < total ? (j0 + j) * c.dst_entry + piece[u] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kGatherUnroll; ++u) {
             v[u] = V{};
-            to[u] = -1;
-            if (i < total) {
-                const int j = i / per, piece = (i - j * per) * (int)sizeof(V);
-                const int32_t from = __ldg(keep + j0 + j);
-                to[u] = (j0 + j) * c.dst_entry + piece;
-                if (from >= 0 && from < a.length)
-                    v[u] = __ldcs(reinterpret_cast<const V*>(src + from * c.src_entry + piece));
-            }
+            if (from[u] >= 0 && from[u] < a.length)
+                v[u] = load_once(reinterpret_cast<const V*>(src + from[u] * c.src_entry + piece[u]));
         }
 #pragma unroll
         for (int u = 0; u < kGatherUnroll; ++u)
@@ -733,9 +736,9 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const __gr
 // chunks together.  An entry that stays where it is is not touched.
 //
 // Bound by the meetings between loading and storing, on cold inputs: 32 rows of
-// 16384 kept of 131072 entries (keys and values of 256 bytes, a score) 142 us,
-// 2 rows of 65536 72 us (369 with one CTA to a column).  Into other memory these
-// take 93 and 29 us, before anything is brought back.
+// 16384 kept of 131072 entries (keys and values of 256 bytes, a score) 99 us,
+// 2 rows of 65536 52 us.  Into other memory these take 91 and 27 us, before
+// anything is brought back.
 
 constexpr int kInPlaceThreads = 512;
 
@@ -754,20 +757,20 @@ __device__ __forceinline__ void gather_row_in_place(const GatherArgs& a, const o
         int64_t to[U];
     };
     auto load = [&](unsigned i0, Chunk& x) {
+        int32_t from[U];
+        unsigned piece[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const unsigned i = i0 + u * stride + first;
+            const unsigned i = i0 + u * stride + first, j = i / per;
+            from[u] = i < total ? keep[j] : (int32_t)j;
+            piece[u] = (i - j * per) * (unsigned)sizeof(V);
+            x.to[u] = from[u] != (int32_t)j ? j * c.dst_entry + piece[u] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
             x.v[u] = V{};
-            x.to[u] = -1;
-            if (i < total) {
-                const unsigned j = i / per, piece = (i - j * per) * (unsigned)sizeof(V);
-                const int32_t from = __ldg(keep + j);
-                if (from != (int32_t)j) {
-                    x.to[u] = j * c.dst_entry + piece;
-                    if (from >= 0 && from < a.length)
-                        x.v[u] = *reinterpret_cast<const V*>(base + from * c.dst_entry + piece);
-                }
-            }
+            if (x.to[u] >= 0 && from[u] >= 0 && from[u] < a.length)
+                x.v[u] = *reinterpret_cast<const V*>(base + from[u] * c.dst_entry + piece[u]);
         }
     };
     Chunk now, next;

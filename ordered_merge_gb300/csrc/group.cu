@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_by_id_kernel(GroupArgs a)
     for (int64_t i0 = wlo + lane; i0 < whi; i0 += 32 * U) {
         int32_t id[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) id[u] = i0 + 32 * u < whi ? __ldg(a.ids + i0 + 32 * u) : 0;
+        for (int u = 0; u < U; ++u) id[u] = i0 + 32 * u < whi ? a.ids[i0 + 32 * u] : 0;
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (i0 + 32 * u < whi) atomicAdd(&next[group_of(id[u], a.groups)], 1);
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_by_id_kernel(GroupArgs a)
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const unsigned c = c0 + 32 * r + lane;
-                    count[r] = c < ctas ? __ldcg(a.place + a.start(c) + g) : 0;
+                    count[r] = c < ctas ? load_l2(a.place + a.start(c) + g) : 0;
                 }
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(kGroupThreads) group_by_id_kernel(GroupArgs a)
         int total = 0, before = 0;
         if (g < E) {
             if (WAY == kGroupGrid) {
-                before = __ldcg(a.place + lo + g);
-                total = __ldcg(a.place + lo + E + g);
+                before = load_l2(a.place + lo + g);
+                total = load_l2(a.place + lo + E + g);
             } else if (WAY == kGroupCluster) {
 #pragma unroll
                 for (unsigned r = 0; r < kGroupCluster8; ++r) {
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_by_id_kernel(GroupArgs a)
     for (int r0 = (int)(wlo - lo) + lane; r0 - lane < r1; r0 += 32 * U) {
         int32_t id[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) id[u] = r0 + 32 * u < r1 ? __ldg(ids + r0 + 32 * u) : 0;
+        for (int u = 0; u < U; ++u) id[u] = r0 + 32 * u < r1 ? ids[r0 + 32 * u] : 0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int r = r0 + 32 * u;

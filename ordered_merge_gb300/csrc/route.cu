@@ -240,7 +240,7 @@ __device__ __forceinline__ Eight<T> load_eight(const T* row, int e, int end, boo
     if (aligned && e + 8 <= end) {
 #pragma unroll
         for (int i = 0; i < W; i += 4) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e) + i / 4);
+            const uint4 v = reinterpret_cast<const uint4*>(row + e)[i / 4];
             x.w[i] = v.x, x.w[i + 1] = v.y, x.w[i + 2] = v.z, x.w[i + 3] = v.w;
         }
     } else {
@@ -248,8 +248,8 @@ __device__ __forceinline__ Eight<T> load_eight(const T* row, int e, int end, boo
         for (int i = 0; i < 8; ++i) {
             uint32_t bits = no_value(T{});
             if (e + i < end) {
-                if (sizeof(T) == 4) bits = __ldg(reinterpret_cast<const uint32_t*>(row) + e + i);
-                else bits = __ldg(reinterpret_cast<const unsigned short*>(row) + e + i);
+                if (sizeof(T) == 4) bits = reinterpret_cast<const uint32_t*>(row)[e + i];
+                else bits = reinterpret_cast<const unsigned short*>(row)[e + i];
             }
             if (sizeof(T) == 4) x.w[i] = bits;
             else x.w[i / 2] = i & 1 ? x.w[i / 2] | bits << 16 : bits;
@@ -689,8 +689,8 @@ __global__ void __launch_bounds__(128) route_topk_backward_kernel(RouteBackArgs 
     int id = -1;
     float g = 0.0f;
     if (l < a.top_k) {
-        id = __ldg(a.ids + at * a.top_k + l);
-        g = __ldg(a.grad_weights + at * a.top_k + l) * a.scale;
+        id = a.ids[at * a.top_k + l];
+        g = a.grad_weights[at * a.top_k + l] * a.scale;
     }
     constexpr int H = DENSE ? kBackHeld : 1;
     Eight<T> x[H];

@@ -89,9 +89,57 @@ cudaError_t counted(F&& launch) {
 // before it in the stream still drains; wait_for_stream, its first statement,
 // holds it back until that one has ended and its writes are visible.  Then it
 // lets the next such kernel come, which waits in its turn.
+//
+// Its inputs may thus be written during its life, so it reads them by ordinary
+// loads and by those below, never by the read-only path (__ldg), which takes
+// memory that nobody writes while the kernel lives, and which the compiler may
+// lift over the wait.
 
 __device__ __forceinline__ void wait_for_stream() {
     asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Loads with a cache hint; volatile, so that they stay behind the wait.
+// load_once: what is read once (evicted first).
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(__cvta_generic_to_global(p)));
+    return v;
+}
+__device__ __forceinline__ float4 load_once(const float4* p) {
+    float4 v;
+    asm volatile("ld.global.cs.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "l"(__cvta_generic_to_global(p)));
+    return v;
+}
+__device__ __forceinline__ float load_once(const float* p) {
+    float v;
+    asm volatile("ld.global.cs.f32 %0, [%1];" : "=f"(v) : "l"(__cvta_generic_to_global(p)));
+    return v;
+}
+__device__ __forceinline__ uint32_t load_once(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.global.cs.u32 %0, [%1];" : "=r"(v) : "l"(__cvta_generic_to_global(p)));
+    return v;
+}
+__device__ __forceinline__ unsigned short load_once(const unsigned short* p) {
+    unsigned short v;
+    asm volatile("ld.global.cs.u16 %0, [%1];" : "=h"(v) : "l"(__cvta_generic_to_global(p)));
+    return v;
+}
+__device__ __forceinline__ unsigned char load_once(const unsigned char* p) {
+    uint32_t v;
+    asm volatile("ld.global.cs.u8 %0, [%1];" : "=r"(v) : "l"(__cvta_generic_to_global(p)));
+    return (unsigned char)v;
+}
+// load_l2: a word that another CTA of this launch has written (past the L1 cache).
+__device__ __forceinline__ int load_l2(const int* p) {
+    int v;
+    asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(__cvta_generic_to_global(p)) : "memory");
+    return v;
 }
 
 // The attribute of such a launch.
