@@ -717,7 +717,8 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const __gr
     int k = a.count - 1;
     while (k > 0 && (int)blockIdx.x < a.first_cta[k]) --k;
     const int t = (int)blockIdx.x - a.first_cta[k], row = t / a.tiles[k];
-    const int j0 = (t - row * a.tiles[k]) * a.tile_entries[k], j1 = min(j0 + a.tile_entries[k], a.budget);
+    const int j0 = (t - row * a.tiles[k]) * a.tile_entries[k];
+    const int j1 = j0 + min(a.tile_entries[k], a.budget - j0);  // budgets go up to 2^31 - 1
     switch (a.vector[k]) {
         case 16: gather_tile<uint4>(a, a.arrays[k], row, j0, j1); break;
         case 4: gather_tile<uint32_t>(a, a.arrays[k], row, j0, j1); break;
