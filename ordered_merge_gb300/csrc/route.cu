@@ -37,6 +37,15 @@ __device__ __forceinline__ float sigmoid(float x) {
     return x >= 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x) / (1.0f + expf(x));
 }
 
+// What experts are chosen by where that is the sigmoid score: the same bits in
+// every kernel.  One exponential, of -|x|, so that the divisor lies in [1, 2],
+// where the fast division is good to 2 ulps (it gives 0 for divisors above 2^126),
+// and scores below the normal range stay apart.
+__device__ __forceinline__ float sigmoid_choice(float x) {
+    const float t = expf(-fabsf(x)), r = __fdividef(1.0f, 1.0f + t);
+    return x >= 0.0f ? r : __fmul_rn(t, r);
+}
+
 // One warp per token; lane l holds the experts l, l + 32, ...
 template <typename T, int R>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(RouteArgs a) {
@@ -74,7 +83,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(RouteArgs 
             const int e = r * 32 + lane;
             float c = x[r];
             if (!by_logit && x[r] > kNone) {
-                c = a.score == OM_SCORE_SOFTMAX ? expf(x[r] - top) / sum : sigmoid(x[r]);
+                c = a.score == OM_SCORE_SOFTMAX ? expf(x[r] - top) / sum : sigmoid_choice(x[r]);
                 if (a.bias != nullptr) c += a.bias[e];
             }
             const bool open = x[r] > kNone && c > kNone;  // false for NaN too
@@ -389,7 +398,7 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
             // scores to a few units in the last place: ordered as 32 bits can order them (the
             // hardware's 2^x alone, whose error grows with |v|, would take 7 % off the largest calls)
             if (MODE == kListSoftmax) k[i] = expf(v - top) * inverse;
-            else if (MODE == kListSigmoid) k[i] = __fdividef(1.0f, 1.0f + expf(-v));
+            else if (MODE == kListSigmoid) k[i] = sigmoid_choice(v);
             else k[i] = v;
         }
         if (!BY_LOGIT && a.bias != nullptr) {
