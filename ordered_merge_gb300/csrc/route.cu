@@ -496,8 +496,9 @@ __global__ void __launch_bounds__(kListThreads) route_list_kernel(RouteArgs a, b
             b0 = fmaxf(b0, o0);
         }
         const int group = l / wide;
-        const float score = a.group_best == 2 && b1 > kNone ? b0 + b1 : b0;
-        int ahead = b0 > kNone ? 0 : a.groups;  // groups that go first; an empty one is never picked
+        // an empty group is NaN: never picked, and ahead of no other, not even of a sum that overflows to -inf
+        const float score = !(b0 > kNone) ? NAN : a.group_best == 2 && b1 > kNone ? b0 + b1 : b0;
+        int ahead = b0 > kNone ? 0 : a.groups;  // groups that go first
         for (int g = 0; g < a.groups; ++g) {
             const float other = __shfl_sync(kAll, score, (threadIdx.x & 31 & ~(L - 1)) + g * wide);
             ahead += other > score || (other == score && g < group);
