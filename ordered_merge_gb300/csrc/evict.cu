@@ -29,20 +29,6 @@ __device__ __forceinline__ int64_t valid_length(const int32_t* lengths, int64_t 
     return n < 0 ? 0 : n < length ? n : length;
 }
 
-// Two sums in one register pair, added to at once.
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-    uint64_t p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
-    return p;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t p) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
-    return f;
-}
-__device__ __forceinline__ void add2(uint64_t& sum, uint64_t x) {
-    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(x));
-}
 // The values of a 16-byte vector added to their sums.
 __device__ __forceinline__ void add_vector(uint64_t (&sum)[2], const uint4& w, float) {
     add2(sum[0], pack2(__uint_as_float(w.x), __uint_as_float(w.y)));

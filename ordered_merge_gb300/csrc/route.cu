@@ -267,16 +267,27 @@ __device__ __forceinline__ Eight<T> load_eight(const T* row, int e, int end, boo
     return x;
 }
 
+// Two values as they lie in memory, the first one low.
+__device__ __forceinline__ uint32_t pair_of(float x, float y, __nv_bfloat16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pair_of(float x, float y, __half) {
+    const __half2 v = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // Eight values written from e on, those before the end.
 template <typename T>
 __device__ __forceinline__ void store_eight(T* row, int e, int end, bool aligned, const float (&y)[8]) {
     if (aligned && e + 8 <= end) {
-        __align__(16) T v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = from_float<T>(y[i]);
-#pragma unroll
-        for (int i = 0; i < 8 * (int)sizeof(T) / 16; ++i)
-            reinterpret_cast<uint4*>(row + e)[i] = reinterpret_cast<const uint4*>(v)[i];
+        if constexpr (sizeof(T) == 4) {
+            reinterpret_cast<float4*>(row + e)[0] = make_float4(y[0], y[1], y[2], y[3]);
+            reinterpret_cast<float4*>(row + e)[1] = make_float4(y[4], y[5], y[6], y[7]);
+        } else {
+            *reinterpret_cast<uint4*>(row + e) = make_uint4(pair_of(y[0], y[1], T{}), pair_of(y[2], y[3], T{}),
+                                                            pair_of(y[4], y[5], T{}), pair_of(y[6], y[7], T{}));
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -323,9 +334,19 @@ __device__ __forceinline__ uint32_t plain_pair(uint32_t w, __half) {
 }
 __device__ __forceinline__ uint32_t plain_pair(uint32_t, float) { return 0; }  // not used
 
+// The greater of each two 16-bit values; of a NaN and another, the other.
+__device__ __forceinline__ uint32_t greater_pair(uint32_t a, uint32_t b, __nv_bfloat16) {
+    const __nv_bfloat162 v = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t greater_pair(uint32_t a, uint32_t b, __half) {
+    const __half2 v = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // e^(x - top) for a sum: one multiplication and the hardware's 2^x, terms below
 // 2^-126 as zero.  What the rounding of the argument costs a term falls with the
-// term itself.  x = -inf gives 0; top must be finite or +inf.
+// term itself.  For sums alone: as gradients the terms are taken by expf.  x = -inf gives 0; top must be finite or +inf.
 __device__ __forceinline__ float exp_term(float x, float top) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((x - top) * 1.4426950408889634f));
@@ -668,11 +689,13 @@ struct RouteBackArgs {
 // arrive.  Rows go out in 16-byte vectors where they are aligned, and the picks
 // over them, each by its own lane.
 //
-// Bound by memory for large batches: what a row takes besides its bytes is
-// about 9 instructions per logit of DENSE, and the picked logits cost a sector
-// each.  Measured: 65536 tokens of 160 bf16, softmax, 12.6 us
-// (45 MB); 4099 tokens of 256 f32, renormalised sigmoid, 4.4 us (4.6 MB), of
-// which 2.2 are those of a single token.
+// Bound by issue for large batches of DENSE: its terms are gradients, so they
+// are taken by expf, to its last places and through the subnormal range (2 us
+// more than the hardware's 2^x alone, of which packed maxima and register pairs
+// give half back); the picked logits cost a sector each.  Measured, cold: 65536
+// tokens of 160 bf16, softmax, 13.4 us (45 MB); 4099 tokens of 256 f32,
+// renormalised sigmoid, 4.4 us (4.6 MB), of which 2.2 are those of a single
+// token.
 template <typename T, bool DENSE, int L>
 __global__ void __launch_bounds__(128) route_topk_backward_kernel(RouteBackArgs a, bool aligned_in, bool aligned_out) {
     wait_for_stream();
@@ -718,28 +741,49 @@ __global__ void __launch_bounds__(128) route_topk_backward_kernel(RouteBackArgs 
     if (!there) g = 0.0f;
 
     float top = kNone, inverse = 1.0f;
-    float y[H][8];
+    uint64_t y[H][4];  // the terms e^(x - top), two to a register pair
     if (DENSE) {
+        // NaN to -inf, and the greatest
+        uint32_t most = 0xffffffffu;  // of 16-bit values, two at a time; a pair of NaN
 #pragma unroll
         for (int step = 0; step < H; ++step)
             if (step < steps) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    y[step][i] = fmaxf(value_of(x[step], i), kNone);  // NaN to -inf
-                    top = fmaxf(top, y[step][i]);
+                for (int i = 0; i < 8 * (int)sizeof(T) / 4; ++i) {
+                    uint32_t& w = x[step].w[i];
+                    if constexpr (sizeof(T) == 4) {
+                        w = __float_as_uint(fmaxf(__uint_as_float(w), kNone));
+                        top = fmaxf(top, __uint_as_float(w));
+                    } else {
+                        w = greater_pair(w, no_value(T{}) * 0x10001u, T{});
+                        most = greater_pair(most, w, T{});
+                    }
                 }
             }
+        if constexpr (sizeof(T) == 2) {
+            Eight<T> two;
+            two.w[0] = most;
+            top = fmaxf(value_of(two, 0), value_of(two, 1));
+        }
         top = reduce_max(top);
         if (!(top > kNone)) top = 0.0f;  // nothing is there
-        float part = 0.0f;
+        const uint64_t less = pack2(-top, -top);
+        uint64_t part = 0;
 #pragma unroll
         for (int step = 0; step < H; ++step)
             if (step < steps) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) part += y[step][i] = exp_term(y[step][i], top);
+                for (int i = 0; i < 4; ++i) {
+                    uint64_t d = pack2(value_of(x[step], 2 * i), value_of(x[step], 2 * i + 1));
+                    add2(d, less);
+                    const float2 f = unpack2(d);
+                    y[step][i] = pack2(expf(f.x), expf(f.y));  // they are gradients: to the last places, subnormal ones too
+                    add2(part, y[step][i]);
+                }
             }
-        part = reduce_sum(part);
-        inverse = part == 0.0f ? 0.0f : 1.0f / part;
+        const float2 sums = unpack2(part);
+        const float sum = reduce_sum(sums.x + sums.y);
+        inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
     }
     // w: the pick's weight before scale
     float w = 0.0f, dot = 0.0f;
@@ -754,12 +798,17 @@ __global__ void __launch_bounds__(128) route_topk_backward_kernel(RouteBackArgs 
     if (DENSE || a.renorm) dot = reduce_sum(g * w);
     if (DENSE) {
         const float every = -dot * inverse;
+        const uint64_t both = pack2(every, every);
 #pragma unroll
         for (int step = 0; step < H; ++step)
             if (step < steps) {
+                float out[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[step][i] *= every;
-                if (live) store_eight(grad, (step * L + l) * 8, a.experts, aligned_out, y[step]);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack2(mul2(y[step][i], both));
+                    out[2 * i] = f.x, out[2 * i + 1] = f.y;
+                }
+                if (live) store_eight(grad, (step * L + l) * 8, a.experts, aligned_out, out);
             }
     }
     __syncwarp();  // the picks are written over what another lane may have written

@@ -49,6 +49,26 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
+// Two floats in one register pair, added or multiplied at once.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ void add2(uint64_t& sum, uint64_t x) {
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(x));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+    uint64_t p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(x), "l"(y));
+    return p;
+}
+
 // ---- thread-block clusters
 
 __device__ __forceinline__ uint32_t cluster_rank() {
