@@ -79,6 +79,12 @@ constexpr int kAccMaxWarps = 8;
 constexpr int acc_unroll(bool aligned) { return aligned ? 8 : 4; }
 constexpr int acc_warps(bool aligned) { return aligned ? 24 : 32; }
 
+// Rows that go one after another into one 32-bit sum.  Their sum is then added to
+// the tile's, so that the error grows with 128 + rows / 128 and not with the rows
+// (65536 equal ones: up to 1e-3 of the sum in one, 8e-6 so).
+constexpr int kSumRows = 128;
+static_assert(kSumRows % acc_unroll(true) == 0 && kSumRows % acc_unroll(false) == 0, "whole batches");
+
 // A warp sums rows over one tile of entries, V = 16 bytes' worth per lane; the
 // rows of a tile (share * queries of them) are split over 2^log_split warps of
 // the CTA, whose sums are then added in the order of the warps, so the result
@@ -153,6 +159,9 @@ __global__ void __launch_bounds__(WARPS * 32, acc_warps(ALIGNED) / WARPS)
     uint64_t sum[V / 2];
 #pragma unroll
     for (int v = 0; v < V / 2; ++v) sum[v] = 0;
+    uint64_t whole[V / 2];  // DIRECT: the blocks of rows before
+#pragma unroll
+    for (int v = 0; v < V / 2; ++v) whole[v] = 0;
     int cur = -1;  // offset, in values, of what `sum` holds
     bool fresh = true;
     // adds the sums to the tile's entries; entries left of it or past its end are other tiles'
@@ -189,14 +198,15 @@ __global__ void __launch_bounds__(WARPS * 32, acc_warps(ALIGNED) / WARPS)
         const char* at = base + (g * a.w_head + q * a.w_query) * size;
         const int64_t step = STEP * a.w_query * size;
         const int room = (int)min(n - first - c0 - lane * V, (int64_t)1 << 20);  // valid from this lane's first on
-        for (int r = r0; r < r1; r += U) {
+        const int n_rows = r1 - r0;
+        for (int r = 0; r < n_rows; r += U) {
             uint4 w[U];
             int skip[U], changes = 0;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 w[u] = make_uint4(0, 0, 0, 0);
                 skip[u] = u > 0 ? skip[u - 1] : 0;
-                if (r + u < r1) {
+                if (r + u < n_rows) {
                     if (!ALIGNED) skip[u] = (int)(reinterpret_cast<uintptr_t>(at) & 15) / (int)sizeof(T);
                     if (room + skip[u] > 0)
                         w[u] = load_once(reinterpret_cast<const uint4*>(at - skip[u] * (int)sizeof(T)) + lane);
@@ -216,12 +226,15 @@ __global__ void __launch_bounds__(WARPS * 32, acc_warps(ALIGNED) / WARPS)
                 }
                 changes |= skip[u] ^ skip[0];
             }
-            if (!ALIGNED) {
-                const int want = changes == 0 ? skip[0] : 0;
-                if (cur != want) {
-                    if (cur >= 0) settle();
-                    cur = want;
+            const int want = changes == 0 ? skip[0] : 0;  // 0 where ALIGNED
+            if (cur != want || r % kSumRows == 0) {
+                if (DIRECT) {
+#pragma unroll
+                    for (int v = 0; v < V / 2; ++v) add2(whole[v], sum[v]), sum[v] = 0;
+                } else if (cur >= 0) {
+                    settle();
                 }
+                cur = want;
             }
             if (ALIGNED || changes == 0) {
 #pragma unroll
@@ -236,6 +249,7 @@ __global__ void __launch_bounds__(WARPS * 32, acc_warps(ALIGNED) / WARPS)
 #pragma unroll
         for (int k = 0; k < V; k += 4) {
             const int j = c0 + lane * V + k;
+            add2(sum[k / 2], whole[k / 2]), add2(sum[k / 2 + 1], whole[k / 2 + 1]);
             const float2 lo = unpack2(sum[k / 2]), hi = unpack2(sum[k / 2 + 1]);
             float x[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
