@@ -9,8 +9,8 @@ The ordered selections as a model uses them together:
             by them (evict_select) and moved (evict_gather)
   experts   a router scores the experts of each token (route_topk), the slots
             are grouped by expert (group_by_id), each expert multiplies its own
-            rows, and the rows come back weighted; the router learns through
-            route_topk_backward, and a bias evens out the experts' loads
+            rows, and the rows come back weighted; the router learns through the
+            weights' gradient, and a bias evens out the experts' loads
 
 Attention and the experts' products are plain torch: only their order is the
 library's business here.
@@ -69,27 +69,10 @@ class BoundedCache:
         self.lengths = kept
 
 
-class Route(torch.autograd.Function):
-    """route_topk with its gradient: (weights, ids) of logits."""
-
-    @staticmethod
-    def forward(ctx, logits, bias, top_k, options):
-        ids, weights = om.route_topk(logits, top_k, bias=bias, **options)
-        ctx.save_for_backward(logits, ids)
-        ctx.options = {k: options[k] for k in ("score", "renorm", "scale") if k in options}
-        ctx.mark_non_differentiable(ids)
-        return weights, ids
-
-    @staticmethod
-    def backward(ctx, grad_weights, _):
-        logits, ids = ctx.saved_tensors
-        return om.route_topk_backward(logits, ids, grad_weights.contiguous(), **ctx.options), None, None, None
-
-
 def experts_forward(x, router, up, down, top_k, bias=None, **options):
     """sum over the picks of weight * down[e] @ silu(up[e] @ x) for the rows of x, and the experts' loads."""
     experts = router.shape[1]
-    weights, ids = Route.apply(x @ router, bias, top_k, options)
+    ids, weights = om.route_topk(x @ router, top_k, bias=bias, **options)
     offsets, order, place = om.group_by_id(ids, experts)
     rows = x[(order // top_k).long()]  # grouped by expert
     ends = offsets.tolist()

@@ -5,7 +5,8 @@ eviction from a cache.
 Like the rest of the package this is argument marshalling only: tensors'
 pointers, strides and the current stream go to the C ABI (declared in
 ``include/ordmerge.h``), which validates and launches.  Outputs may be passed
-in; those not passed are allocated.
+in; those not passed are allocated.  om_route_topk's weights carry their
+gradient; the other calls stand outside autograd: what they give has none.
 """
 from __future__ import annotations
 
@@ -91,13 +92,43 @@ def _lengths(lengths, batch: int):
     return _ptr(lengths)
 
 
+class _RouteWithGradient(torch.autograd.Function):
+    """om_route_topk with om_route_topk_backward behind it.  The backward pass
+    runs on the stream that autograd runs it on, the caller's at the forward
+    call: who gives another `stream` joins the two before using the weights."""
+
+    @staticmethod
+    def forward(ctx, logits, top_k, options):
+        # outputs handed in come as options: what an earlier call wrote into them is no part of this one
+        ids, weights = om_route_topk(logits, top_k, **options)
+        for given in (options["ids"], options["weights"]):
+            if given is not None:
+                torch.autograd.graph.increment_version(given)
+        ctx.mark_non_differentiable(ids)
+        ctx.save_for_backward(logits, ids)
+        ctx.options = {name: options[name] for name in ("score", "renorm", "scale")}
+        return ids, weights
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _, grad_weights):
+        logits, ids = ctx.saved_tensors
+        return om_route_topk_backward(logits, ids, grad_weights.contiguous(), **ctx.options), None, None
+
+
 def om_route_topk(logits, top_k: int, score: str = "softmax", bias=None, groups: int = 1, group_picks: int = 1,
                   group_best: int = 1, renorm: bool = False, scale: float = 1.0, ids=None, weights=None, stream=None):
     """(ids, weights) of the top_k experts of each row of logits [tokens,
     experts]: greatest score + bias first, ties to the lower index, from the
     group_picks groups whose group_best greatest sum highest; weights are the
     scores without the bias (divided by their sum with renorm) times scale.
-    Masked experts (-inf or NaN) are never chosen; id -1, weight 0 fill up."""
+    Masked experts (-inf or NaN) are never chosen; id -1, weight 0 fill up.
+    Where logits require a gradient the weights carry it to them (the choice
+    is constant, the bias has none)."""
+    if logits.requires_grad and torch.is_grad_enabled():
+        options = dict(score=score, bias=bias, groups=groups, group_picks=group_picks, group_best=group_best,
+                       renorm=renorm, scale=scale, ids=ids, weights=weights, stream=stream)
+        return _RouteWithGradient.apply(logits, top_k, options)
     row_stride = _rows(logits, "logits", 2)[0]
     tokens, experts = logits.shape
     if bias is not None:
