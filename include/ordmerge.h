@@ -402,7 +402,8 @@ om_status om_group_by_id(const int32_t *ids, int64_t n, int64_t groups,
  *                  0                                    up to `length`.
  * Sums run in 32 bits in an order fixed by the shapes.  score (NULL: start
  * from zero) and out are rows of `length` floats at b * batch stride + h *
- * head stride; out may be score itself, with the same strides.  lengths
+ * head stride; out may be score itself, with the same strides, or share no byte
+ * with it (nor its span with that of weights).  lengths
  * (NULL: all `length`) is a device array of batch int32, clamped into
  * [0, length]; nothing past them is read.  batch * kv_heads, q_heads and
  * queries are at most 65535, strides 2^40, else OM_ERANGE.
@@ -450,9 +451,11 @@ typedef struct {
  * Moves the kept entries of `count` (at most 8) cache arrays (keys, values,
  * scores, ...) together: dst entry (b, h, j) = src entry (b, h, keep[b][h][j])
  * for j < budget, zero bytes where keep is outside [0, length).  `arrays` is
- * a host array, read before the call returns.  No dst may overlap a src,
- * another dst or keep (compared by the span from the first to the last entry),
- * nor share bytes between its own entries.
+ * a host array, read before the call returns.  No dst may share a byte with a
+ * src, another dst or keep, nor between its own entries.  Arrays may lie between
+ * each other's rows (keys beside values in one buffer) where their strides are
+ * the same; with other strides, and with keep, what counts is the span from the
+ * first entry to the last.
  * In place: all arrays together may have dst = src, with the same strides;
  * keep has to rise then, as om_evict_select's does (values are lost
  * otherwise), and entries past the budget keep what they held.

@@ -1,5 +1,6 @@
 // om_accumulate_weights / om_evict_select / om_evict_gather: eviction from a
 // cache by accumulated attention weight.
+#include <algorithm>
 #include <cstdint>
 #include <mutex>
 
@@ -838,6 +839,48 @@ static int64_t strided_span(int64_t bytes, const int64_t (&count)[3], const int6
     return span;
 }
 
+// Two strided arrays of the same dimensions: of each their counts and strides in bytes.
+struct DimPair {
+    int64_t count_a, stride_a, count_b, stride_b;
+};
+
+// Whether an element of a and one of b share a byte, b's first one being `delta`
+// bytes after a's; dims greatest stride first.  Rows of one stride can only meet
+// at the few multiples of it that bring their insides together.  A yes may be
+// wrong where strides differ, a no never is.
+static bool rows_meet(int64_t delta, const DimPair* dim, int dims, int64_t bytes_a, int64_t bytes_b) {
+    int64_t in_a = bytes_a, in_b = bytes_b;  // spans of the dimensions below the first
+    for (int i = 1; i < dims; ++i) {
+        in_a += dim[i].stride_a * (dim[i].count_a - 1);
+        in_b += dim[i].stride_b * (dim[i].count_b - 1);
+    }
+    if (dims == 0) return delta < in_a && -delta < in_b;
+    if (delta >= in_a + dim->stride_a * (dim->count_a - 1) || -delta >= in_b + dim->stride_b * (dim->count_b - 1))
+        return false;
+    const int64_t s = dim->stride_a;
+    if (s != dim->stride_b || s == 0 || (in_a + in_b) / s > 4) return true;
+    // row i of a and row i + k of b
+    const int64_t low = std::max((-in_b - delta) / s - 1, -(dim->count_a - 1));
+    const int64_t high = std::min((in_a - delta) / s + 1, dim->count_b - 1);
+    for (int64_t k = low; k <= high; ++k)
+        if (rows_meet(delta + k * s, dim + 1, dims - 1, bytes_a, bytes_b)) return true;
+    return false;
+}
+
+// The same of arrays of three dimensions at a and b, whose spans are known.
+static bool arrays_meet(const void* a, int64_t span_a, int64_t bytes_a, const int64_t (&count_a)[3],
+                        const int64_t (&stride_a)[3], const void* b, int64_t span_b, int64_t bytes_b,
+                        const int64_t (&count_b)[3], const int64_t (&stride_b)[3]) {
+    if (!overlaps(a, span_a, b, span_b, 1)) return false;
+    DimPair dim[3];
+    int dims = 0;
+    for (int i = 0; i < 3; ++i)
+        if (count_a[i] > 1 || count_b[i] > 1) dim[dims++] = {count_a[i], stride_a[i], count_b[i], stride_b[i]};
+    std::sort(dim, dim + dims, [](const DimPair& x, const DimPair& y) { return x.stride_a > y.stride_a; });
+    return rows_meet((int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)), dim, dims, bytes_a,
+                     bytes_b);
+}
+
 }  // namespace om
 
 using namespace om;
@@ -869,7 +912,9 @@ om_status om_accumulate_weights(int value_type, const void* weights, int64_t bat
     if (queries > 0 && overlaps(out, o_span, weights, w_span, 1)) return OM_EINVAL;
     if (lengths != nullptr && overlaps(out, o_span, lengths, batch * 4, 1)) return OM_EINVAL;
     if (score != nullptr && !(score == out && s_batch == o_batch && s_head == o_head) &&
-        overlaps(out, o_span, score, ((batch - 1) * s_batch + (kv_heads - 1) * s_head + length) * 4, 1))
+        arrays_meet(out, o_span, length * 4, {batch, kv_heads, 1}, {o_batch * 4, o_head * 4, 0}, score,
+                    ((batch - 1) * s_batch + (kv_heads - 1) * s_head + length) * 4, length * 4, {batch, kv_heads, 1},
+                    {s_batch * 4, s_head * 4, 0}))
         return OM_EINVAL;
     AccumulateArgs a{weights, score, lengths, out,    w_batch, w_head,        w_query, s_batch, s_head, o_batch, o_head,
                      length,  (int)kv_heads, (int)(q_heads / kv_heads), (int)queries, decay};
@@ -945,10 +990,17 @@ om_status om_evict_gather(const int32_t* keep, int64_t batch, int64_t heads, int
     }
     if (in_place != 0 && in_place != count) return OM_EINVAL;
     for (int i = 0; i < count; ++i)
-        for (int j = 0; j < count; ++j)
-            if ((!(in_place && i == j) && overlaps(a.arrays[i].dst, spans[i], a.arrays[j].src, src_spans[j], 1)) ||
-                (i < j && overlaps(a.arrays[i].dst, spans[i], a.arrays[j].dst, spans[j], 1)))
+        for (int j = 0; j < count; ++j) {
+            const om_cache_array &c = a.arrays[i], &o = a.arrays[j];
+            auto dst_meets = [&](const void* p, int64_t span, int64_t entries, int64_t sb, int64_t sh, int64_t se) {
+                return span > 0 && arrays_meet(c.dst, spans[i], c.entry_bytes, {batch, heads, budget},
+                                               {c.dst_batch, c.dst_head, c.dst_entry}, p, span, o.entry_bytes,
+                                               {batch, heads, entries}, {sb, sh, se});
+            };
+            if (!(in_place && i == j) && dst_meets(o.src, src_spans[j], length, o.src_batch, o.src_head, o.src_entry))
                 return OM_EINVAL;
+            if (i < j && dst_meets(o.dst, spans[j], budget, o.dst_batch, o.dst_head, o.dst_entry)) return OM_EINVAL;
+        }
     a.keep = keep;
     a.length = length;
     a.budget = (int)budget;

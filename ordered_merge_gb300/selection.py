@@ -290,7 +290,7 @@ def om_evict_gather(keep, arrays, out=None, stream=None):
     """The cache arrays (each [batch, heads, entries, ...], any element type,
     entries contiguous) gathered to keep [batch, heads, budget]: entry j
     becomes entry keep[j], zero where keep is -1.  Returns new arrays, or
-    `out`, which must not overlap the inputs, or is their first budget entries
+    `out`, which must share no byte with the inputs, or is their first budget entries
     (out[i] = arrays[i][:, :, :budget]: in place, for rising keep).  One launch
     moves all of them."""
     arrays = tuple(arrays)
