@@ -349,6 +349,10 @@ typedef enum {
  *    the slots left over, a wholly masked one in all of them.
  *  - The renormalised weights come from shifted exponentials: they stay
  *    right when every s underflows.
+ *  - The same call on the same GPU repeats bit for bit.  With another number of
+ *    tokens a row's sums (softmax's, renorm's) may run in another order: its
+ *    weights, and a choice by softmax scores that hangs on the last bit of one,
+ *    may then differ by that bit.  Sigmoid scores are the same in every call.
  *  - 1 <= top_k <= group_picks * (experts / groups), groups divides experts.
  *    At most 1024 experts, 32 groups, top_k 32 and 2^32 tokens, else
  *    OM_ERANGE.
@@ -400,13 +404,16 @@ om_status om_group_by_id(const int32_t *ids, int64_t n, int64_t groups,
  *   out[b][h][i] = decay * score[b][h][i] + sum over the queries and query
  *                  heads of h of weights(b, hq, q, i)   for i < lengths[b],
  *                  0                                    up to `length`.
- * Sums run in 32 bits in an order fixed by the shapes.  score (NULL: start
- * from zero) and out are rows of `length` floats at b * batch stride + h *
- * head stride; out may be score itself, with the same strides, or share no byte
- * with it (nor its span with that of weights).  lengths
- * (NULL: all `length`) is a device array of batch int32, clamped into
- * [0, length]; nothing past them is read.  batch * kv_heads, q_heads and
- * queries are at most 65535, strides 2^40, else OM_ERANGE.
+ * Sums run in 32 bits, by blocks of 128 rows, in an order fixed by the
+ * shapes, the strides, the address of weights modulo 16 and the number of SMs:
+ * the same call repeats bit for bit, and the same values at other addresses may
+ * differ in the last places.  score (NULL: start from zero) and out are rows of
+ * `length` floats at b * batch stride + h * head stride; out may be score
+ * itself, with the same strides, or share no byte with it (nor its span with
+ * that of weights).  lengths (NULL: all `length`) is a device array of batch
+ * int32, clamped into [0, length]; nothing past them counts (whole aligned 16
+ * bytes are read: up to 15 bytes beside the values that do).  batch * kv_heads,
+ * q_heads and queries are at most 65535, strides 2^40, else OM_ERANGE.
  */
 om_status om_accumulate_weights(int value_type, const void *weights,
                                 int64_t batch, int64_t q_heads,

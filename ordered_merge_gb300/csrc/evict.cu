@@ -88,8 +88,9 @@ static_assert(kSumRows % acc_unroll(true) == 0 && kSumRows % acc_unroll(false) =
 
 // A warp sums rows over one tile of entries, V = 16 bytes' worth per lane; the
 // rows of a tile (share * queries of them) are split over 2^log_split warps of
-// the CTA, whose sums are then added in the order of the warps, so the result
-// depends on the shapes alone.
+// the CTA, whose sums are then added in the order of the warps.  The order of
+// addition is fixed by the shapes, the strides, the rows' places within 16 bytes
+// and the number of SMs (which the split goes by).
 //
 // Rows may start at any element (ALIGNED: all start on 16 bytes).  A lane loads
 // the aligned 16 bytes that its part of the row begins in and adds them up as
@@ -106,9 +107,10 @@ static_assert(kSumRows % acc_unroll(true) == 0 && kSumRows % acc_unroll(false) =
 // themselves, with no turn through shared memory.
 //
 // Bound by memory: every weight is read once.  64 x 8 cache heads of 8192 bf16
-// entries, eight query heads each (90 MB): 13.2 us a pass, the copy rate;
-// 8 cache heads of 65539 f16 entries, 128 rows each, on odd addresses (138 MB):
-// 25.9 us, where each 16-byte vector of a warp also costs 67 instructions.
+// entries, eight query heads each (90 MB): 16.6 us cold, 80 % of the copy rate,
+// and 13.2 a pass with part of them left in L2; 8 cache heads of 65539 f16
+// entries, 128 rows each, on odd addresses (138 MB): 28.5 us cold and 25.5 a pass,
+// where each 16-byte vector of a warp also costs 67 instructions.
 template <typename T, bool ALIGNED, bool DIRECT, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, acc_warps(ALIGNED) / WARPS)
     accumulate_weights_kernel(AccumulateArgs a, int log_split) {
@@ -389,7 +391,7 @@ struct SelectShared {
 //
 // Bound by its chain: each of the three digits is a pass over the keys, a meeting
 // of the cluster and a search of the sums.  32 rows of 131072 entries (16.8 MB)
-// take 21 us, 8 rows of 4096 8.0; the bytes alone would take 2.5 and 0.02.
+// take 22 us, 8 rows of 4096 8.0; the bytes alone would take 2.5 and 0.02.
 template <bool CACHED, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) evict_select_kernel(EvictArgs a) {
     wait_for_stream();
@@ -607,8 +609,8 @@ static size_t select_smem(int64_t keys) {
 }
 
 // Entries up to which a row's CTA has 8 warps instead of 16 where there are more
-// rows than SMs: 1024 rows of 2048 entries 17 us against 29, of 4096 21 against
-// 32, but 512 of 8192 24 against 21, and 8 of 4096 9.4 against 9.0.
+// rows than SMs: 1024 rows of 2048 entries 17.6 us against 29.4, of 4096 20.7
+// against 32.3, but 512 of 8192 22.7 against 21.1, and 150 of 4096 8.6 against 8.4.
 constexpr int64_t kSelectShort = 4096;
 
 // Once per device: the selection kernels' shared-memory limit.
@@ -631,7 +633,8 @@ static om_status prepare_select(const DeviceState* d) {
 template <int WARPS>
 static cudaError_t launch_select_warps(const EvictArgs& a, int64_t rows, int sm_count, cudaStream_t st) {
     // As many CTAs per row as fill the SMs (two CTAs each), but at least 8192 entries
-    // a CTA: 8 rows of 16384 10.3 us, with 2048 11.5; of 4096 7.8, with 2048 9.0.
+    // a CTA: 8 rows of 16384 10.4 us, with 2048 11.9, with 16384 11.3; of 8192 8.7,
+    // with 2048 10.2, with 4096 9.6.
     int ctas = 1;
     while (ctas < kMaxCluster && rows * ctas * 2 <= 2 * (int64_t)sm_count && a.length > ctas * 8192) ctas *= 2;
     const int64_t warps = ctas * WARPS;
@@ -679,7 +682,7 @@ constexpr int kGatherUnroll = 4;  // vectors in flight per thread
 
 // One tile of one row of one array: the CTA's threads take its vectors in turn.
 // Bound by memory: 32 rows of 16384 kept entries of 256 + 256 + 4 bytes (0.54 GB)
-// take 84 us, 95 % of the copy rate; CTAs of 256 threads took 94, of 128 90.
+// take 86 us, 93 % of the copy rate; CTAs of 256 threads take 94, of 128 86.
 template <typename V>
 __device__ __forceinline__ void gather_tile(const GatherArgs& a, const om_cache_array& c, int64_t row, int j0, int j1) {
     const int per = (int)(c.entry_bytes / (int)sizeof(V));
@@ -738,8 +741,8 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const __gr
 // chunks together.  An entry that stays where it is is not touched.
 //
 // Bound by the meetings between loading and storing, on cold inputs: 32 rows of
-// 16384 kept of 131072 entries (keys and values of 256 bytes, a score) 99 us,
-// 2 rows of 65536 52 us.  Into other memory these take 91 and 27 us, before
+// 16384 kept of 131072 entries (keys and values of 256 bytes, a score) 94 us,
+// 2 rows of 65536 47 us.  Into other memory these take 86 and 24 us, before
 // anything is brought back.
 
 constexpr int kInPlaceThreads = 512;

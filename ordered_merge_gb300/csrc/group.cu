@@ -60,9 +60,9 @@ enum GroupWay {
 //
 // What bounds it: for few slots the chain of loads and barriers, 4 us of which
 // one CTA needs for its first loads; for many the two grid barriers (1.4 us
-// each) and the ranking, about 130 instructions per 32 slots.  Measured, times
-// of the kernel: 512 slots of 256 groups 4.3 us, 32768 8.0 us, 1.05 M of 128
-// 16.3 us.  Writing `order` from a chunk put in order in shared memory first,
+// each) and counting and ranking, about 150 instructions per 32 slots.  Measured,
+// times of the kernel: 512 slots of 256 groups 4.0 us, 32768 7.6 us, 1.05 M of
+// 128 16.4 us.  Writing `order` from a chunk put in order in shared memory first,
 // in runs, was no faster (16.5 us).
 // BITS: of the greatest group, `groups` itself.
 template <int WAY, int BITS>
@@ -246,12 +246,12 @@ static om_status prepare_group(const DeviceState* d) {
 }
 
 // Slots up to which one CTA, and one cluster, does the call: 2048 slots of 64
-// groups 5.2 us alone, 6.0 in a cluster; 8192 of 128 11.1 and 6.3; 32768 of 256
-// 9.3 in a cluster, 11.5 in a grid; 65536 of 256 13.4 and 10.4 (all before the
-// votes' number became a constant, which took a tenth off each).
+// groups 4.6 us alone, 5.1 in a cluster; 4096 6.3 and 5.2, 8192 of 128 10.0 and
+// 5.3; 49152 of 256 9.1 in a cluster, 9.9 in a grid; 65536 11.5 and 10.0.
 constexpr int64_t kGroupLoneSlots = 2048;
 constexpr int64_t kGroupClusterSlots = 49152;
-// Least slots of a CTA of several (8192 slots in 8 CTAs 6.3 us, in 4 7.1).
+// Least slots of a CTA of several (8192 slots in 8 CTAs 5.3 us, in 4 5.9; 4096 of
+// 64 groups in 4 5.2 us, in 2 5.8, in 8 5.0).
 constexpr int64_t kGroupLeastChunk = 1024;
 
 }  // namespace om

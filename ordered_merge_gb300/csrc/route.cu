@@ -184,10 +184,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(RouteArgs 
 // taken from their heads, and the lists of groups not picked are dropped.
 
 // What bounds it is the rate of minima and maxima (half of the issue rate): a
-// token of 128 bf16 logits takes about 40 warp instructions of them and 94 in
-// all, 64 of them in that pipe.  Measured, 131071 tokens, top 8: 128 bf16 logits 18 us (2.3 TB/s), 128
-// f32 29 us, 256 f32 sigmoid scores with bias in 8 groups 71 us, where the
-// kernel above takes 87, 87 and 271 us; top 16 of 160 bf16 42 us against 225.
+// token of 128 bf16 logits takes about 40 warp instructions of them and 96 in
+// all, 61 of them in that pipe.  Measured, 131071 tokens, top 8: 128 bf16 logits
+// 17.7 us (2.4 TB/s), 128 f32 29 us, 256 f32 sigmoid scores with bias in 8 groups
+// 74 us (there by issue: 3.1 of 4 a clock), where the kernel above takes 87, 87 and
+// 271 us; top 16 of 160 bf16 42 us against 225.
 constexpr int kListThreads = 128;
 constexpr int kListPitch = kListThreads + 1;  // of the rows of choices: neighbouring rows start on other banks
 
@@ -346,7 +347,8 @@ __device__ __forceinline__ uint32_t greater_pair(uint32_t a, uint32_t b, __half)
 
 // e^(x - top) for a sum: one multiplication and the hardware's 2^x, terms below
 // 2^-126 as zero.  What the rounding of the argument costs a term falls with the
-// term itself.  For sums alone: as gradients the terms are taken by expf.  x = -inf gives 0; top must be finite or +inf.
+// term itself.  For sums alone: as gradients the terms are taken by expf.
+// x = -inf gives 0; top must be finite or +inf.
 __device__ __forceinline__ float exp_term(float x, float top) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((x - top) * 1.4426950408889634f));
@@ -777,7 +779,7 @@ __global__ void __launch_bounds__(128) route_topk_backward_kernel(RouteBackArgs 
                     uint64_t d = pack2(value_of(x[step], 2 * i), value_of(x[step], 2 * i + 1));
                     add2(d, less);
                     const float2 f = unpack2(d);
-                    y[step][i] = pack2(expf(f.x), expf(f.y));  // they are gradients: to the last places, subnormal ones too
+                    y[step][i] = pack2(expf(f.x), expf(f.y));
                     add2(part, y[step][i]);
                 }
             }
@@ -844,8 +846,8 @@ static cudaError_t launch_list_lanes(const RouteArgs& a, bool aligned, cudaStrea
 
 // A token gets 32 lanes (PACKED: 16) while that gives an SM at most this many
 // threads (2432 tokens): the shorter chain wins until the SMs are busy.  2048
-// biased sigmoid tokens in 8 groups of 32 experts: 5.8 us against 6.3 with
-// 8 lanes each; 4096: 7.8 against 7.6; 131071: 140 against 71.
+// biased sigmoid tokens in 8 groups of 32 experts: 5.7 us against 6.9 with
+// 8 lanes each; 4096: 7.9 against 7.8; 131071: 147 against 74.
 constexpr int kListFewThreads = 512;
 // The most experts that 4 (grouped: twice as many for 8) lanes take, whose
 // choices then fill 37 KB of shared memory; not for PACKED, which keeps none.
@@ -883,9 +885,9 @@ static void launch_back_lanes(const RouteBackArgs& a, bool in, bool out, cudaStr
 }
 
 // 8 lanes a token, or 32: where there are more picks than 8, and in DENSE where
-// the row fits the registers of 32 lanes only (65536 tokens of 257 f32: 50 us,
-// 8 lanes 62) or the tokens are few (`few`; 512 of 160 bf16: 3.1 us against
-// 3.5, 65536: 31 against 17.5).
+// the row fits the registers of 32 lanes only (65536 tokens of 257 f32: 49 us) or
+// the tokens are few (`few`; 512 of 160 bf16: 3.2 us against 3.4, 4099: 3.8 against
+// 3.7, 65536: 31 against 13.4).
 template <typename T, bool DENSE>
 static void launch_back(const RouteBackArgs& a, bool in, bool out, bool few, cudaStream_t st) {
     constexpr int kHeld8 = 8 * 8 * kBackHeld, kHeld32 = 8 * 32 * kBackHeld;
@@ -955,7 +957,7 @@ om_status om_route_topk(int value_type, const void* logits, int64_t tokens, int6
         listed = fits(few ? 32 : 8);
     } else {
         // 8 lanes and lists of 16; a few tokens' f32 logits are as well off with a warp each (512 of 128, top 10:
-        // 3.6 us against 4.9; of 256 with bias, top 12: 10.7 against 8.4; 131071 of 160 bf16, top 16: 225 against 42)
+        // 3.7 us against 4.9; of 256 with bias, top 12: 10.7 against 8.1; 131071 of 160 bf16, top 16: 225 against 42)
         listed = top_k <= 16 && room && fits(8) && !(some && vb == 4 && bias == nullptr && groups == 1);
     }
     if (listed) {

@@ -15,7 +15,7 @@ import struct
 
 import torch
 
-from . import _check, _lib, _stream
+from . import CacheArray, _check, _lib, _stream
 
 VALUE_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -283,7 +283,7 @@ def _gather_geometry(keep_shape, *arrays):
             raise ValueError("the arrays must have as many entries each")
         length = src_shape[2]
         words.append((inner * size, *(s * size for s in src_strides[:3]), *(s * size for s in dst_strides[:3])))
-    return words, length, struct.Struct(f"{9 * len(words)}q").pack
+    return words, length, struct.Struct(f"{len(CacheArray._fields_) * len(words)}q").pack
 
 
 def om_evict_gather(keep, arrays, out=None, stream=None):
@@ -315,6 +315,6 @@ def om_evict_gather(keep, arrays, out=None, stream=None):
     table = []
     for src, dst, fixed in zip(arrays, out, words):
         table += (src.data_ptr(), dst.data_ptr(), *fixed)
-    # om_cache_array: nine 64-bit words
+    # om_cache_array, whose fields are 64-bit words in this order
     _check(_lib.om_evict_gather(_ptr(keep), *shape, length, pack(*table), len(arrays), handle), "om_evict_gather")
     return out
