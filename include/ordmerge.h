@@ -474,6 +474,152 @@ om_status om_evict_gather(const int32_t *keep, int64_t batch, int64_t heads,
                           const om_cache_array *arrays, int count,
                           void *stream);
 
+/* ---- a decoding step around the ordered selections ----------------------- */
+
+/*
+ * What stands next to the selections above when a model decodes: the beams
+ * that go on and their states, the rows of the embedding that the tokens ask
+ * for (and, in training, that table's gradient), and the routed experts
+ * themselves for a few tokens.  The calls are asynchronous on `stream`;
+ * launches are counted by om_launch_count, om_trace_read has no kind for them.
+ */
+
+/*
+ * The best continuations of a beam search.  For each of `batch` sequences,
+ * `beams` rows of `vocab` logits (beam i of sequence b starts batch_stride * b
+ * + beam_stride * i values after `logits`, its values contiguous):
+ *   c[i][v] = scores[b][i] + (logits[b][i][v] - log sum_u exp logits[b][i][u])
+ *   out_* [b][0 .. top) = the `top` greatest c, greatest first: c itself,
+ *   the beam it goes on from (parent) and its token.
+ * Equal c go to the lower beam, then to the lower token.  Sums of exponentials
+ * run in 32 bits; c is formed and compared in 64 bits and rounded once, within
+ * a beam the order is that of the logits themselves.
+ *  - scores (NULL: all zero) holds batch * beams cumulative log probabilities.
+ *    A beam whose score is -inf or NaN does not go on.
+ *  - finished (NULL: none), batch * beams bytes: a beam where it is not zero
+ *    has one continuation, token end_id with c = scores[b][i]; its logits are
+ *    not read.
+ *  - A logit of -inf or NaN has no probability: it counts in no sum and is not
+ *    chosen.  A row that holds +inf has no continuation.  What is left over
+ *    of out_* gets score -inf, parent -1 and token -1.
+ *  - A row's sum does not depend on its address: equal rows tie.  The same call
+ *    on the same GPU repeats bit for bit; with another batch or number of beams
+ *    a row is cut into other slices, and sums may differ in the last places.
+ *  - Whole aligned 16 bytes around a row's values are read.  beams and top are
+ *    at most 64, vocab 2^30, batch 2^24, strides 2^40, else OM_ERANGE.  No
+ *    scratch.
+ */
+om_status om_beam_select(int value_type, const void *logits, int64_t batch,
+                         int64_t beams, int64_t vocab, int64_t batch_stride,
+                         int64_t beam_stride, const float *scores,
+                         const uint8_t *finished, int64_t end_id, int top,
+                         float *out_scores, int32_t *out_parents,
+                         int32_t *out_tokens, void *stream);
+
+/*
+ * One array of the beams' states for om_beam_gather: entry (b, i, h, s),
+ * entry_bytes long, of sequence b, beam i, head h is at src + b * src_batch +
+ * i * src_beam + h * src_head + s * src_entry, all in bytes; likewise dst.
+ */
+typedef struct {
+    const void *src;
+    void *dst;
+    int64_t entry_bytes;
+    int64_t src_batch, src_beam, src_head, src_entry;
+    int64_t dst_batch, dst_beam, dst_head, dst_entry;
+} om_beam_array;
+
+/*
+ * Moves the states of `count` (at most 64) arrays to the beams that go on:
+ *   dst(b, i, h, s) = src(b, parents[b][i], h, s)
+ * for starts[b] <= s < lengths[b].  parents holds batch * beams int32; a beam
+ * whose parent is outside [0, beams) is left as it is, and so are entries
+ * before starts[b] (what the beams share) and from lengths[b] on.  starts
+ * (NULL: 0) and lengths (NULL: all) are device arrays of batch int32, clamped
+ * into [0, entries].
+ * In place: all arrays together may have dst = src, with the same strides, for
+ * any parents; beams that keep their place are not touched.  Otherwise no dst
+ * may share a byte with a src or another dst; never with parents, starts or
+ * lengths, nor between its own entries.  Arrays may lie between each other's
+ * rows as in om_evict_gather, and `arrays` is read before the call returns as
+ * there.  Vectors of 16 bytes where every address allows them.  beams <= 64,
+ * heads <= 65535, batch <= 32767, entries < 2^31, entries' bytes and strides
+ * at most 2^30, other strides 2^40, else OM_ERANGE.  No scratch.
+ */
+om_status om_beam_gather(const int32_t *parents, int64_t batch, int64_t beams,
+                         int64_t heads, int64_t entries, const int32_t *starts,
+                         const int32_t *lengths, const om_beam_array *arrays,
+                         int count, void *stream);
+
+/*
+ * Rows of an embedding table by token: out[i] = scale * table[ids[i]] for i < n,
+ * `width` values each, multiplied in 32 bits and rounded once.  Rows of the table
+ * (of the output) are table_stride (out_stride) values apart.  ids holds n
+ * integers of id_bytes (4 or 8) bytes; one outside [0, rows) gives a row of zeros.
+ * out shares no byte with the inputs.  rows < 2^31 - 1, n < 2^31, width <= 2^24,
+ * strides <= 2^40, else OM_ERANGE.  No scratch.
+ */
+om_status om_embed_lookup(int value_type, const void *table, int64_t rows,
+                          int64_t width, int64_t table_stride, const void *ids,
+                          int id_bytes, int64_t n, float scale, void *out,
+                          int64_t out_stride, void *stream);
+
+/*
+ * Gradient of om_embed_lookup's rows by the table:
+ *   grad_table[v] = scale * sum of grad[i] over the i with ids[i] = v,
+ * added to what grad_table holds when accumulate is nonzero, else written to
+ * every row (zeros where no token asks for it).  table_type is value_type or
+ * OM_VALUE_F32; grad_table is rounded once.  ids outside [0, rows) count for
+ * nothing.  The tokens are sorted stably (om_merge_sort_u32) and each row's terms
+ * added in 32 bits in the order of i, in pieces of 64 that are then added in their
+ * order: the same call repeats bit for bit, and no atomics are used.
+ * Takes stream-ordered scratch from the library's pool: 16 n bytes, and with n >
+ * 64 up to n * width / 8 bytes.  n <= 2^30, width <= 2^20, n * ceil(width / 1024)
+ * < 2^31, rows and strides as above, else OM_ERANGE.
+ */
+om_status om_embed_lookup_backward(int value_type, const void *grad, int64_t n,
+                                   int64_t width, int64_t grad_stride,
+                                   const void *ids, int id_bytes, int64_t rows,
+                                   float scale, int accumulate, int table_type,
+                                   void *grad_table, int64_t table_stride,
+                                   void *stream);
+
+/* Activations of om_expert_mlp. */
+typedef enum {
+    OM_ACT_SILU = 0, /* x / (1 + exp(-x)) */
+    OM_ACT_GELU = 1, /* x (1 + erf(x / sqrt 2)) / 2 */
+    OM_ACT_RELU = 2  /* max(x, 0) */
+} om_activation;
+
+/*
+ * The routed experts' layer for a few tokens (om_route_topk's ids and weights):
+ *   out[t] = sum over the picks j of weights[t][j] * down[e] h,   e = ids[t][j],
+ *   h = act(gate[e] x[t]) * (up[e] x[t])   (gate NULL: h = act(up[e] x[t])).
+ * Values are of value_type, OM_VALUE_BF16 or OM_VALUE_F16.  x and out are rows of
+ * `hidden` values; up and gate hold for each expert `inner` rows of `hidden`,
+ * down `hidden` rows of `inner`, as a linear layer keeps them: row r of expert e
+ * starts e * *_expert + r * *_row values after the first, its values contiguous
+ * (gate and up may lie in one array).  ids (outside [0, experts): an empty slot)
+ * and weights hold tokens * picks values, dense.
+ * Sums run in 32 bits; h goes to the second product as the sum of two values of
+ * value_type; out is rounded once.  An h beyond f16's range is infinite there.
+ * Only the weights of experts that are asked for are read, each once where no
+ * more than 16 tokens (64, where tokens * picks > 8 * experts) ask for it.  The
+ * same call repeats bit for bit.  Takes stream-ordered scratch from the library's
+ * pool: 4 * tokens * picks * inner bytes.  out shares no byte with the inputs.
+ * At most 64 tokens, 32 picks, 1024 experts, hidden and inner 2^20, strides
+ * 2^40, else OM_ERANGE.  Whole 16-byte vectors where hidden, inner, strides and
+ * addresses allow them; single values (several times slower) otherwise.
+ */
+om_status om_expert_mlp(int value_type, const void *x, int64_t tokens,
+                        int64_t hidden, int64_t x_stride, const int32_t *ids,
+                        const float *weights, int64_t picks, int64_t experts,
+                        int64_t inner, const void *up, int64_t up_expert,
+                        int64_t up_row, const void *gate, int64_t gate_expert,
+                        int64_t gate_row, const void *down,
+                        int64_t down_expert, int64_t down_row, int act,
+                        void *out, int64_t out_stride, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,7 +10,8 @@ Import fails loudly if the library has not been built
 (``python -m ordered_merge_gb300.build`` or ``__graft_entry__.build()``).
 
 The ordered selections of a language model (routing, grouping, eviction) are
-in ``selection.py``, reached through this package like the rest.
+in ``selection.py``, the rest of a decoding step (beam search, embedding rows,
+routed experts) in ``decoding.py``; both are reached through this package.
 
 Functions carry the C names (``om_merge_i32`` ...) with unprefixed aliases
 (``merge_i32`` ...).
@@ -37,6 +38,15 @@ class CacheArray(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("entry_bytes", ctypes.c_int64),
                 ("src_batch", ctypes.c_int64), ("src_head", ctypes.c_int64), ("src_entry", ctypes.c_int64),
                 ("dst_batch", ctypes.c_int64), ("dst_head", ctypes.c_int64), ("dst_entry", ctypes.c_int64)]
+
+
+class BeamArray(ctypes.Structure):
+    """om_beam_array: one array of the beams' states for om_beam_gather."""
+
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("entry_bytes", ctypes.c_int64),
+                ("src_batch", ctypes.c_int64), ("src_beam", ctypes.c_int64), ("src_head", ctypes.c_int64),
+                ("src_entry", ctypes.c_int64), ("dst_batch", ctypes.c_int64), ("dst_beam", ctypes.c_int64),
+                ("dst_head", ctypes.c_int64), ("dst_entry", ctypes.c_int64)]
 
 
 class OrdMergeError(RuntimeError):
@@ -105,6 +115,17 @@ def _load():
     lib.om_evict_select.restype = I32
     lib.om_evict_gather.argtypes = [P, I64, I64, I64, I64, P, I32, P]
     lib.om_evict_gather.restype = I32
+    lib.om_beam_select.argtypes = [I32, P, I64, I64, I64, I64, I64, P, P, I64, I32, P, P, P, P]
+    lib.om_beam_select.restype = I32
+    lib.om_beam_gather.argtypes = [P, I64, I64, I64, I64, P, P, P, I32, P]
+    lib.om_beam_gather.restype = I32
+    lib.om_embed_lookup.argtypes = [I32, P, I64, I64, I64, P, I32, I64, F32, P, I64, P]
+    lib.om_embed_lookup.restype = I32
+    lib.om_embed_lookup_backward.argtypes = [I32, P, I64, I64, I64, P, I32, I64, F32, I32, I32, P, I64, P]
+    lib.om_embed_lookup_backward.restype = I32
+    lib.om_expert_mlp.argtypes = [I32, P, I64, I64, I64, P, P, I64, I64, I64, P, I64, I64, P, I64, I64, P, I64, I64, I32,
+                                  P, I64, P]
+    lib.om_expert_mlp.restype = I32
     return lib
 
 
@@ -424,16 +445,20 @@ merge_sort_u32 = om_merge_sort_u32
 device_error = om_device_error
 release_scratch = om_release_scratch
 
-# The ordered selections live in selection.py, which needs torch at import
-# time; it is loaded when one of its names is first used.
+# The ordered selections live in selection.py, the calls around them in
+# decoding.py; both need torch at import time and are loaded when one of their
+# names is first used.
 _SELECTION = ("route_topk", "route_topk_backward", "group_by_id", "accumulate_weights", "evict_select", "evict_gather")
+_DECODING = ("beam_select", "beam_gather", "embed_lookup", "embed_lookup_backward", "expert_mlp")
 
 
 def __getattr__(name: str):
-    if name.removeprefix("om_") in _SELECTION:
-        from . import selection
+    base = name.removeprefix("om_")
+    if base in _SELECTION or base in _DECODING:
+        from . import decoding, selection
 
-        for base in _SELECTION:
-            globals()[base] = globals()["om_" + base] = getattr(selection, "om_" + base)
+        for module, names in ((selection, _SELECTION), (decoding, _DECODING)):
+            for base in names:
+                globals()[base] = globals()["om_" + base] = getattr(module, "om_" + base)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

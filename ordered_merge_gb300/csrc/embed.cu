@@ -1,0 +1,153 @@
+// om_embed_lookup / om_embed_lookup_backward: argument checks, scratch and launches.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "api_internal.cuh"
+#include "embed_kernels.cuh"
+#include "select_common.cuh"
+#include "strided.cuh"
+
+namespace om {
+
+// Values of the widest vector (16 bytes at most) that the addresses, strides (in
+// values) and the width allow.
+static int vector_values(int value, const void* p, int64_t stride, int64_t width) {
+    int n = 16 / value;
+    while (n > 1 && ((reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n * value - 1)) != 0 || stride % n != 0 || width % n != 0))
+        n /= 2;
+    return n;
+}
+
+template <typename T>
+static cudaError_t launch_lookup(EmbedArgs a, cudaStream_t st) {
+    constexpr int kMost = 16 / (int)sizeof(T);
+    const int n = std::min(vector_values(sizeof(T), a.table, a.table_stride, a.width),
+                           vector_values(sizeof(T), a.out, a.out_stride, a.width));
+    const int step = n == kMost ? kMost : n >= 2 ? 2 : 1;
+    const int64_t vectors = a.n * (a.width / step), ctas = (vectors + kEmbedThreads * kEmbedUnroll - 1) / (kEmbedThreads * kEmbedUnroll);
+    if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+    auto* kern = step == kMost ? embed_lookup_kernel<T, kMost> : step == 2 ? embed_lookup_kernel<T, 2> : embed_lookup_kernel<T, 1>;
+    return counted([&] { launch_early(kern, (unsigned)ctas, kEmbedThreads, 0, st, a); });
+}
+
+template <typename T, typename O>
+static cudaError_t launch_backward(EmbedBackArgs a, int sm_count, cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    if (a.n > 0) {
+        e = counted([&] { launch_early(embed_keys_kernel, (unsigned)((a.n + 255) / 256), 256, 0, st, a); });
+        if (e != cudaSuccess) return e;
+        const om_status s = om_merge_sort_u32(a.keys, a.slots, a.n, st);
+        if (s != OM_OK) return s == OM_ENOMEM ? cudaErrorMemoryAllocation : cudaErrorUnknown;
+    }
+    constexpr int kMost = 8;
+    const int n = std::min(vector_values(sizeof(T), a.grad, a.grad_stride, a.width),
+                           vector_values(sizeof(O), a.grad_table, a.table_stride, a.width));
+    const int step = std::min(n, 16 / (int)std::max(sizeof(T), sizeof(O)));
+    a.tiles = (a.width + kEmbedTile - 1) / kEmbedTile;
+    // sorted places of a warp: as few as still give every SM 32 warps
+    a.window = 1;
+    while (a.window < 32 && a.n * a.tiles / a.window > 64 * (int64_t)sm_count) a.window *= 2;
+    const int64_t per = kEmbedBackThreads / 32;
+    a.sum_ctas = ((a.n + a.window - 1) / a.window * a.tiles + per - 1) / per;
+    a.zero_rows = 8;
+    const int64_t zeros = a.accumulate ? 0 : (a.rows + a.zero_rows - 1) / a.zero_rows;
+    const int64_t ctas = a.sum_ctas + (zeros + per - 1) / per;
+    if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+    if (ctas > 0) {
+        auto* kern = step >= 8   ? embed_sum_kernel<T, O, sizeof(T) == 2 && sizeof(O) == 2 ? kMost : 4>
+                     : step >= 4 ? embed_sum_kernel<T, O, 4>
+                     : step >= 2 ? embed_sum_kernel<T, O, 2>
+                                 : embed_sum_kernel<T, O, 1>;
+        e = counted([&] { launch_early(kern, (unsigned)ctas, kEmbedBackThreads, 0, st, a); });
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t joins = (a.n - 1) / kEmbedPiece;  // multiples of kEmbedPiece in (0, n)
+    if (a.n > kEmbedPiece && joins > 0)
+        e = counted([&] { launch_early(embed_join_kernel<O>, (unsigned)(joins * a.tiles), 256, 0, st, a); });
+    return e;
+}
+
+}  // namespace om
+
+using namespace om;
+
+extern "C" {
+
+om_status om_embed_lookup(int value_type, const void* table, int64_t rows, int64_t width, int64_t table_stride,
+                          const void* ids, int id_bytes, int64_t n, float scale, void* out, int64_t out_stride,
+                          void* stream) {
+    const int vb = value_bytes(value_type);
+    if (vb == 0 || rows < 0 || width < 1 || table_stride < 0 || out_stride < 0 || n < 0 || (id_bytes != 4 && id_bytes != 8))
+        return OM_EINVAL;
+    if (rows > INT32_MAX - 1 || n > INT32_MAX || width > (1 << 24) || table_stride > kMaxStride || out_stride > kMaxStride)
+        return OM_ERANGE;
+    if (n == 0) return OM_OK;
+    if ((rows > 0 && table == nullptr) || ids == nullptr || out == nullptr || misaligned(table, vb) ||
+        misaligned(ids, id_bytes) || misaligned(out, vb) || (n > 1 && out_stride < width))
+        return OM_EINVAL;
+    const int64_t span = ((n - 1) * out_stride + width) * vb;
+    if (overlaps(out, span, ids, n * id_bytes, 1)) return OM_EINVAL;
+    if (rows > 0 && overlaps(out, span, table, ((rows - 1) * table_stride + width) * vb, 1)) return OM_EINVAL;
+    if ((n * width + kEmbedThreads * kEmbedUnroll - 1) / (kEmbedThreads * kEmbedUnroll) > INT32_MAX) return OM_ERANGE;
+    DeviceState* d = nullptr;
+    const om_status s = device_state(&d);
+    if (s != OM_OK) return s;
+    const EmbedArgs a{table, ids, out, rows, n, table_stride, out_stride, (int)width, id_bytes == 8, 0, 0, scale};
+    const cudaError_t e =
+        with_value_type(value_type, [&](auto v) { return launch_lookup<decltype(v)>(a, (cudaStream_t)stream); });
+    return e == cudaSuccess ? OM_OK : cuda_fail(e);
+}
+
+om_status om_embed_lookup_backward(int value_type, const void* grad, int64_t n, int64_t width, int64_t grad_stride,
+                                   const void* ids, int id_bytes, int64_t rows, float scale, int accumulate,
+                                   int table_type, void* grad_table, int64_t table_stride, void* stream) {
+    const int vb = value_bytes(value_type), ob = value_bytes(table_type);
+    if (vb == 0 || ob == 0 || (table_type != value_type && table_type != OM_VALUE_F32) || rows < 0 || width < 1 ||
+        grad_stride < 0 || table_stride < 0 || n < 0 || (id_bytes != 4 && id_bytes != 8))
+        return OM_EINVAL;
+    if (rows > INT32_MAX - 1 || n > (1 << 30) || width > (1 << 20) || grad_stride > kMaxStride || table_stride > kMaxStride)
+        return OM_ERANGE;
+    if (rows == 0) return OM_OK;
+    if (grad_table == nullptr || misaligned(grad_table, ob) || (rows > 1 && table_stride < width)) return OM_EINVAL;
+    if (n > 0 && (grad == nullptr || ids == nullptr || misaligned(grad, vb) || misaligned(ids, id_bytes))) return OM_EINVAL;
+    const int64_t span = ((rows - 1) * table_stride + width) * ob;
+    if (n > 0 && (overlaps(grad_table, span, grad, ((n - 1) * grad_stride + width) * vb, 1) ||
+                  overlaps(grad_table, span, ids, n * id_bytes, 1)))
+        return OM_EINVAL;
+    const int64_t tiles = (width + kEmbedTile - 1) / kEmbedTile;
+    if (n * tiles > (int64_t)INT32_MAX) return OM_ERANGE;
+    DeviceState* d = nullptr;
+    om_status s = device_state(&d);
+    if (s != OM_OK) return s;
+    EmbedBackArgs a{};
+    a.grad = grad, a.ids = ids, a.grad_table = grad_table;
+    a.n = n, a.rows = rows, a.grad_stride = grad_stride, a.table_stride = table_stride;
+    a.width = (int)width, a.wide = id_bytes == 8, a.accumulate = accumulate != 0, a.scale = scale;
+    cudaStream_t st = (cudaStream_t)stream;
+    unsigned char* scratch = nullptr;
+    const size_t list = ((size_t)n * 4 + 255) & ~(size_t)255;
+    if (n > 0) {
+        cudaMemPool_t pool = nullptr;
+        s = scratch_pool(d, &pool);
+        if (s != OM_OK) return s;
+        const size_t sums = n > kEmbedPiece ? (size_t)(2 * ((n - 1) / kEmbedPiece + 1)) * (size_t)width * 4 : 0;
+        const cudaError_t e = scratch_alloc(pool, reinterpret_cast<void**>(&scratch), 2 * list + sums, st);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return OM_ENOMEM;
+        }
+        a.keys = reinterpret_cast<uint32_t*>(scratch);
+        a.slots = reinterpret_cast<uint32_t*>(scratch + list);
+        a.partial = reinterpret_cast<float*>(scratch + 2 * list);
+    }
+    const cudaError_t e = with_value_type(value_type, [&](auto v) {
+        using T = decltype(v);
+        return table_type == value_type ? launch_backward<T, T>(a, d->sm_count, st) : launch_backward<T, float>(a, d->sm_count, st);
+    });
+    if (scratch != nullptr) scratch_free(scratch, st);
+    return e == cudaSuccess ? OM_OK : cuda_fail(e);
+}
+
+}  // extern "C"
