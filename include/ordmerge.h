@@ -570,12 +570,12 @@ om_status om_embed_lookup(int value_type, const void *table, int64_t rows,
  * added to what grad_table holds when accumulate is nonzero, else written to
  * every row (zeros where no token asks for it).  table_type is value_type or
  * OM_VALUE_F32; grad_table is rounded once.  ids outside [0, rows) count for
- * nothing.  The tokens are sorted stably (om_merge_sort_u32) and each row's terms
- * added in 32 bits in the order of i, in pieces of 64 that are then added in their
- * order: the same call repeats bit for bit, and no atomics are used.
- * Takes stream-ordered scratch from the library's pool: 16 n bytes, and with n >
- * 64 up to n * width / 8 bytes.  n <= 2^30, width <= 2^20, n * ceil(width / 1024)
- * < 2^31, rows and strides as above, else OM_ERANGE.
+ * nothing.  The tokens are sorted stably and each row's terms added in 32 bits in
+ * the order of i, in pieces of 32 that are then added in their order: the same
+ * call repeats bit for bit.
+ * Takes stream-ordered scratch from the library's pool: 16 n bytes and,
+ * with n > 32, n * width / 4.  n <= 2^30, width <=
+ * 2^20, n * width < 2^38, rows and strides as above, else OM_ERANGE.
  */
 om_status om_embed_lookup_backward(int value_type, const void *grad, int64_t n,
                                    int64_t width, int64_t grad_stride,
@@ -604,9 +604,11 @@ typedef enum {
  * Sums run in 32 bits; h goes to the second product as the sum of two values of
  * value_type; out is rounded once.  An h beyond f16's range is infinite there.
  * Only the weights of experts that are asked for are read, each once where no
- * more than 16 tokens (64, where tokens * picks > 8 * experts) ask for it.  The
+ * more than 8 tokens (16 or 32, where experts have more than 4 or 8 on average)
+ * ask for it.  The
  * same call repeats bit for bit.  Takes stream-ordered scratch from the library's
- * pool: 4 * tokens * picks * inner bytes.  out shares no byte with the inputs.
+ * pool: 4 * tokens * picks * (inner + hidden) bytes.  One cooperative launch, of a
+ * CTA on every SM.  out shares no byte with the inputs.
  * At most 64 tokens, 32 picks, 1024 experts, hidden and inner 2^20, strides
  * 2^40, else OM_ERANGE.  Whole 16-byte vectors where hidden, inner, strides and
  * addresses allow them; single values (several times slower) otherwise.

@@ -1,6 +1,7 @@
 // om_embed_lookup / om_embed_lookup_backward: argument checks, scratch and launches.
 #include <algorithm>
 #include <cstdint>
+#include <mutex>
 
 #include <cuda_runtime.h>
 
@@ -32,40 +33,93 @@ static cudaError_t launch_lookup(EmbedArgs a, cudaStream_t st) {
     return counted([&] { launch_early(kern, (unsigned)ctas, kEmbedThreads, 0, st, a); });
 }
 
+// Tokens that one cluster sorts; more take the library's merge sort.
+constexpr int64_t kEmbedSortMost = 1 << 18;
+
+// Once per device: clusters of 16, and the sort's shared memory.
+static om_status prepare_embed(const DeviceState* d) {
+    static std::mutex mu;
+    static bool ready[128];
+    std::lock_guard<std::mutex> lk(mu);
+    if (!ready[d->dev]) {
+        if (cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+            cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kEmbedSortSmem) !=
+                cudaSuccess) {
+            cudaGetLastError();
+            return OM_ECUDA;
+        }
+        ready[d->dev] = true;
+    }
+    return OM_OK;
+}
+
+// CTAs of a cluster that goes over n tokens: a CTA for 1024, up to 16.
+static unsigned cluster_for(int64_t n) {
+    unsigned ctas = 1;
+    while (ctas < kEmbedCluster && ctas * 1024 < n) ctas *= 2;
+    return ctas;
+}
+
 template <typename T, typename O>
 static cudaError_t launch_backward(EmbedBackArgs a, int sm_count, cudaStream_t st) {
+    constexpr int kMostT = 16 / (int)sizeof(T), kMostO = 16 / (int)sizeof(O);
+    const int nt = vector_values(sizeof(T), a.grad, a.grad_stride, a.width);
+    const int no = vector_values(sizeof(O), a.grad_table, a.table_stride, a.width);
     cudaError_t e = cudaSuccess;
-    if (a.n > 0) {
+    if (a.n > 0 && a.n <= kEmbedSortMost) {
+        int bits = 1;
+        while (bits < 31 && (a.rows >> bits) != 0) ++bits;  // of the greatest key, `rows`
+        a.passes = (bits + 8) / 9;
+        a.bits = (bits + a.passes - 1) / a.passes;
+        if (a.n <= kEmbedSmallMost) {
+            const unsigned blocks = (unsigned)((a.n + 31) / 32);
+            const size_t smem = (size_t)blocks * 32 * 4 + kEmbedSmallThreads * 4;
+            e = counted([&] { launch_early(embed_sort_small_kernel, blocks, kEmbedSmallThreads, smem, st, a); });
+        } else {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(cluster_for(a.n));
+            cfg.blockDim = dim3(kEmbedSortThreads);
+            cfg.dynamicSmemBytes = kEmbedSortSmem;
+            cfg.stream = st;
+            cudaLaunchAttribute attr[2] = {early_attribute()};
+            attr[1].id = cudaLaunchAttributeClusterDimension;
+            attr[1].val.clusterDim.x = cfg.gridDim.x;
+            attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 2;
+            e = counted([&] { cudaLaunchKernelEx(&cfg, embed_sort_kernel, a); });
+        }
+        if (e != cudaSuccess) return e;
+    } else if (a.n > 0) {
         e = counted([&] { launch_early(embed_keys_kernel, (unsigned)((a.n + 255) / 256), 256, 0, st, a); });
         if (e != cudaSuccess) return e;
         const om_status s = om_merge_sort_u32(a.keys, a.slots, a.n, st);
         if (s != OM_OK) return s == OM_ENOMEM ? cudaErrorMemoryAllocation : cudaErrorUnknown;
     }
-    constexpr int kMost = 8;
-    const int n = std::min(vector_values(sizeof(T), a.grad, a.grad_stride, a.width),
-                           vector_values(sizeof(O), a.grad_table, a.table_stride, a.width));
-    const int step = std::min(n, 16 / (int)std::max(sizeof(T), sizeof(O)));
-    a.tiles = (a.width + kEmbedTile - 1) / kEmbedTile;
-    // sorted places of a warp: as few as still give every SM 32 warps
-    a.window = 1;
-    while (a.window < 32 && a.n * a.tiles / a.window > 64 * (int64_t)sm_count) a.window *= 2;
-    const int64_t per = kEmbedBackThreads / 32;
+    const int step = no == kMostO ? nt : std::min(nt, no);
+    const int values = step == kMostT ? kMostT : step >= 2 ? 2 : 1;
+    a.tiles = (a.width + 32 * values - 1) / (32 * values);
+    // sorted places of a warp: as few as still give every SM its 48 warps
+    a.window = 4;
+    while (a.window < 32 && a.n * a.tiles / a.window > 96 * (int64_t)sm_count) a.window *= 2;
+    const int64_t per = kEmbedSumThreads / 32;
     a.sum_ctas = ((a.n + a.window - 1) / a.window * a.tiles + per - 1) / per;
-    a.zero_rows = 8;
+    a.zero_rows = 32;
+    while (a.zero_rows > 4 && a.rows / a.zero_rows < 32 * (int64_t)sm_count) a.zero_rows /= 2;
     const int64_t zeros = a.accumulate ? 0 : (a.rows + a.zero_rows - 1) / a.zero_rows;
     const int64_t ctas = a.sum_ctas + (zeros + per - 1) / per;
+    if (ctas == 0) return e;
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-    if (ctas > 0) {
-        auto* kern = step >= 8   ? embed_sum_kernel<T, O, sizeof(T) == 2 && sizeof(O) == 2 ? kMost : 4>
-                     : step >= 4 ? embed_sum_kernel<T, O, 4>
-                     : step >= 2 ? embed_sum_kernel<T, O, 2>
-                                 : embed_sum_kernel<T, O, 1>;
-        e = counted([&] { launch_early(kern, (unsigned)ctas, kEmbedBackThreads, 0, st, a); });
-        if (e != cudaSuccess) return e;
-    }
+    auto* kern = values == kMostT ? embed_sum_kernel<T, O, kMostT>
+                 : values == 2    ? embed_sum_kernel<T, O, 2>
+                                  : embed_sum_kernel<T, O, 1>;
+    e = counted([&] { launch_early(kern, (unsigned)ctas, kEmbedSumThreads, 0, st, a); });
     const int64_t joins = (a.n - 1) / kEmbedPiece;  // multiples of kEmbedPiece in (0, n)
-    if (a.n > kEmbedPiece && joins > 0)
-        e = counted([&] { launch_early(embed_join_kernel<O>, (unsigned)(joins * a.tiles), 256, 0, st, a); });
+    if (e == cudaSuccess && joins > 0) {
+        const int tiles = (a.width + kEmbedJoinColumns - 1) / kEmbedJoinColumns;
+        const int64_t groups = (joins + kEmbedJoinPlaces - 1) / kEmbedJoinPlaces;
+        e = counted([&] { launch_early(embed_join_kernel<O>, (unsigned)(groups * tiles), kEmbedJoinThreads, 0, st, a, tiles); });
+    }
     return e;
 }
 
@@ -116,10 +170,10 @@ om_status om_embed_lookup_backward(int value_type, const void* grad, int64_t n, 
     if (n > 0 && (overlaps(grad_table, span, grad, ((n - 1) * grad_stride + width) * vb, 1) ||
                   overlaps(grad_table, span, ids, n * id_bytes, 1)))
         return OM_EINVAL;
-    const int64_t tiles = (width + kEmbedTile - 1) / kEmbedTile;
-    if (n * tiles > (int64_t)INT32_MAX) return OM_ERANGE;
+    if ((n + 3) / 4 * ((width + 31) / 32) > (int64_t)INT32_MAX) return OM_ERANGE;
     DeviceState* d = nullptr;
     om_status s = device_state(&d);
+    if (s == OM_OK) s = prepare_embed(d);
     if (s != OM_OK) return s;
     EmbedBackArgs a{};
     a.grad = grad, a.ids = ids, a.grad_table = grad_table;
@@ -128,19 +182,25 @@ om_status om_embed_lookup_backward(int value_type, const void* grad, int64_t n, 
     cudaStream_t st = (cudaStream_t)stream;
     unsigned char* scratch = nullptr;
     const size_t list = ((size_t)n * 4 + 255) & ~(size_t)255;
+    const size_t sums = n > kEmbedPiece ? (size_t)(2 * ((n - 1) / kEmbedPiece + 1)) * (size_t)width * 4 : 0;
     if (n > 0) {
         cudaMemPool_t pool = nullptr;
         s = scratch_pool(d, &pool);
         if (s != OM_OK) return s;
-        const size_t sums = n > kEmbedPiece ? (size_t)(2 * ((n - 1) / kEmbedPiece + 1)) * (size_t)width * 4 : 0;
-        const cudaError_t e = scratch_alloc(pool, reinterpret_cast<void**>(&scratch), 2 * list + sums, st);
+        const int lists = n <= kEmbedSortMost ? 4 : 2;
+        const cudaError_t e = scratch_alloc(pool, reinterpret_cast<void**>(&scratch), lists * list + sums, st);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return OM_ENOMEM;
         }
-        a.keys = reinterpret_cast<uint32_t*>(scratch);
-        a.slots = reinterpret_cast<uint32_t*>(scratch + list);
-        a.partial = reinterpret_cast<float*>(scratch + 2 * list);
+        unsigned char* at = scratch;
+        a.keys = reinterpret_cast<uint32_t*>(at), at += list;
+        a.slots = reinterpret_cast<uint32_t*>(at), at += list;
+        if (lists == 4) {
+            a.other_keys = reinterpret_cast<uint32_t*>(at), at += list;
+            a.other_slots = reinterpret_cast<uint32_t*>(at), at += list;
+        }
+        a.partial = reinterpret_cast<float*>(at);
     }
     const cudaError_t e = with_value_type(value_type, [&](auto v) {
         using T = decltype(v);

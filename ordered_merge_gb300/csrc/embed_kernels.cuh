@@ -22,6 +22,16 @@ struct alignas(sizeof(T) * N) ValueVec {
     T v[N];
 };
 
+// A vector stored past the caches' usual order: it is not read again soon.
+template <typename T, int N>
+__device__ __forceinline__ void store_streaming(ValueVec<T, N>* p, const ValueVec<T, N>& v) {
+    constexpr int B = (int)sizeof(T) * N;
+    if constexpr (B == 16) __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&v));
+    else if constexpr (B == 8) __stcs(reinterpret_cast<uint2*>(p), *reinterpret_cast<const uint2*>(&v));
+    else if constexpr (B == 4) __stcs(reinterpret_cast<unsigned*>(p), *reinterpret_cast<const unsigned*>(&v));
+    else __stcs(reinterpret_cast<unsigned short*>(p), *reinterpret_cast<const unsigned short*>(&v));
+}
+
 // --------------------------------------------------------------- lookup --
 
 struct EmbedArgs {
@@ -72,31 +82,216 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_lookup_kernel(const Embed
 #pragma unroll
             for (int k = 0; k < N; ++k) v[u].v[k] = from_float<T>(to_float(v[u].v[k]) * a.scale);
         }
-        *reinterpret_cast<V*>(static_cast<T*>(a.out) + token[u] * a.out_stride + piece[u]) = v[u];
+        store_streaming(reinterpret_cast<V*>(static_cast<T*>(a.out) + token[u] * a.out_stride + piece[u]), v[u]);
     }
 }
 
 // ------------------------------------------------------------- gradient --
+//
+// The tokens are sorted stably; the rows of equal tokens are then neighbours, and
+// are summed in their order.  The same launch writes the zeros of the rows that no
+// token asks for; a last one joins the pieces of long runs.
 
 struct EmbedBackArgs {
     const void* grad;
     const void* ids;
     void* grad_table;
-    uint32_t *keys, *slots;  // tokens sorted (rows: none of the table's), and where they stand
-    float* partial;          // sums of the pieces of long runs
+    uint32_t *keys, *slots;            // tokens sorted (rows: none of the table's), and where they stand
+    uint32_t *other_keys, *other_slots;  // (sorting) the passes' other side
+    float* partial;  // sums of the pieces of long runs
     int64_t n, rows, grad_stride, table_stride;
     int width, wide, accumulate;
-    int tiles;               // column tiles of a row
-    int window;              // sorted places of a warp
-    int64_t sum_ctas, zero_rows;  // CTAs that sum, and rows that a zeroing warp looks after
+    int tiles;            // column tiles of a row
+    int window;           // sorted places of a warp
+    int passes, bits;     // (sorting) digits of a key and bits of a digit
+    int64_t sum_ctas;     // CTAs that sum; those after them write zeros
+    int zero_rows;        // rows of a warp of them
     float scale;
 };
 
-constexpr int kEmbedBackThreads = 128;
-constexpr int kEmbedPiece = 64;  // tokens of a run that one warp sums
-constexpr int kEmbedTile = 1024;  // columns of a warp
+constexpr int kEmbedPiece = 32;  // tokens of a run that one warp sums
 
-// Sort keys: tokens that are no row of the table come last.
+// ---- the sort: one cluster, least digit first
+//
+// As in the grouping of slots by id: a place is the sum of the places of lower
+// digits, those of its own in the chunks of the CTAs before, in the parts of the
+// warps before, and before it in its warp's part.  Counts go through the cluster's
+// shared memory.
+
+constexpr int kEmbedCluster = 16;
+constexpr int kEmbedSortThreads = 1024;
+constexpr int kEmbedSortWarps = kEmbedSortThreads / 32;
+constexpr int kEmbedDigits = 512;
+constexpr size_t kEmbedSortSmem = (size_t)(kEmbedSortWarps + 2) * kEmbedDigits * 4;
+
+struct EmbedDigits {
+    const EmbedBackArgs& a;
+    const uint32_t *keys, *slots;  // nullptr: the tokens themselves
+    int shift;
+
+    // Two words of place i; written by other CTAs of the cluster, so past the L1 cache.
+    __device__ __forceinline__ uint32_t key(int64_t i) const {
+        if (keys != nullptr) return (uint32_t)load_l2(reinterpret_cast<const int*>(keys + i));
+        const int64_t row = embed_row(a.ids, a.wide, i, a.rows);
+        return row >= 0 ? (uint32_t)row : (uint32_t)a.rows;
+    }
+    __device__ __forceinline__ uint32_t slot(int64_t i) const {
+        return slots != nullptr ? (uint32_t)load_l2(reinterpret_cast<const int*>(slots + i)) : (uint32_t)i;
+    }
+    __device__ __forceinline__ int digit(uint32_t key) const { return (int)(key >> shift) & ((1 << a.bits) - 1); }
+};
+
+__global__ void __launch_bounds__(kEmbedSortThreads) embed_sort_kernel(const EmbedBackArgs a) {
+    wait_for_stream();
+    extern __shared__ int s_next[];  // [warps][digits]: a warp's counts, then its next place less the CTA's first
+    __shared__ int s_part[kEmbedSortWarps];
+    int* s_count = s_next + kEmbedSortWarps * kEmbedDigits;
+    int* s_first = s_count + kEmbedDigits;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t ctas = cluster_size(), rank = cluster_rank();
+    const int64_t chunk = (a.n + ctas - 1) / ctas;
+    const int64_t lo = min((int64_t)rank * chunk, a.n), hi = min(lo + chunk, a.n);
+    const int64_t part = ((hi - lo + kEmbedSortWarps - 1) / kEmbedSortWarps + 31) / 32 * 32;
+    const int64_t wlo = min(lo + warp * part, hi), whi = min(wlo + part, hi);
+    int* next = s_next + warp * kEmbedDigits;
+    constexpr int U = 4;
+    for (int pass = 0; pass < a.passes; ++pass) {
+        // the last pass ends in keys and slots
+        const bool even = (a.passes - 1 - pass) % 2 == 0;
+        const EmbedDigits from{a, pass == 0 ? nullptr : even ? a.other_keys : a.keys,
+                               pass == 0 ? nullptr : even ? a.other_slots : a.slots, pass * a.bits};
+        uint32_t* to_keys = even ? a.keys : a.other_keys;
+        uint32_t* to_slots = even ? a.slots : a.other_slots;
+        for (int d = lane; d < kEmbedDigits; d += 32) next[d] = 0;
+        __syncwarp();
+        for (int64_t i0 = wlo + lane; i0 < whi; i0 += 32 * U) {
+            uint32_t key[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) key[u] = i0 + 32 * u < whi ? from.key(i0 + 32 * u) : 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + 32 * u < whi) atomicAdd(&next[from.digit(key[u])], 1);
+        }
+        __syncthreads();
+        if (threadIdx.x < kEmbedDigits) {
+            int run = 0;
+#pragma unroll 8
+            for (int w = 0; w < kEmbedSortWarps; ++w) {
+                const int c = s_next[w * kEmbedDigits + threadIdx.x];
+                s_next[w * kEmbedDigits + threadIdx.x] = run;
+                run += c;
+            }
+            s_count[threadIdx.x] = run;
+        }
+        if (ctas > 1) cluster_sync();
+        else __syncthreads();
+        int total = 0, before = 0, run = 0;
+        if (threadIdx.x < kEmbedDigits) {
+#pragma unroll 4
+            for (uint32_t r = 0; r < ctas; ++r) {
+                const int c = peer_word(s_count + threadIdx.x, r);
+                total += c;
+                before += r < rank ? c : 0;
+            }
+            run = total;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, run, d);
+                if (lane >= d) run += up;
+            }
+            if (lane == 31) s_part[warp] = run;
+        }
+        __syncthreads();
+        if (threadIdx.x < kEmbedDigits) {
+            int lower = 0;
+            for (int w = 0; w < warp; ++w) lower += s_part[w];
+            s_first[threadIdx.x] = lower + run - total + before;
+        }
+        __syncthreads();
+        const unsigned before_me = (1u << lane) - 1;
+        for (int64_t i0 = wlo; i0 < whi; i0 += 32 * U) {
+            uint32_t key[U], slot[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t i = i0 + 32 * u + lane;
+                key[u] = i < whi ? from.key(i) : 0;
+                slot[u] = i < whi ? from.slot(i) : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i0 + 32 * u >= whi) break;
+                const bool live = i0 + 32 * u + lane < whi;
+                const int g = from.digit(key[u]);
+                unsigned same = __ballot_sync(0xffffffffu, live);
+#pragma unroll
+                for (int bit = 0; bit < 9; ++bit) {
+                    const bool one = g >> bit & 1;
+                    same &= __ballot_sync(0xffffffffu, one) ^ (one ? 0u : 0xffffffffu);
+                }
+                const int place = __popc(same & before_me);
+                const int at = next[g] + place;
+                __syncwarp();
+                if (live && place == 0) next[g] = at + __popc(same);
+                __syncwarp();
+                if (live) {
+                    __stcg(to_keys + s_first[g] + at, key[u]);
+                    __stcg(to_slots + s_first[g] + at, slot[u]);
+                }
+            }
+        }
+        __threadfence();
+        if (ctas > 1) cluster_sync();  // what this pass wrote the next one reads; no CTA leaves, or counts anew, before
+        else __syncthreads();
+    }
+}
+
+// The same for few tokens, by all SMs and without a pass over digits: the place of
+// a token is the number of smaller ones and of equal ones before it.  A CTA counts
+// for 32 tokens, a lane each; its warps share out what they are compared with, which
+// lies in shared memory.
+constexpr int64_t kEmbedSmallMost = 8192;
+constexpr int kEmbedSmallThreads = 512;
+
+__global__ void __launch_bounds__(kEmbedSmallThreads) embed_sort_small_kernel(const EmbedBackArgs a) {
+    wait_for_stream();
+    extern __shared__ __align__(16) uint32_t s_key[];  // all keys, then the warps' counts
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (int)a.n, i0 = blockIdx.x * 32, i = i0 + lane;
+    const int whole = (n + 31) / 32 * 32;
+    for (int j = threadIdx.x; j < whole; j += kEmbedSmallThreads) {
+        const int64_t row = j < n ? embed_row(a.ids, a.wide, j, a.rows) : 0;
+        s_key[j] = j >= n ? 0xffffffffu : row >= 0 ? (uint32_t)row : (uint32_t)a.rows;  // past the end: smaller than none
+    }
+    __syncthreads();
+    const uint32_t mine = s_key[i];
+    int count = 0;
+    // 32 at a time: those before mine count when equal, those after do not
+    for (int b = warp; b < whole / 32; b += kEmbedSmallThreads / 32) {
+        const uint4* other = reinterpret_cast<const uint4*>(s_key + 32 * b);
+        if (32 * b == i0) {
+            for (int k = 0; k < 32; ++k) count += s_key[i0 + k] < mine || (s_key[i0 + k] == mine && k < lane);
+        } else {
+            const bool before = 32 * b < i0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint4 v = other[q];
+                if (before) count += (v.x <= mine) + (v.y <= mine) + (v.z <= mine) + (v.w <= mine);
+                else count += (v.x < mine) + (v.y < mine) + (v.z < mine) + (v.w < mine);
+            }
+        }
+    }
+    int* s_count = reinterpret_cast<int*>(s_key + whole);
+    s_count[threadIdx.x] = count;
+    __syncthreads();
+    if (warp == 0 && i < n) {
+        int place = 0;
+#pragma unroll
+        for (int w = 0; w < kEmbedSmallThreads / 32; ++w) place += s_count[w * 32 + lane];
+        a.keys[place] = mine;
+        a.slots[place] = (uint32_t)i;
+    }
+}
+
+// Sort keys for more tokens than one cluster sorts.
 __global__ void __launch_bounds__(256) embed_keys_kernel(const EmbedBackArgs a) {
     wait_for_stream();
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -104,6 +299,27 @@ __global__ void __launch_bounds__(256) embed_keys_kernel(const EmbedBackArgs a) 
     const int64_t row = embed_row(a.ids, a.wide, i, a.rows);
     a.keys[i] = row >= 0 ? (uint32_t)row : (uint32_t)a.rows;
     a.slots[i] = (uint32_t)i;
+}
+
+// ---- sums
+
+constexpr int kEmbedSumThreads = 128;
+constexpr int kEmbedSumRows = 16;  // rows of a warp in flight
+
+// Copies a lane's vector into its own place of shared memory, in the background
+// where the hardware has such copies (4, 8 and 16 bytes).
+template <typename V>
+__device__ __forceinline__ void copy_async(V* to, const V* from) {
+    constexpr int B = (int)sizeof(V);
+    if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+    else if constexpr (B >= 4) asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(to)), "l"(from), "n"(B) : "memory");
+    else *to = *from;
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most N of the groups committed last are on their way.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // First sorted place whose key is at least `key`, in [lo, hi].
@@ -116,60 +332,18 @@ __device__ __forceinline__ int64_t first_place(const uint32_t* keys, int64_t lo,
     return lo;
 }
 
-// A lane's columns of a tile: vectors of N values, 32 vectors a step, C of them.
-template <typename T, int N>
-struct EmbedLane {
-    static constexpr int kSteps = kEmbedTile / (32 * N);
-};
-
-// The sum of `count` sorted places' rows, in their order, for a lane's columns.
-// Two rows at a time are in flight.
-template <typename T, int N>
-__device__ __forceinline__ void sum_run(const EmbedBackArgs& a, int64_t at, int count, int column,
-                                        float (&sum)[kEmbedTile / 32]) {
-    constexpr int S = EmbedLane<T, N>::kSteps;
-    using V = ValueVec<T, N>;
+// The same for one key by a warp, which looks at 32 places at a time.
+__device__ __forceinline__ int64_t first_place_warp(const uint32_t* keys, int64_t lo, int64_t hi, uint32_t key) {
     const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int k = 0; k < kEmbedTile / 32; ++k) sum[k] = 0.0f;
-    for (int r = 0; r < count; ++r) {
-        const T* row = static_cast<const T*>(a.grad) + (int64_t)a.slots[at + r] * a.grad_stride + column;
-        V v[S];
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int c = (s * 32 + lane) * N;
-            if (column + c < a.width) v[s] = *reinterpret_cast<const V*>(row + c);
-            else
-#pragma unroll
-                for (int k = 0; k < N; ++k) v[s].v[k] = from_float<T>(0.0f);
-        }
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int k = 0; k < N; ++k) sum[s * N + k] += to_float(v[s].v[k]);
+    while (lo < hi) {
+        const int64_t step = (hi - lo + 31) / 32, probe = lo + lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, probe < hi && keys[probe] < key);
+        const int n = __popc(below);  // probes rise, so the first n of them are below
+        if (n == 0) return lo;
+        hi = min(hi, lo + n * step);
+        lo = lo + (n - 1) * step + 1;
     }
-}
-
-// A row of the table's gradient from its sum.
-template <typename O, int N>
-__device__ __forceinline__ void store_row(const EmbedBackArgs& a, uint32_t row, int column, int steps,
-                                          const float (&sum)[kEmbedTile / 32]) {
-    const int lane = threadIdx.x & 31;
-    using V = ValueVec<O, N>;
-    O* out = static_cast<O*>(a.grad_table) + (int64_t)row * a.table_stride + column;
-#pragma unroll
-    for (int s = 0; s < kEmbedTile / (32 * N); ++s) {
-        const int c = (s * 32 + lane) * N;
-        if (column + c >= a.width) continue;
-        V v;
-        if (a.accumulate) v = *reinterpret_cast<const V*>(out + c);
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const float x = sum[s * N + k] * a.scale;
-            v.v[k] = from_float<O>(a.accumulate ? to_float(v.v[k]) + x : x);
-        }
-        *reinterpret_cast<V*>(out + c) = v;
-    }
+    return lo;
 }
 
 // The slot of a piece's sum in `partial`: pieces start at multiples of
@@ -177,112 +351,224 @@ __device__ __forceinline__ void store_row(const EmbedBackArgs& a, uint32_t row, 
 // one that starts a long run start in the same kEmbedPiece places.
 __device__ __forceinline__ int64_t piece_slot(int64_t at, bool first) { return 2 * (at / kEmbedPiece) + first; }
 
-// Sums: a warp looks after `window` sorted places and the column tiles of one
-// tile; for each place that starts a run of equal tokens, or a further piece of a
-// long run, it sums the run (or the piece) in order.  Short runs go straight to
-// the table, pieces of long ones to `partial`.
-// Zeros: rows that no token asks for, found by a search of the sorted tokens.
-template <typename T, typename O, int N>
-__global__ void __launch_bounds__(kEmbedBackThreads) embed_sum_kernel(const EmbedBackArgs a) {
-    wait_for_stream();
-    const int lane = threadIdx.x & 31;
-    const int64_t warp = (int64_t)blockIdx.x * (kEmbedBackThreads / 32) + (threadIdx.x >> 5);
-    if ((int64_t)blockIdx.x >= a.sum_ctas) {
-        const int64_t zero = warp - a.sum_ctas * (kEmbedBackThreads / 32);
-        const int64_t lo = zero * a.zero_rows, mine = lo + lane;
-        if (lo >= a.rows) return;
-        bool absent = false;
-        if (lane < a.zero_rows && mine < a.rows) {
-            const int64_t at = first_place(a.keys, 0, a.n, (uint32_t)mine);
-            absent = at == a.n || a.keys[at] != (uint32_t)mine;
-        }
-        unsigned todo = __ballot_sync(0xffffffffu, absent);
-        using V = ValueVec<O, N>;
-        V none;
+// N sums of a lane to a row of the table's gradient (scaled), or as they are.
+template <typename O, int N>
+__device__ __forceinline__ void store_sums(const EmbedBackArgs& a, uint32_t row, int column, const float (&sum)[N]) {
+    constexpr int W = N * (int)sizeof(O) > 16 ? 16 / (int)sizeof(O) : N;  // values of a store
+    using V = ValueVec<O, W>;
+    O* out = static_cast<O*>(a.grad_table) + (int64_t)row * a.table_stride + column;
 #pragma unroll
-        for (int k = 0; k < N; ++k) none.v[k] = from_float<O>(0.0f);
-        while (todo != 0) {
-            const int r = __ffs(todo) - 1;
-            todo &= todo - 1;
-            O* out = static_cast<O*>(a.grad_table) + (lo + r) * a.table_stride;
-            for (int c = lane * N; c < a.width; c += 32 * N) *reinterpret_cast<V*>(out + c) = none;
+    for (int p = 0; p < N; p += W) {
+        V v;
+        if (a.accumulate) v = *reinterpret_cast<const V*>(out + p);
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const float x = sum[p + k] * a.scale;
+            v.v[k] = from_float<O>(a.accumulate ? to_float(v.v[k]) + x : x);
         }
+        *reinterpret_cast<V*>(out + p) = v;
+    }
+}
+
+// Zeros in those rows of a warp's share that no token asks for.
+template <typename O, int N>
+__device__ __forceinline__ void zero_rows(const EmbedBackArgs& a, int64_t warp) {
+    constexpr int W = N * (int)sizeof(O) > 16 ? 16 / (int)sizeof(O) : N;  // values of a store
+    using V = ValueVec<O, W>;
+    const int lane = threadIdx.x & 31;
+    const int64_t lo = warp * a.zero_rows, mine = lo + lane;
+    if (lo >= a.rows) return;
+    // the sorted tokens from the first of these rows on: mostly few, or none
+    const int64_t at = first_place_warp(a.keys, 0, a.n, (uint32_t)lo);
+    const uint32_t key = at + lane < a.n ? a.keys[at + lane] : 0xffffffffu;
+    const uint32_t there = __reduce_or_sync(0xffffffffu, key - (uint32_t)lo < 32 ? 1u << (key - (uint32_t)lo) : 0u);
+    bool absent = lane < a.zero_rows && mine < a.rows && !(there >> lane & 1);
+    if (__shfl_sync(0xffffffffu, key, 31) < lo + a.zero_rows && absent) {  // more than 32 tokens ask for them
+        const int64_t p = first_place(a.keys, at, a.n, (uint32_t)mine);
+        absent = p == a.n || a.keys[p] != (uint32_t)mine;
+    }
+    V none;
+#pragma unroll
+    for (int k = 0; k < W; ++k) none.v[k] = from_float<O>(0.0f);
+    for (unsigned todo = __ballot_sync(0xffffffffu, absent); todo != 0; todo &= todo - 1) {
+        O* out = static_cast<O*>(a.grad_table) + (lo + __ffs(todo) - 1) * a.table_stride;
+        for (int c = lane * W; c < a.width; c += 32 * W) store_streaming(reinterpret_cast<V*>(out + c), none);
+    }
+}
+
+// A warp looks after the pieces that start in its window of sorted places, for a
+// tile of 32 N columns.  A piece is a run of equal tokens, or up to kEmbedPiece
+// places of a longer one, counted from its start; so those of a window are
+// neighbours, and the warp streams their rows, 16 in flight through shared memory
+// (each lane copies and reads its own vectors: no barrier), adding each to the sum
+// in its order and putting the sum away where a piece ends: to the table, or, for
+// pieces of a longer run, to `partial`.
+//
+// Zeros: a warp searches the sorted tokens for its rows.
+//
+// Bound by memory.
+template <typename T, typename O, int N>
+__global__ void __launch_bounds__(kEmbedSumThreads) embed_sum_kernel(const EmbedBackArgs a) {
+    wait_for_stream();
+    if ((int64_t)blockIdx.x >= a.sum_ctas) {
+        zero_rows<O, N>(a, ((int64_t)blockIdx.x - a.sum_ctas) * (kEmbedSumThreads / 32) + (threadIdx.x >> 5));
         return;
     }
-    const int64_t w = warp / a.tiles;
-    const int column = (int)(warp - w * a.tiles) * kEmbedTile;
-    const int64_t lo = w * a.window, mine = lo + lane;
+    using V = ValueVec<T, N>;
+    constexpr int D = kEmbedSumRows;
+    __shared__ V s_ring[kEmbedSumThreads / 32][D][32];
+    const int lane = threadIdx.x & 31;
+    V* ring = &s_ring[threadIdx.x >> 5][0][lane];
+    const int64_t warp = (int64_t)blockIdx.x * (kEmbedSumThreads / 32) + (threadIdx.x >> 5);
+    const int64_t w = warp / a.tiles, lo = w * a.window;
     if (lo >= a.n) return;
-    // does a piece start at this lane's place, and is it its run's first?
-    uint32_t key = (uint32_t)a.rows;
-    bool starts = false, first = false;
-    if (lane < a.window && mine < a.n) {
-        key = a.keys[mine];
-        first = mine == 0 || a.keys[mine - 1] != key;
-        starts = first;
-        if (!first && mine >= kEmbedPiece && a.keys[mine - kEmbedPiece] == key)
-            starts = (mine - first_place(a.keys, 0, mine, key)) % kEmbedPiece == 0;
-        if (key >= (uint32_t)a.rows) starts = false;
-    }
-    unsigned todo = __ballot_sync(0xffffffffu, starts);
-    const unsigned firsts = __ballot_sync(0xffffffffu, first);
-    while (todo != 0) {
-        const int r = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int64_t at = lo + r;
-        const uint32_t row = __shfl_sync(0xffffffffu, key, r);
-        // places from here on with the same token, kEmbedPiece + 1 at most
-        int count = 0;
+    const int column = (int)(warp - w * a.tiles) * (32 * N) + lane * N;
+    const bool inside = column < a.width;
+    const T* grad = static_cast<const T*>(a.grad) + column;
+    float sum[N];
+    int64_t at = -1;  // where the piece being summed starts, its token, and whether it starts its run
+    uint32_t row = 0;
+    bool run_start = false;
 #pragma unroll
-        for (int k = 0; k < kEmbedPiece; k += 32) {
-            if (count != k) break;
-            const int64_t p = at + k + lane;
-            const unsigned same = __ballot_sync(0xffffffffu, p < a.n && a.keys[p] == row);
-            count += same == 0xffffffffu ? 32 : __ffs(~same) - 1;
-        }
-        const bool is_first = firsts >> r & 1;
-        const bool more = count == kEmbedPiece && at + kEmbedPiece < a.n && a.keys[at + kEmbedPiece] == row;
-        float sum[kEmbedTile / 32];
-        sum_run<T, N>(a, at, count, column, sum);
-        if (is_first && !more) {
-            store_row<O, N>(a, row, column, 0, sum);
+    for (int n = 0; n < N; ++n) sum[n] = 0.0f;
+    auto put_away = [&](uint32_t next_key) {
+        if (at < 0 || !inside) return;
+        if (run_start && next_key != row) {
+            store_sums<O, N>(a, row, column, sum);
         } else {
-            float* out = a.partial + piece_slot(at, is_first) * a.width + column;
+            float* out = a.partial + piece_slot(at, run_start) * a.width + column;
 #pragma unroll
-            for (int s = 0; s < EmbedLane<T, N>::kSteps; ++s) {
-                const int c = (s * 32 + lane) * N;
+            for (int k = 0; k < N; ++k) out[k] = sum[k];
+        }
+    };
+    for (int64_t base = lo;; base += 32) {
+        const int64_t mine = base + lane;
+        uint32_t key = 0xffffffffu, slot = 0;
+        bool starts = false, first = false;
+        if (mine < a.n) {
+            key = a.keys[mine];
+            slot = a.slots[mine];
+            first = mine == 0 || a.keys[mine - 1] != key;
+            starts = first;
+        }
+        const unsigned outside = __ballot_sync(0xffffffffu, key >= (uint32_t)a.rows);
+        const unsigned firsts = __ballot_sync(0xffffffffu, first);
+        // Further pieces of a long run among these places: only of the run that the first
+        // one is in the midst of (one that starts here has its next piece 32 places on).
+        const uint32_t key0 = __shfl_sync(0xffffffffu, key, 0);
+        if (!(firsts & 1) && base >= kEmbedPiece - 31 && key0 < (uint32_t)a.rows) {
+            const int64_t back = max(base - kEmbedPiece + 1, (int64_t)0);
+            // where that run started, if it was less than a piece ago, or else by a search
+            const unsigned there = __ballot_sync(0xffffffffu, back + lane < base && a.keys[back + lane] != key0);
+            int64_t run;
+            if (there != 0) run = back + 32 - __clz(there);
+            else run = first_place_warp(a.keys, 0, back, key0);
+            if (mine < a.n && key == key0 && !first) starts = (mine - run) % kEmbedPiece == 0;
+        }
+        const unsigned start = __ballot_sync(0xffffffffu, starts);
+        const unsigned window = base > lo ? 0u : a.window >= 32 ? 0xffffffffu : (1u << a.window) - 1;
+        const unsigned stops = (start & ~window) | outside;
+        const int stop = stops != 0 ? __ffs(stops) - 1 : 32;
+        int r = 0;
+        if (at < 0) {
+            r = (start & window & ~outside) != 0 ? __ffs(start & window & ~outside) - 1 : 32;
+            if (r > stop || r == 32) return;  // no piece starts here
+        }
+        const int count = stop - r;
+        auto fetch = [&](int i) {
+            const uint32_t from = __shfl_sync(0xffffffffu, slot, (r + i) & 31);
+            if (i < count && inside) copy_async(ring + (i % D) * 32, reinterpret_cast<const V*>(grad + (int64_t)from * a.grad_stride));
+            copy_commit();
+        };
+        for (int i = 0; i < D; ++i) fetch(i);
+        for (int i = 0; i < count; ++i) {
+            copy_wait<D - 1>();
+            const V v = ring[(i % D) * 32];
+            const uint32_t k = __shfl_sync(0xffffffffu, key, r + i);
+            if (start >> (r + i) & 1) {
+                put_away(k);
+                at = base + r + i, row = k, run_start = firsts >> (r + i) & 1;
 #pragma unroll
-                for (int k = 0; k < N; ++k)
-                    if (column + c + k < a.width) out[c + k] = sum[s * N + k];
+                for (int n = 0; n < N; ++n) sum[n] = 0.0f;
             }
+            if (inside) {
+#pragma unroll
+                for (int n = 0; n < N; ++n) sum[n] += to_float(v.v[n]);
+            }
+            fetch(i + D);
+        }
+        if (stop < 32) {
+            put_away(__shfl_sync(0xffffffffu, key, stop));
+            return;
         }
     }
 }
 
 // Long runs: the pieces' sums in order.  A run of more than kEmbedPiece places
-// holds a multiple of kEmbedPiece after its start; the first of them is its CTA.
+// holds a multiple of kEmbedPiece after its start; the first of them is the one
+// that its CTA looks at.  The four warps take a quarter of the pieces each, and
+// their sums are added in order.
+constexpr int kEmbedJoinThreads = 128;
+constexpr int kEmbedJoinColumns = 128;  // four to a lane
+constexpr int kEmbedJoinPlaces = 8;     // multiples of kEmbedPiece that a CTA looks at
+
 template <typename O>
-__global__ void __launch_bounds__(256) embed_join_kernel(const EmbedBackArgs a) {
+__global__ void __launch_bounds__(kEmbedJoinThreads) embed_join_kernel(const EmbedBackArgs a, int tiles) {
     wait_for_stream();
-    const int64_t q = blockIdx.x / a.tiles;
-    const int column = (int)(blockIdx.x - q * a.tiles) * kEmbedTile;
-    const int64_t at = (q + 1) * kEmbedPiece;
-    if (at >= a.n) return;
-    const uint32_t key = a.keys[at];
-    if (key >= (uint32_t)a.rows || a.keys[at - 1] != key) return;
-    const int64_t lo = at - kEmbedPiece;
-    if (lo > 0 && a.keys[lo] == key && a.keys[lo - 1] == key) return;  // an earlier multiple lies inside the run
-    int64_t start = first_place(a.keys, lo, at, key);
-    const int64_t end = first_place(a.keys, at, a.n, key + 1);
-    if (end - start <= kEmbedPiece) return;
-    const int64_t pieces = (end - start + kEmbedPiece - 1) / kEmbedPiece;
-    for (int c = column + (int)threadIdx.x; c < min(column + kEmbedTile, a.width); c += 256) {
-        float sum = a.partial[piece_slot(start, true) * a.width + c];
-        for (int64_t p = 1; p < pieces; ++p)
-            sum += a.partial[piece_slot(start + p * kEmbedPiece, false) * a.width + c];
-        O* out = static_cast<O*>(a.grad_table) + (int64_t)key * a.table_stride + c;
-        sum *= a.scale;
-        *out = from_float<O>(a.accumulate ? to_float(*out) + sum : sum);
+    __shared__ float s_sum[kEmbedJoinThreads / 32][kEmbedJoinColumns];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t group = blockIdx.x / tiles;
+    const int column = (int)(blockIdx.x - group * tiles) * kEmbedJoinColumns;
+    bool mine = false;
+    if (lane < kEmbedJoinPlaces) {
+        const int64_t at = (group * kEmbedJoinPlaces + lane + 1) * kEmbedPiece, lo = at - kEmbedPiece;
+        if (at < a.n) {
+            const uint32_t key = a.keys[at], last = a.keys[at - 1], low = a.keys[lo];
+            const uint32_t lower = lo > 0 ? a.keys[lo - 1] : 0xffffffffu;
+            mine = key < (uint32_t)a.rows && last == key && !(low == key && lower == key);
+        }
+    }
+    for (unsigned todo = __ballot_sync(0xffffffffu, mine); todo != 0; todo &= todo - 1) {
+        const int64_t at = (group * kEmbedJoinPlaces + __ffs(todo)) * kEmbedPiece;
+        const uint32_t key = a.keys[at];
+        const int64_t start = first_place_warp(a.keys, at - kEmbedPiece, at, key);
+        const int64_t end = first_place_warp(a.keys, at, a.n, key + 1);
+        if (end - start <= kEmbedPiece) continue;
+        const int64_t pieces = (end - start + kEmbedPiece - 1) / kEmbedPiece, share = (pieces + 3) / 4;
+        const int64_t p0 = min(warp * share, pieces), p1 = min(p0 + share, pieces);
+        // piece p starts in the block of kEmbedPiece places p blocks after the run's start
+        const float* first = a.partial + piece_slot(start, true) * a.width;
+        const float* others = a.partial + piece_slot(start, false) * a.width;
+        const int64_t step = 2 * (int64_t)a.width;
+        float sum[4] = {};
+        constexpr int U = 4;
+        for (int64_t p = p0; p < p1; p += U) {
+            float v[U][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int c = column + lane + 32 * k;
+                    v[u][k] = p + u < p1 && c < a.width ? (p + u == 0 ? first : others + (p + u) * step)[c] : 0.0f;
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sum[k] += v[u][k];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s_sum[warp][lane + 32 * k] = sum[k];
+        __syncthreads();
+        const int c = column + (int)threadIdx.x;
+        if (c < a.width) {
+            float total = s_sum[0][threadIdx.x];
+#pragma unroll
+            for (int w = 1; w < kEmbedJoinThreads / 32; ++w) total += s_sum[w][threadIdx.x];
+            O* out = static_cast<O*>(a.grad_table) + (int64_t)key * a.table_stride + c;
+            total *= a.scale;
+            *out = from_float<O>(a.accumulate ? to_float(*out) + total : total);
+        }
+        __syncthreads();
     }
 }
 

@@ -4,6 +4,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include "select_common.cuh"
@@ -15,8 +16,17 @@ constexpr int kExpertMaxPicks = 32;
 constexpr int kExpertMaxExperts = 1024;
 constexpr int kExpertWarps = 8;
 constexpr int kExpertRows = 16;    // weight rows of a CTA: the height of one matrix instruction
-constexpr int kExpertUnroll = 4;   // steps of 32 columns whose weights are in flight
 constexpr int kExpertCluster = 8;
+
+// 16 bytes that other CTAs of this launch have written (past the L1 cache).
+__device__ __forceinline__ uint4 load_l2(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(__cvta_generic_to_global(p))
+                 : "memory");
+    return v;
+}
 
 enum ExpertAct { kActSilu = 0, kActGelu = 1, kActRelu = 2 };
 
@@ -30,8 +40,9 @@ struct ExpertArgs {
     int64_t x_stride, out_stride;
     int64_t up_expert, up_row, gate_expert, gate_row, down_expert, down_row;  // strides in values
     int tokens, picks, slots, experts, hidden, inner, inner_pad, act;
-    int by_slot;  // first kernel: CTAs by slot (the first of its expert works), not by expert
-    int parts;    // second kernel: pieces of an expert's columns
+    int by_slot;  // expert_up_kernel: CTAs by slot (the first of its expert works), not by expert
+    int parts;    // expert_down_kernel: pieces of an expert's columns
+    float* each;  // expert_layer_kernel: [slots][hidden], what each slot adds to its token
 };
 
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -57,21 +68,14 @@ __device__ __forceinline__ void mma_step(float (&d)[4], const uint4& a, const ui
     mma_16x8x16(d, a.z, b.z, a.w, b.w, x.z, x.w, T{});
 }
 
-// 8 values of a row of `columns` from column k on, zeros past its end.
-// VEC: rows are aligned to 16 bytes and columns a multiple of 8.
-template <typename T, bool VEC>
+// 8 values of a row of `columns` from column k on, zeros past its end, one by one.
+template <typename T>
 __device__ __forceinline__ uint4 load8(const T* row, int k, int columns) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (VEC) {
-        if (k < columns) v = *reinterpret_cast<const uint4*>(row + k);
-    } else {
-        const unsigned short* p = reinterpret_cast<const unsigned short*>(row) + k;
-        uint32_t h[8];
+    const unsigned short* p = reinterpret_cast<const unsigned short*>(row) + k;
+    uint32_t h[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = k + i < columns ? p[i] : 0;
-        v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-    }
-    return v;
+    for (int i = 0; i < 8; ++i) h[i] = k + i < columns ? p[i] : 0;
+    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
 }
 
 // The next slots, from `from` on, whose id is e: up to `most` of them into list (in
@@ -104,17 +108,17 @@ __device__ __forceinline__ float activate(float x, int act) {
     return x > 0.0f || x != x ? x : 0.0f;
 }
 
-// First kernel: the activations act(gate x) * (up x), or act(up x), of every slot
-// whose id is an expert.  A CTA takes 16 rows of one expert, its eight warps every
-// eighth step of 32 columns of them, and its tokens 8 NT at a time; the warps' sums
-// meet in shared memory.  With at most a few tokens to an expert the weights'
-// bytes bound it: each is read once, straight from memory to the instruction's
-// registers, 16 bytes a lane, and the tokens' rows come from the caches.  The
-// tensor work is small beside that, so mma.sync does.
-template <typename T, bool GATED, int NT, bool VEC>
+// ---- rows that no 16-byte copy can take (odd sizes, strides or addresses): two
+// kernels whose lanes load value by value
+
+// First the activations act(gate x) * (up x), or act(up x), of every slot whose id
+// is an expert.  A CTA takes 16 rows of one expert, its eight warps every eighth
+// step of 32 columns of them, and its tokens 8 NT at a time; the warps' sums meet
+// in shared memory.
+template <typename T, bool GATED, int NT>
 __global__ void __launch_bounds__(kExpertWarps * 32) expert_up_kernel(const ExpertArgs a) {
     wait_for_stream();
-    constexpr int MATS = GATED ? 2 : 1, COLS = 8 * NT, U = VEC ? kExpertUnroll : 1;
+    constexpr int MATS = GATED ? 2 : 1, COLS = 8 * NT;
     extern __shared__ __align__(16) float s_sum[];  // [warps][MATS][COLS][16]
     __shared__ uint16_t s_list[COLS];
     __shared__ int s_count, s_from;
@@ -148,25 +152,18 @@ __global__ void __launch_bounds__(kExpertWarps * 32) expert_up_kernel(const Expe
             tokens[n] = c < count ? static_cast<const T*>(a.x) + (int64_t)(s_list[c] / a.picks) * a.x_stride : nullptr;
         }
         float d[MATS][NT][4] = {};
-        for (int s0 = warp; s0 < steps; s0 += kExpertWarps * U) {
-            uint4 w[U][2 * MATS];
+        for (int s = warp; s < steps; s += kExpertWarps) {
+            const int k = s * 32 + 8 * t;
+            uint4 w[2 * MATS];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int k = (s0 + u * kExpertWarps) * 32 + 8 * t;
+            for (int m = 0; m < 2 * MATS; ++m) w[m] = load8<T>(rows[m], k, a.hidden);
 #pragma unroll
-                for (int m = 0; m < 2 * MATS; ++m) w[u][m] = load8<T, VEC>(rows[m], k, a.hidden);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int k = (s0 + u * kExpertWarps) * 32 + 8 * t;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (8 * n >= count) break;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (tokens[n] != nullptr) x = load8<T, VEC>(tokens[n], k, a.hidden);
-                    mma_step<T>(d[0][n], w[u][0], w[u][1], x);
-                    if (GATED) mma_step<T>(d[MATS - 1][n], w[u][2 * MATS - 2], w[u][2 * MATS - 1], x);
-                }
+            for (int n = 0; n < NT; ++n) {
+                if (8 * n >= count) break;
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (tokens[n] != nullptr) x = load8<T>(tokens[n], k, a.hidden);
+                mma_step<T>(d[0][n], w[0], w[1], x);
+                if (GATED) mma_step<T>(d[MATS - 1][n], w[2 * MATS - 2], w[2 * MATS - 1], x);
             }
         }
         // lane's sums: rows g, g and g + 8, g + 8, tokens 2t, 2t + 1
@@ -202,15 +199,15 @@ __global__ void __launch_bounds__(kExpertWarps * 32) expert_up_kernel(const Expe
     }
 }
 
-// Second kernel: y = sum over a token's slots of weight * down[e] a.  A cluster
+// Then y = sum over a token's slots of weight * down[e] a.  A cluster
 // takes 16 rows of the output; its warps share out the experts that any slot asks
 // for (cut into `parts` pieces of their columns where there are few), each adding
 // what its items give to its own sums of all tokens in shared memory; these are
 // added in a fixed order, over the CTAs of the cluster through its shared memory.
-template <typename T, bool VEC>
+template <typename T>
 __global__ void __launch_bounds__(kExpertWarps * 32) expert_down_kernel(const ExpertArgs a) {
     wait_for_stream();
-    constexpr int U = VEC ? kExpertUnroll : 1, NT = 2, COLS = 8 * NT;
+    constexpr int NT = 2, COLS = 8 * NT;
     extern __shared__ __align__(16) float s_sum[];  // [warps][tokens][16]
     __shared__ float s_tile[kExpertWarps][COLS][kExpertRows];
     __shared__ uint16_t s_list[kExpertWarps][COLS];
@@ -259,25 +256,16 @@ __global__ void __launch_bounds__(kExpertWarps * 32) expert_down_kernel(const Ex
                 low[n] = c < count ? static_cast<const T*>(a.low) + (int64_t)s_list[warp][c] * a.inner_pad : nullptr;
             }
             float d[NT][4] = {};
-            for (int s0 = s_lo; s0 < s_hi; s0 += U) {
-                uint4 w[U][2];
+            for (int s = s_lo; s < s_hi; ++s) {
+                const int k = s * 32 + 8 * t;
+                const uint4 w0 = load8<T>(row0, k, a.inner), w1 = load8<T>(row1, k, a.inner);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int k = s0 + u < s_hi ? (s0 + u) * 32 + 8 * t : a.inner;
-                    w[u][0] = load8<T, VEC>(row0, k, a.inner);
-                    w[u][1] = load8<T, VEC>(row1, k, a.inner);
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int k = s0 + u < s_hi ? (s0 + u) * 32 + 8 * t : a.inner;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (8 * n >= count) break;
-                        uint4 h = make_uint4(0, 0, 0, 0), l = h;
-                        if (high[n] != nullptr) h = load8<T, VEC>(high[n], k, a.inner), l = load8<T, VEC>(low[n], k, a.inner);
-                        mma_step<T>(d[n], w[u][0], w[u][1], h);
-                        mma_step<T>(d[n], w[u][0], w[u][1], l);
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    if (8 * n >= count) break;
+                    uint4 h = make_uint4(0, 0, 0, 0), l = h;
+                    if (high[n] != nullptr) h = load8<T>(high[n], k, a.inner), l = load8<T>(low[n], k, a.inner);
+                    mma_step<T>(d[n], w0, w1, h);
+                    mma_step<T>(d[n], w0, w1, l);
                 }
             }
 #pragma unroll
@@ -312,6 +300,320 @@ __global__ void __launch_bounds__(kExpertWarps * 32) expert_down_kernel(const Ex
         if (row < a.hidden) static_cast<T*>(a.out)[token * a.out_stride + row] = from_float<T>(y);
     }
     if (ctas > 1) cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+// ---- the layer in one launch
+//
+// With a few tokens to an expert the weights' bytes bound the layer: each is to be
+// read once, at the memory's rate.  Two CTAs an SM, all at once (a cooperative
+// launch), take items of 16 or 32 weight rows of one expert in turn; a block of an
+// item is 1024 columns, of which each of the eight warps has every eighth step of
+// 32.  A lane loads its 16 bytes of the rows straight into the registers that the
+// tensor instructions take (16 rows by 8 tokens; mma.sync: at 64 tokens the tensor
+// work is a few percent of what it can do, and 8 columns waste least), all of a
+// block at once, and the next block's before the sums of this one are put together
+// in shared memory: 64 KB a CTA are on their way most of the time.
+// (Rings in shared memory were slower: filled by bulk copies of 512-byte pieces of
+// rows, 90 cycles apiece, the layer took four times as long, by 16-byte copies of
+// producer warps 327 us against 500 first and 2xx here.)
+//
+// First all items of the up (and gate) products, then, after a barrier of the
+// grid, those of the down products, whose first weights are loaded before the
+// barrier; each slot's products go to `each`, and after another barrier a token's
+// slots are added in their order.
+
+constexpr int kLayerSteps = 4;                                     // of a warp in a block
+constexpr int kLayerColumns = 32 * kExpertWarps * kLayerSteps;     // of a block
+constexpr int kLayerThreads = kExpertWarps * 32;
+
+struct LayerShared {
+    uint16_t order[kExpertMaxTokens * kExpertMaxPicks];  // the slots, by expert
+    uint16_t expert[kExpertMaxExperts];                  // the experts asked for, rising
+    uint16_t start[kExpertMaxExperts + 1];               // and where their slots start
+    int count[kExpertMaxExperts];
+    int experts;
+};
+
+// All threads of the grid.
+__device__ __noinline__ void layer_barrier() { cooperative_groups::this_grid().sync(); }
+
+// One of the two products: its weights, their shape and the rows that they meet.
+template <typename T, bool SECOND, bool GATED, int TILES>
+struct LayerProduct {
+    const ExpertArgs& a;
+    static constexpr int kMats = GATED ? 2 : 1;       // matrices that give 16 TILES / kMats rows each
+    static constexpr int kRows = 16 * TILES / kMats;  // rows of the result in an item
+    static constexpr int kSets = SECOND ? 2 : 1;      // rows of a token
+    static constexpr bool kSecond = SECOND;
+    __device__ __forceinline__ int columns() const { return SECOND ? a.inner : a.hidden; }
+    __device__ __forceinline__ int result() const { return SECOND ? a.hidden : a.inner; }
+    __device__ __forceinline__ int64_t row_stride(int m) const { return SECOND ? a.down_row : m == 0 ? a.up_row : a.gate_row; }
+    __device__ __forceinline__ const T* expert(int m, int e) const {
+        if (SECOND) return static_cast<const T*>(a.down) + e * a.down_expert;
+        return m == 0 ? static_cast<const T*>(a.up) + e * a.up_expert : static_cast<const T*>(a.gate) + e * a.gate_expert;
+    }
+    __device__ __forceinline__ const T* token(int slot) const {
+        if (!SECOND) return static_cast<const T*>(a.x) + slot / a.picks * a.x_stride;
+        return static_cast<const T*>(a.high) + (int64_t)slot * a.inner_pad;
+    }
+};
+
+// A warp's way through the blocks of a product.
+template <typename T, int NT, int TILES, typename P>
+struct LayerWork {
+    static constexpr int COLS = 8 * NT, S = kLayerSteps;
+    static constexpr bool kAhead = NT == 1;  // the tokens' rows are loaded with the weights (with more there is no room)
+    const P& p;
+    const LayerShared& s;
+    const int tiles, items, columns;
+    int item, tile, expert, q, end, c;  // the block: first slot in order, those of its expert, first column
+    const T* rows[TILES];               // this lane's, in the tiles, at its columns of the first step
+    const T* tokens[NT];
+    uint4 w[S][TILES][2], x[kAhead ? S : 1][NT][P::kSets];
+
+    __device__ __forceinline__ LayerWork(const P& product, const LayerShared& shared)
+        : p(product), s(shared), tiles((product.result() + P::kRows - 1) / P::kRows), items(shared.experts * tiles),
+          columns(product.columns()) {
+        item = (int)blockIdx.x;
+        if (here()) start_item();
+    }
+    __device__ __forceinline__ int lane_column() const { return 32 * (int)(threadIdx.x >> 5) + 8 * (int)(threadIdx.x & 3); }
+    __device__ __forceinline__ bool here() const { return item < items; }
+    __device__ __forceinline__ bool last_columns() const { return c + kLayerColumns >= columns; }
+    __device__ __forceinline__ int count() const { return min(COLS, end - q); }
+    __device__ __forceinline__ void start_item() {
+        const int k = item / tiles;
+        tile = item - k * tiles, expert = s.expert[k], q = s.start[k], end = s.start[k + 1], c = 0;
+        const int g = (int)(threadIdx.x & 31) >> 2;
+#pragma unroll
+        for (int m = 0; m < TILES; ++m) {  // rows past the matrix's end are its last one again: they are not stored
+            const int row = min(tile * P::kRows + (P::kMats == 1 ? 16 * m : 0) + g, p.result() - 1);
+            const int mat = P::kMats == 1 ? 0 : m;
+            rows[m] = p.expert(mat, expert) + row * p.row_stride(mat) + lane_column();
+        }
+        start_tokens();
+    }
+    __device__ __forceinline__ void start_tokens() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int i = q + 8 * n + ((int)(threadIdx.x & 31) >> 2);
+            tokens[n] = i < end && 8 * n < COLS ? p.token(s.order[i]) + lane_column() : nullptr;
+        }
+    }
+    __device__ __forceinline__ void next() {
+        c += kLayerColumns;
+        if (c < columns) return;
+        c = 0, q += COLS;
+        if (q < end) {
+            start_tokens();
+            return;
+        }
+        item += (int)gridDim.x;
+        if (here()) start_item();
+    }
+    // From a lane's row to the one 8 below it, or 0 where that is past the end.
+    __device__ __forceinline__ int64_t second_row(int m) const {
+        const int row = tile * P::kRows + (P::kMats == 1 ? 16 * m : 0) + ((int)(threadIdx.x & 31) >> 2);
+        return row + 8 < p.result() ? 8 * p.row_stride(P::kMats == 1 ? 0 : m) : 0;
+    }
+    __device__ __forceinline__ void load_weights() {
+        const int left = columns - c - lane_column();
+#pragma unroll
+        for (int m = 0; m < TILES; ++m) {
+            const int64_t below = second_row(m);
+#pragma unroll
+            for (int u = 0; u < S; ++u) {
+                const int k = u * 32 * kExpertWarps;
+                w[u][m][0] = w[u][m][1] = make_uint4(0, 0, 0, 0);
+                if (k < left) {
+                    w[u][m][0] = load_once(reinterpret_cast<const uint4*>(rows[m] + c + k));
+                    w[u][m][1] = load_once(reinterpret_cast<const uint4*>(rows[m] + below + c + k));
+                }
+            }
+        }
+    }
+    // Behind the barrier of the grid h is there; other SMs wrote it, so past the L1 cache.
+    __device__ __forceinline__ uint4 load_token(int n, int set, int k) const {
+        if (!P::kSecond) return *reinterpret_cast<const uint4*>(tokens[n] + k);
+        const T* from = tokens[n] + k + (set == 0 ? 0 : static_cast<const T*>(p.a.low) - static_cast<const T*>(p.a.high));
+        return load_l2(reinterpret_cast<const uint4*>(from));
+    }
+    __device__ __forceinline__ void load_tokens(int u, uint4 (&to)[NT][P::kSets]) const {
+        const int k = c + u * 32 * kExpertWarps;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int set = 0; set < P::kSets; ++set) {
+                to[n][set] = make_uint4(0, 0, 0, 0);
+                if (tokens[n] != nullptr && k + lane_column() < columns) to[n][set] = load_token(n, set, k);
+            }
+    }
+    __device__ __forceinline__ void load_all_tokens() {
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int u = 0; u < S; ++u) load_tokens(u, x[u]);
+        }
+    }
+    __device__ __forceinline__ void multiply(float (&d)[TILES][NT][4]) {
+        const int warp_column = c + 32 * (int)(threadIdx.x >> 5), n_here = count();
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+            if (warp_column + u * 32 * kExpertWarps >= columns) break;
+            if constexpr (!kAhead) load_tokens(u, x[0]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (8 * n >= n_here) break;
+#pragma unroll
+                for (int set = 0; set < P::kSets; ++set)
+#pragma unroll
+                    for (int m = 0; m < TILES; ++m) mma_step<T>(d[m][n], w[u][m][0], w[u][m][1], x[kAhead ? u : 0][n][set]);
+            }
+        }
+    }
+};
+
+// All blocks of a product; done(slot in order, first row, sums of the TILES tiles)
+// takes an item's sums.  The first block's weights are there.
+template <typename T, int NT, int TILES, typename P, typename F>
+__device__ __forceinline__ void layer_product(LayerWork<T, NT, TILES, P>& work, float* sums, int& turn, F&& done) {
+    constexpr int COLS = 8 * NT;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    float d[TILES][NT][4] = {};
+    while (work.here()) {
+        work.multiply(d);
+        const bool last = work.last_columns();
+        const int q = work.q, count = work.count(), row = work.tile * P::kRows;
+        work.next();
+        if (work.here()) work.load_weights(), work.load_all_tokens();
+        if (!last) continue;
+        // lane's sums: rows g, g and g + 8, g + 8, tokens 2t, 2t + 1.  Two turns of the memory:
+        // one barrier an item.
+        float* mine = sums + turn * kExpertWarps * TILES * COLS * kExpertRows;
+        turn ^= 1;
+#pragma unroll
+        for (int m = 0; m < TILES; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float* to = mine + ((warp * TILES + m) * COLS + 8 * n + 2 * t) * kExpertRows + g;
+                to[0] = d[m][n][0], to[kExpertRows] = d[m][n][1];
+                to[8] = d[m][n][2], to[kExpertRows + 8] = d[m][n][3];
+                d[m][n][0] = d[m][n][1] = d[m][n][2] = d[m][n][3] = 0.0f;
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < count * kExpertRows; i += kLayerThreads) {
+            float v[TILES];
+#pragma unroll
+            for (int m = 0; m < TILES; ++m) {
+                v[m] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kExpertWarps; ++k) v[m] += mine[(k * TILES + m) * COLS * kExpertRows + i];
+            }
+            done(q + i / kExpertRows, row + i % kExpertRows, v);
+        }
+    }
+}
+
+template <int NT, int UP, int DOWN>
+constexpr size_t layer_smem_bytes() {
+    return (size_t)2 * kExpertWarps * (UP > DOWN ? UP : DOWN) * 8 * NT * kExpertRows * 4;
+}
+
+// CTAs of an SM: two need their 128 registers a thread.
+constexpr int layer_ctas(int nt) { return nt <= 2 ? 2 : 1; }
+
+// NT: tokens taken at once, in eights.  UP, DOWN: 16-row tiles of an item.
+template <typename T, bool GATED, int NT, int UP, int DOWN>
+__global__ void __launch_bounds__(kLayerThreads, layer_ctas(NT)) expert_layer_kernel(const ExpertArgs a) {
+    wait_for_stream();
+    static_assert(!GATED || UP == 2, "up and gate tiles");
+    extern __shared__ __align__(16) float s_sums[];
+    __shared__ LayerShared s;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // the slots by expert
+    for (int e = threadIdx.x; e < kExpertMaxExperts; e += kLayerThreads) s.count[e] = 0;
+    __syncthreads();
+    for (int q = threadIdx.x; q < a.slots; q += kLayerThreads) {
+        const int e = a.ids[q];
+        if ((unsigned)e < (unsigned)a.experts) atomicAdd(&s.count[e], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {  // 32 experts a round
+        int slots = 0, asked = 0;
+        for (int e0 = 0; e0 < a.experts; e0 += 32) {
+            const int c = s.count[e0 + lane];
+            const unsigned there = __ballot_sync(0xffffffffu, c != 0);
+            if (there == 0) continue;
+            int run = c;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, run, d);
+                if (lane >= d) run += up;
+            }
+            if (c != 0) {
+                const int at = asked + __popc(there & ((1u << lane) - 1));
+                s.expert[at] = (uint16_t)(e0 + lane);
+                s.start[at] = (uint16_t)(slots + run - c);
+                s.count[e0 + lane] = slots + run - c;
+            }
+            asked += __popc(there);
+            slots += __shfl_sync(0xffffffffu, run, 31);
+        }
+        if (lane == 0) s.experts = asked, s.start[asked] = (uint16_t)slots;
+    }
+    __syncthreads();
+    for (int q = threadIdx.x; q < a.slots; q += kLayerThreads) {  // in any order: a slot's values do not depend on it
+        const int e = a.ids[q];
+        if ((unsigned)e < (unsigned)a.experts) s.order[atomicAdd(&s.count[e], 1)] = (uint16_t)q;
+    }
+    __syncthreads();
+
+    int turn = 0;
+    {
+        const LayerProduct<T, false, GATED, UP> product{a};
+        LayerWork<T, NT, UP, LayerProduct<T, false, GATED, UP>> work(product, s);
+        if (work.here()) work.load_weights(), work.load_all_tokens();
+        layer_product<T, NT, UP>(work, s_sums, turn, [&](int q, int row, const float (&v)[UP]) {
+            const int64_t to = (int64_t)s.order[q] * a.inner_pad;
+#pragma unroll
+            for (int m = 0; m < (GATED ? 1 : UP); ++m) {
+                const int r = row + 16 * m;
+                if (r >= a.inner) break;
+                const float act = GATED ? activate(v[UP - 1], a.act) * v[0] : activate(v[m], a.act);
+                // two roundings hold the value to 16 (bf16) or 22 bits, so that the second
+                // product loses nothing that its sums in 32 bits keep
+                const T high = from_float<T>(act);
+                const T low = from_float<T>(isinf(to_float(high)) ? 0.0f : act - to_float(high));
+                static_cast<T*>(a.high)[to + r] = high;
+                static_cast<T*>(a.low)[to + r] = low;
+            }
+        });
+    }
+    {
+        const LayerProduct<T, true, false, DOWN> product{a};
+        LayerWork<T, NT, DOWN, LayerProduct<T, true, false, DOWN>> work(product, s);
+        if (work.here()) work.load_weights();
+        layer_barrier();
+        if (work.here()) work.load_all_tokens();
+        layer_product<T, NT, DOWN>(work, s_sums, turn, [&](int q, int row, const float (&v)[DOWN]) {
+            const int slot = s.order[q];
+#pragma unroll
+            for (int m = 0; m < DOWN; ++m)
+                if (row + 16 * m < a.hidden) __stcg(a.each + (int64_t)slot * a.hidden + row + 16 * m, v[m]);
+        });
+    }
+    layer_barrier();
+    const int64_t all = (int64_t)a.tokens * a.hidden;
+    for (int64_t i = (int64_t)blockIdx.x * kLayerThreads + threadIdx.x; i < all; i += (int64_t)gridDim.x * kLayerThreads) {
+        const int token = (int)(i / a.hidden), row = (int)(i - (int64_t)token * a.hidden);
+        float y = 0.0f;
+#pragma unroll 4
+        for (int j = 0; j < a.picks; ++j) {
+            const int q = token * a.picks + j;
+            if ((unsigned)a.ids[q] < (unsigned)a.experts)
+                y += a.weights[q] * __int_as_float(load_l2(reinterpret_cast<const int*>(a.each + (int64_t)q * a.hidden + row)));
+        }
+        static_cast<T*>(a.out)[token * a.out_stride + row] = from_float<T>(y);
+    }
 }
 
 }  // namespace om

@@ -22,40 +22,78 @@ constexpr int kFewTiles = 2, kManyTiles = 8;  // tokens of an expert taken at on
 
 static constexpr size_t up_smem(int mats, int tiles) { return (size_t)kExpertWarps * mats * 8 * tiles * kExpertRows * 4; }
 
-template <typename T, bool VEC>
+template <typename T>
 static auto up_kernel(bool gated, bool many) {
-    return gated ? (many ? expert_up_kernel<T, true, kManyTiles, VEC> : expert_up_kernel<T, true, kFewTiles, VEC>)
-                 : (many ? expert_up_kernel<T, false, kManyTiles, VEC> : expert_up_kernel<T, false, kFewTiles, VEC>);
+    return gated ? (many ? expert_up_kernel<T, true, kManyTiles> : expert_up_kernel<T, true, kFewTiles>)
+                 : (many ? expert_up_kernel<T, false, kManyTiles> : expert_up_kernel<T, false, kFewTiles>);
 }
 
-// Once per device: the first kernel's shared-memory limit.
+// The one-launch kernel by the tokens that an expert has on average: how many are
+// taken at once, and the rows of an item.
+enum LayerWay { kLayerOne, kLayerFew, kLayerEight, kLayerMany };
+
+static int layer_way(int slots, int experts) {
+    return slots <= experts ? kLayerOne : slots <= 4 * experts ? kLayerFew : slots <= 8 * experts ? kLayerEight : kLayerMany;
+}
+
+template <typename T, bool GATED, int WAY>
+static auto layer_of() {
+    if constexpr (WAY == kLayerOne) return expert_layer_kernel<T, GATED, 1, 2, 1>;
+    else if constexpr (WAY == kLayerFew) return expert_layer_kernel<T, GATED, 1, 2, 2>;
+    else if constexpr (WAY == kLayerEight) return expert_layer_kernel<T, GATED, 2, 2, 2>;
+    else return expert_layer_kernel<T, GATED, 4, 2, 2>;
+}
+template <typename T>
+static auto layer_kernel(bool gated, int way) {
+    return way == kLayerOne     ? (gated ? layer_of<T, true, kLayerOne>() : layer_of<T, false, kLayerOne>())
+           : way == kLayerFew   ? (gated ? layer_of<T, true, kLayerFew>() : layer_of<T, false, kLayerFew>())
+           : way == kLayerEight ? (gated ? layer_of<T, true, kLayerEight>() : layer_of<T, false, kLayerEight>())
+                                : (gated ? layer_of<T, true, kLayerMany>() : layer_of<T, false, kLayerMany>());
+}
+static size_t layer_smem(int way) {
+    return way == kLayerOne     ? layer_smem_bytes<1, 2, 1>()
+           : way == kLayerFew   ? layer_smem_bytes<1, 2, 2>()
+           : way == kLayerEight ? layer_smem_bytes<2, 2, 2>()
+                                : layer_smem_bytes<4, 2, 2>();
+}
+
+// Once per device: the kernels' shared-memory limits.
 static om_status prepare_experts(const DeviceState* d) {
     static std::mutex mu;
     static bool ready[128];
     std::lock_guard<std::mutex> lk(mu);
     if (!ready[d->dev]) {
-        for (const bool gated : {false, true})
-            for (auto* kern : {up_kernel<__half, false>(gated, true), up_kernel<__half, true>(gated, true),
-                               up_kernel<__nv_bfloat16, false>(gated, true), up_kernel<__nv_bfloat16, true>(gated, true)})
-                if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)up_smem(2, kManyTiles)) !=
-                    cudaSuccess) {
-                    cudaGetLastError();
-                    return OM_ECUDA;
-                }
+        bool ok = true;
+        auto limit = [&](auto* kern, size_t bytes) {
+            ok = ok && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+        };
+        for (const bool gated : {false, true}) {
+            limit(up_kernel<__half>(gated, true), up_smem(2, kManyTiles));
+            limit(up_kernel<__nv_bfloat16>(gated, true), up_smem(2, kManyTiles));
+            for (const int way : {kLayerOne, kLayerFew, kLayerEight, kLayerMany}) {
+                limit(layer_kernel<__half>(gated, way), layer_smem(way));
+                limit(layer_kernel<__nv_bfloat16>(gated, way), layer_smem(way));
+            }
+        }
+        if (!ok) {
+            cudaGetLastError();
+            return OM_ECUDA;
+        }
         ready[d->dev] = true;
     }
     return OM_OK;
 }
 
-template <typename T, bool VEC>
-static cudaError_t launch_experts(ExpertArgs a, int sm_count, cudaStream_t st) {
+// Rows of any size and address.
+template <typename T>
+static cudaError_t launch_odd_rows(ExpertArgs a, int sm_count, cudaStream_t st) {
     const bool gated = a.gate != nullptr;
     a.by_slot = a.slots < a.experts;
-    const bool many = a.slots > 8 * kFewTiles / 2 * a.experts;
+    const bool many = a.slots > 8 * a.experts;
     const int tiles = many ? kManyTiles : kFewTiles;
     const dim3 grid((unsigned)((a.inner + kExpertRows - 1) / kExpertRows), (unsigned)std::min(a.slots, a.experts));
     cudaError_t e = counted([&] {
-        launch_early(up_kernel<T, VEC>(gated, many), grid, kExpertWarps * 32, up_smem(gated ? 2 : 1, tiles), st, a);
+        launch_early(up_kernel<T>(gated, many), grid, kExpertWarps * 32, up_smem(gated ? 2 : 1, tiles), st, a);
     });
     if (e != cudaSuccess) return e;
     const int64_t rows = (a.hidden + kExpertRows - 1) / kExpertRows;
@@ -63,7 +101,7 @@ static cudaError_t launch_experts(ExpertArgs a, int sm_count, cudaStream_t st) {
     while (ctas < kExpertCluster && rows * ctas < 3 * (int64_t)sm_count) ctas *= 2;
     // pieces of the experts' columns: enough for every warp of the cluster, of four steps at least
     const int experts = std::min(a.slots, a.experts), steps = (a.inner + 31) / 32;
-    a.parts = std::max(1, std::min((int)(ctas * kExpertWarps) / experts, steps / kExpertUnroll));
+    a.parts = std::max(1, std::min((int)(ctas * kExpertWarps) / experts, steps / 4));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)rows * ctas);
     cfg.blockDim = dim3(kExpertWarps * 32);
@@ -75,7 +113,25 @@ static cudaError_t launch_experts(ExpertArgs a, int sm_count, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return counted([&] { cudaLaunchKernelEx(&cfg, expert_down_kernel<T, VEC>, a); });
+    return counted([&] { cudaLaunchKernelEx(&cfg, expert_down_kernel<T>, a); });
+}
+
+// Rows that bulk copies can take.
+template <typename T>
+static cudaError_t launch_layer(const ExpertArgs& a, int sm_count, cudaStream_t st) {
+    const int way = layer_way(a.slots, a.experts);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sm_count * layer_ctas(way == kLayerMany ? 4 : 1)));
+    cfg.blockDim = dim3(kLayerThreads);
+    cfg.dynamicSmemBytes = layer_smem(way);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1] = {};
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto* kern = layer_kernel<T>(a.gate != nullptr, way);
+    return counted([&] { cudaLaunchKernelEx(&cfg, kern, a); });
 }
 
 }  // namespace om
@@ -128,20 +184,21 @@ om_status om_expert_mlp(int value_type, const void* x, int64_t tokens, int64_t h
     a.down_expert = down_expert, a.down_row = down_row;
     a.tokens = (int)tokens, a.picks = (int)picks, a.slots = (int)slots, a.experts = (int)experts;
     a.hidden = (int)hidden, a.inner = (int)inner, a.inner_pad = (int)((inner + 7) / 8 * 8), a.act = act;
+    // whole vectors where every row starts on 16 bytes and holds a multiple of them
+    bool vec = hidden % 8 == 0 && inner % 8 == 0;
+    for (const int64_t v : {x_stride, up_expert, up_row, gate_expert, gate_row, down_expert, down_row}) vec = vec && v % 8 == 0;
+    for (const void* p : {x, up, gate, down}) vec = vec && !misaligned(p, 16);
     const size_t half = (size_t)slots * a.inner_pad * 2;  // a multiple of 16
-    cudaError_t e = scratch_alloc(pool, &a.high, 2 * half, st);
+    cudaError_t e = scratch_alloc(pool, &a.high, 2 * half + (vec ? (size_t)slots * hidden * 4 : 0), st);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return OM_ENOMEM;
     }
     a.low = static_cast<char*>(a.high) + half;
-    // whole vectors where every row starts on 16 bytes and holds a multiple of them
-    bool vec = hidden % 8 == 0 && inner % 8 == 0;
-    for (const int64_t v : {x_stride, up_expert, up_row, gate_expert, gate_row, down_expert, down_row}) vec = vec && v % 8 == 0;
-    for (const void* p : {x, up, gate, down}) vec = vec && !misaligned(p, 16);
+    a.each = reinterpret_cast<float*>(static_cast<char*>(a.high) + 2 * half);
     e = with_half_type(value_type, [&](auto v) {
         using T = decltype(v);
-        return vec ? launch_experts<T, true>(a, d->sm_count, st) : launch_experts<T, false>(a, d->sm_count, st);
+        return vec ? launch_layer<T>(a, d->sm_count, st) : launch_odd_rows<T>(a, d->sm_count, st);
     });
     scratch_free(a.high, st);
     return e == cudaSuccess ? OM_OK : cuda_fail(e);
