@@ -12,7 +12,9 @@
 
 namespace om {
 
-static size_t beam_smem(int64_t units, int64_t top) { return sizeof(BeamShared) + (size_t)(units * top) * 16; }
+static size_t beam_smem(int stages, int64_t units, int64_t top) {
+    return (size_t)beam_ring_offset() + (size_t)stages * kBeamStageBytes + (size_t)(units * top) * 16;
+}
 
 // Least logits of a slice: 16 for each thread.
 constexpr int64_t kBeamLeastSlice = kBeamThreads * 16;
@@ -27,7 +29,7 @@ static om_status prepare_beam(const DeviceState* d) {
         for (auto* kern : {beam_select_kernel<float>, beam_select_kernel<__nv_bfloat16>, beam_select_kernel<__half>})
             ok = ok &&
                  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      (int)beam_smem(kMaxBeams, kMaxBeamTop)) == cudaSuccess &&
+                                      (int)beam_smem(kBeamMaxStages, kMaxBeams, kMaxBeamTop)) == cudaSuccess &&
                  cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
         for (auto* kern : {beam_gather_kernel<kBeamsInRegisters, true>})
             ok = ok && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -52,7 +54,9 @@ static cudaError_t launch_beam(BeamArgs a, int64_t batch, int sm_count, cudaStre
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(batch * ctas));
     cfg.blockDim = dim3(kBeamThreads);
-    cfg.dynamicSmemBytes = beam_smem((int64_t)a.beams * a.parts, a.top);
+    // chunks on their way: two where there are four CTAs an SM, else four
+    a.stages = batch * ctas > 2 * (int64_t)sm_count ? 2 : kBeamMaxStages;
+    cfg.dynamicSmemBytes = beam_smem(a.stages, (int64_t)a.beams * a.parts, a.top);
     cfg.stream = st;
     cudaLaunchAttribute attr[2] = {early_attribute()};
     attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -108,7 +112,7 @@ om_status om_beam_select(int value_type, const void* logits, int64_t batch, int6
     if (s == OM_OK) s = prepare_beam(d);
     if (s != OM_OK) return s;
     const BeamArgs a{logits, scores,     finished,    batch_stride, beam_stride, (int)beams, (int)vocab, top,
-                     (int)end_id, 1, 0, out_scores, out_parents, out_tokens};
+                     (int)end_id, 1, 0, 0, out_scores, out_parents, out_tokens, d->err};
     const cudaError_t e = with_value_type(value_type, [&](auto v) {
         return launch_beam<decltype(v)>(a, batch, d->sm_count, (cudaStream_t)stream);
     });

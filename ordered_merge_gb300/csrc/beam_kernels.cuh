@@ -16,11 +16,20 @@ constexpr int kMaxBeamTop = 64;
 
 // ------------------------------------------------------------ selection --
 
-constexpr int kBeamThreads = 512;
-constexpr int kBeamGroups = kBeamThreads / 4;  // groups of 4 threads, of whose maxima the top-th bounds the selection
-constexpr int kBeamCandidates = 1024;          // entries of a slice that may reach that bound
-constexpr int kBeamUnroll = 4;                 // vectors in flight per thread
+constexpr int kBeamThreads = 256;
+constexpr int kBeamWarps = kBeamThreads / 32;
+constexpr int kBeamGroups = 128;       // pairs of threads, of whose maxima the top-th bounds the selection
+constexpr int kBeamCandidates = 512;   // entries of a slice that may reach that bound
+constexpr int kBeamEach = 16;          // words of a chunk for each thread
+constexpr int kBeamGroup = 8;          // of them are looked at together
+constexpr int kBeamChunk = kBeamThreads * kBeamEach;
+constexpr int kBeamMaxStages = 4;      // chunks in shared memory
+constexpr int kBeamStageBytes = kBeamChunk * 4 + 32;
 constexpr int kBeamCluster = 16;
+// Continuations of all slices up to which the best are found by counting, each its
+// greater ones, instead of by one warp that takes a winner after the other (8 of 128:
+// 700 cycles against 4300).
+constexpr int kBeamCounted = 512;
 
 struct BeamArgs {
     const void* logits;
@@ -29,100 +38,43 @@ struct BeamArgs {
     int64_t batch_stride, beam_stride;
     int beams, vocab, top, end_id;
     int parts, slice;  // a row is cut into `parts` slices of `slice` logits (a multiple of 8)
+    int stages;        // of the ring
     float* out_scores;
     int32_t* out_parents;
     int32_t* out_tokens;
+    uint32_t* err;
 };
 
-// A row's logits in vectors of 16 bytes from its first one on, whatever the
-// row's address: what thread t sums does not depend on it, so that equal rows
-// have equal sums, and equal continuations tie.
+// The logits of a word: two of 16 bits, or one.
 template <typename T>
-struct RowVectors {
-    static constexpr int kPer = 16 / (int)sizeof(T);
-    const char* base;  // the row's address rounded down to 16 bytes
-    uint32_t shift;    // and the bytes it lies after that
-    uint32_t n;        // logits
-
-    __device__ __forceinline__ RowVectors(const T* row, int logits) {
-        const uintptr_t p = reinterpret_cast<uintptr_t>(row);
-        base = reinterpret_cast<const char*>(p & ~(uintptr_t)15);
-        shift = (uint32_t)(p & 15);
-        n = (uint32_t)logits;
-    }
-    // -inf in every place of a word
+struct WordOf {
+    static constexpr int kPer = 4 / (int)sizeof(T);
     static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    // -inf in every place of a word
     static constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : kBf16 ? 0xff80ff80u : 0xfc00fc00u;
     // Lowest bits of a float that no value of T uses (all equal in an image: not compared).
     static constexpr int kSpare = sizeof(T) == 4 ? 0 : kBf16 ? 16 : 13;
     static constexpr uint64_t kKeyBits = ~((((uint64_t)1 << kSpare) - 1) << 32);
-
-    // Vector j (logits j * kPer ...), -inf past the row's end.  Reads the 16 aligned bytes
-    // around each logit, nothing beyond.
-    __device__ __forceinline__ uint4 load(uint32_t j) const {
-        const uint4* p = reinterpret_cast<const uint4*>(base) + j;
-        const uint32_t left = n > j * kPer ? n - j * kPer : 0;  // logits from here on
-        uint4 v = make_uint4(kNone, kNone, kNone, kNone);
-        if (left == 0) return v;
-        v = *p;
-        if (shift != 0) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (left * (uint32_t)sizeof(T) > 16 - shift) w = p[1];
-            // the 16 bytes from `shift` on
-            uint32_t x[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
-            if (shift & 8) {
-#pragma unroll
-                for (int i = 0; i < 6; ++i) x[i] = x[i + 2];
-            }
-            if (shift & 4) {
-#pragma unroll
-                for (int i = 0; i < 5; ++i) x[i] = x[i + 1];
-            }
-            if (shift & 2) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], 16);
-            }
-            v = make_uint4(x[0], x[1], x[2], x[3]);
-        }
-        if (left < kPer) {
-            uint32_t* x = &v.x;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                constexpr uint32_t in_word = 4 / sizeof(T);
-                if (i * in_word >= left) x[i] = kNone;
-                else if (in_word == 2 && i * in_word + 1 == left) x[i] = (x[i] & 0xffffu) | (kNone & 0xffff0000u);
-            }
-        }
-        return v;
-    }
 };
-// The logits of a vector as floats, NaN as -inf (a maximum takes the operand that is a number).
-__device__ __forceinline__ void logits_of(const uint4& v, float (&x)[4], float) {
-    const uint32_t* w = &v.x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = fmaxf(__uint_as_float(w[i]), -INFINITY);
+
+// The greater of two words, value by value; NaN loses against any number.
+__device__ __forceinline__ uint32_t word_max(uint32_t x, uint32_t y, float) {
+    return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y)));
 }
-__device__ __forceinline__ void logits_of(const uint4& v, float (&x)[8], __nv_bfloat16) {
-    const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&v);
-    const __nv_bfloat162 low = __float2bfloat162_rn(-INFINITY);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 m = __hmax2(w[i], low);
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
-        x[2 * i] = __uint_as_float(u << 16);
-        x[2 * i + 1] = __uint_as_float(u & 0xffff0000u);
-    }
+__device__ __forceinline__ uint32_t word_max(uint32_t x, uint32_t y, __nv_bfloat16) {
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&m);
 }
-__device__ __forceinline__ void logits_of(const uint4& v, float (&x)[8], __half) {
-    const __half2* w = reinterpret_cast<const __half2*>(&v);
-    const __half2 low = __float2half2_rn(-INFINITY);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(__hmax2(w[i], low));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
+__device__ __forceinline__ uint32_t word_max(uint32_t x, uint32_t y, __half) {
+    const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&m);
 }
+// The first value of a word, and the second (32 bits have one).
+__device__ __forceinline__ float2 word_values(uint32_t w, float) { return make_float2(__uint_as_float(w), -INFINITY); }
+__device__ __forceinline__ float2 word_values(uint32_t w, __nv_bfloat16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 word_values(uint32_t w, __half) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -148,21 +100,30 @@ __device__ __forceinline__ uint64_t beam_key(float x, uint32_t token) {
 }
 
 struct BeamShared {
-    float warp_max[kBeamThreads / 32];
-    float warp_sum[kBeamThreads / 32];
-    float group_max[kBeamGroups];
-    float bound;
-    int near;         // threads whose maximum reaches the bound
-    int found;        // logits that reach it
-    int count;        // (settling) those counted
-    uint16_t who[kBeamThreads];
+    uint64_t full[kBeamMaxStages];
     uint64_t key[kBeamCandidates];
-    float2 stats[kMaxBeams];   // of each unit: maximum, sum of exp(x - maximum)
     double lse[kMaxBeams];
+    double base[kMaxBeams];    // of each unit: the sum of exp(x - base)
+    uint64_t sum[kMaxBeams];   // (a float)
     float score[kMaxBeams];
+    float group_max[kBeamGroups];
+    float warp_max[kBeamWarps];
+    float warp_scale[kBeamWarps];
+    float warp_sum[kBeamWarps];
+    float most;       // of the slice
+    int slow;         // its sum is to be made again
+    float bound;
+    int found;        // logits that reach the bound
+    int count;        // (settling) those counted
+    int live;         // units of this CTA that have logits to look at
+    uint8_t unit[kMaxBeams];
 };
-// After it, in the first CTA of a cluster: the units' lists, [units][top] keys,
-// then the images of the continuations' scores in the same places.
+// After it the ring's stages and, in the first CTA of a cluster, the units' lists,
+// [units][top] keys, then the images of the continuations' scores in the same places.
+
+// The two halves of cluster_sync.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // A word pair of CTA `rank`'s shared memory, at the address p has in this CTA's.
 __device__ __forceinline__ void store_peer(uint64_t* p, uint32_t rank, uint64_t v) {
@@ -171,24 +132,55 @@ __device__ __forceinline__ void store_peer(uint64_t* p, uint32_t rank, uint64_t 
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
 }
 
+// What a unit found, to the first CTA.
+__device__ __forceinline__ void store_stats(BeamShared& s, int unit, double base, float sum) {
+    store_peer(reinterpret_cast<uint64_t*>(&s.base[unit]), 0, (uint64_t)__double_as_longlong(base));
+    store_peer(&s.sum[unit], 0, (uint64_t)__float_as_uint(sum));
+}
+
+// A slice of a row: its first logit and how many.
+template <typename T>
+struct BeamSlice {
+    const T* row;
+    int first, n;
+
+    __device__ __forceinline__ BeamSlice(const BeamArgs& a, int64_t b, int unit) {
+        const int beam = unit / a.parts, part = unit - beam * a.parts;
+        row = static_cast<const T*>(a.logits) + b * a.batch_stride + beam * a.beam_stride;
+        first = min(part * a.slice, a.vocab);
+        n = min(a.slice, a.vocab - first);
+    }
+    __device__ __forceinline__ int words() const { return (n + WordOf<T>::kPer - 1) / WordOf<T>::kPer; }
+    __device__ __forceinline__ int chunks() const { return (words() + kBeamChunk - 1) / kBeamChunk; }
+    // NaN as -inf
+    __device__ __forceinline__ float at(int i) const { return fmaxf(to_float(row[first + i]), -INFINITY); }
+    // Word w, -inf past the end, NaN as -inf.  Loads without branches, so that several go together.
+    __device__ __forceinline__ uint32_t word(int w) const {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(row + first) + (uintptr_t)w * 4;
+        const int left = n - w * WordOf<T>::kPer;
+        const uint32_t* at = reinterpret_cast<const uint32_t*>(p & ~(uintptr_t)3);
+        const bool odd = sizeof(T) == 2 && (p & 2) != 0;
+        uint32_t v = left > 0 ? at[0] : WordOf<T>::kNone;
+        const uint32_t up = odd && left > 1 ? at[1] : 0u;
+        v = odd && left > 0 ? __byte_perm(v, up, 0x5432) : v;
+        if (sizeof(T) == 2 && left == 1) v = (v & 0xffffu) | (WordOf<T>::kNone & 0xffff0000u);
+        return word_max(v, WordOf<T>::kNone, T{});
+    }
+};
+
 // The top-th greatest key of a slice too full of equal or near values for the
 // candidates' room (rows of one value, of few values not masked by the type's
 // lowest): its bits one after another, each by a count over the slice.  All threads.
 template <typename T>
-__device__ __noinline__ uint64_t settle_edge(const RowVectors<T>& row, uint32_t v0, uint32_t v1, int top, BeamShared& s) {
-    constexpr int N = RowVectors<T>::kPer;
+__device__ __noinline__ uint64_t settle_edge(const BeamSlice<T>& slice, int top, BeamShared& s) {
     uint64_t edge = 0;
-    for (int bit = 63; bit >= 0; bit = bit == 32 + RowVectors<T>::kSpare ? 31 : bit - 1) {
+    for (int bit = 63; bit >= 0; bit = bit == 32 + WordOf<T>::kSpare ? 31 : bit - 1) {
         const uint64_t want = edge | 1ull << bit;
         int mine = 0;
-        for (uint32_t j = v0 + threadIdx.x; j < v1; j += kBeamThreads) {
-            float x[N];
-            logits_of(row.load(j), x, T{});
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint64_t key = beam_key(x[i], j * N + i) & RowVectors<T>::kKeyBits;
-                mine += x[i] > -INFINITY && key >= want;
-            }
+#pragma unroll 4
+        for (int i = threadIdx.x; i < slice.n; i += kBeamThreads) {
+            const float x = slice.at(i);
+            mine += x > -INFINITY && (beam_key(x, slice.first + i) & WordOf<T>::kKeyBits) >= want;
         }
         if (threadIdx.x == 0) s.count = 0;
         __syncthreads();
@@ -201,123 +193,211 @@ __device__ __noinline__ uint64_t settle_edge(const RowVectors<T>& row, uint32_t 
     return edge;
 }
 
-// One slice of a row: its maximum, its sum of exponentials and its `top`
-// greatest logits in order, into place `unit` of the first CTA.  All threads.
-//
-// Each thread streams its vectors once, keeping a running maximum and sum.  Of
-// the maxima of 128 groups of threads the top-th greatest is a lower bound of the
-// slice's top-th greatest logit, and only threads whose own maximum reaches it
-// hold any that do: few more than `top`.  Their vectors are read again, a warp to
-// each such thread, and what reaches the bound is put in order by counting.
+// x * y + z of two at once.
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t p;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(x), "l"(y), "l"(z));
+    return p;
+}
+
+// What a thread keeps of the words it has seen, 8 at a time ("eights"): the greatest
+// maxima of eights, where the first two were, and the sum of 2^(x log2e - scale).  The
+// scale is its first maximum times log2e, rounded (what the rounding does cancels
+// when sums are joined by their scales), and moves only when logits leave the range
+// that a float can take from there: to move it with every new maximum cost as much
+// as the rest.  Beyond kBeamPlain it no longer says anything, and NaN spoils the
+// sum: such slices are summed once more, slowly.
+constexpr float kBeamPlain = 1e6f;
+
+struct BeamRunning {
+    float most = -INFINITY, second = -INFINITY, third = -INFINITY;
+    int where = 0, next = 0;  // the eights of `most` and `second`
+    float scale = -kBeamPlain * kLog2e, limit = 60.0f - kBeamPlain;
+    uint64_t sum[2] = {0, 0};  // each of first values and second values (of two zeros)
+
+    template <typename T>
+    __device__ __forceinline__ void add(const uint32_t (&w)[kBeamGroup], int index, T) {
+        uint32_t top = WordOf<T>::kNone;
+#pragma unroll
+        for (int i = 0; i < kBeamGroup; ++i) top = word_max(top, w[i], T{});
+        const float2 both = word_values(top, T{});
+        const float best = fmaxf(both.x, both.y);
+        if (best > limit) {  // once, as a rule
+            const float to = best * kLog2e, down = exp2_fast(scale - to);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) sum[i] = mul2(sum[i], pack2(down, down));
+            scale = to, limit = best + 60.0f;
+        }
+        third = fmaxf(third, fminf(best, second));
+        next = best > most ? where : best > second ? index : next;
+        second = fmaxf(second, fminf(best, most));
+        where = best > most ? index : where;
+        most = fmaxf(most, best);
+        const uint64_t log2e = pack2(kLog2e, kLog2e), less = pack2(-scale, -scale);
+        constexpr int kStep = 2 / WordOf<T>::kPer;  // words of two logits
+#pragma unroll
+        for (int i = 0; i < kBeamGroup; i += kStep) {
+            const float2 v = word_values(w[i], T{});
+            const uint64_t x = kStep == 1 ? pack2(v.x, v.y) : pack2(v.x, __uint_as_float(w[i + kStep - 1]));
+            const float2 e = unpack2(fma2(x, log2e, less));
+            add2(sum[(i / kStep) & 1], pack2(exp2_fast(e.x), exp2_fast(e.y)));
+        }
+    }
+    __device__ __forceinline__ float total() const {
+        const float2 x = unpack2(sum[0]), y = unpack2(sum[1]);
+        return (x.x + y.x) + (x.y + y.y);
+    }
+};
+
+// A thread's words of a chunk of `words`, word i of which starts `offset` bytes into
+// the stage and 4 i on.  Which words a thread has does not depend on the row's
+// address, so that equal rows have equal sums and equal continuations tie.
 template <typename T>
-__device__ __forceinline__ void beam_slice(const BeamArgs& a, const T* logits, int part, int unit, uint64_t* lists,
-                                           BeamShared& s) {
-    constexpr int N = RowVectors<T>::kPer, U = kBeamUnroll;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const RowVectors<T> row(logits, a.vocab);
-    const uint32_t v0 = (uint32_t)part * (uint32_t)(a.slice / N);
-    const uint32_t all = (uint32_t)((a.vocab + N - 1) / N), v1 = min(v0 + (uint32_t)(a.slice / N), all);
-
-    float m = -INFINITY;
-    uint64_t sum2 = pack2(0.0f, 0.0f);
-    for (uint32_t j0 = v0 + threadIdx.x; j0 < v1; j0 += kBeamThreads * U) {
-        uint4 v[U];
+__device__ __forceinline__ void beam_chunk(const unsigned char* stage, uint32_t offset, int words, int logits, int chunk,
+                                           BeamRunning& run) {
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(stage) + offset / 4 + threadIdx.x;
+    const bool odd = offset & 2;  // 16-bit logits between two words
+    constexpr int W = kBeamGroup;
+    const bool whole = words == kBeamChunk && logits == words * WordOf<T>::kPer;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t j = j0 + u * kBeamThreads;
-            v[u] = row.load(j < v1 ? j : 0xffffffffu / N);
-        }
-        float x[U][N], best = m;
+    for (int j = 0; j < kBeamEach / W; ++j) {
+        uint32_t w[W];
+        if (whole) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            logits_of(v[u], x[u], T{});
+            for (int i = 0; i < W; ++i) w[i] = s[(j * W + i) * kBeamThreads];
+            if (odd) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) best = fmaxf(best, x[u][i]);
-        }
-        if (best > m) {
-            const float down = exp2_fast((m - best) * kLog2e);
-            sum2 = mul2(sum2, pack2(down, down));
-            m = best;
-        }
-        if (m > -INFINITY) {
-            const uint64_t less = pack2(-m, -m), log2e = pack2(kLog2e, kLog2e);
+                for (int i = 0; i < W; ++i) w[i] = __byte_perm(w[i], s[(j * W + i) * kBeamThreads + 1], 0x5432);
+            }
+        } else {
+            if (j * W * kBeamThreads >= words) break;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < N; i += 2) {
-                    uint64_t d = pack2(x[u][i], x[u][i + 1]);
-                    add2(d, less);
-                    const float2 e = unpack2(mul2(d, log2e));
-                    add2(sum2, pack2(exp2_fast(e.x), exp2_fast(e.y)));
+            for (int i = 0; i < W; ++i) {
+                const int at = (j * W + i) * kBeamThreads + (int)threadIdx.x;
+                w[i] = WordOf<T>::kNone;
+                if (at < words) {
+                    w[i] = s[(j * W + i) * kBeamThreads];
+                    const bool half = sizeof(T) == 2 && 2 * at + 1 == logits;  // its second value is none of the row's
+                    if (odd) w[i] = __byte_perm(w[i], half ? 0u : s[(j * W + i) * kBeamThreads + 1], 0x5432);
+                    if (half) w[i] = (w[i] & 0xffffu) | (WordOf<T>::kNone & 0xffff0000u);
                 }
+            }
         }
+        run.add(w, chunk * (kBeamEach / W) + j, T{});
     }
-    const float2 halves = unpack2(sum2);
-    float sum = halves.x + halves.y;
+}
 
-    // the slice's maximum and sum, and the groups' maxima
-    float g = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-    if ((threadIdx.x & 3) == 0) s.group_max[threadIdx.x >> 2] = g;
-    const float most = warp_max(g);
-    sum = m > -INFINITY ? sum * exp2_fast((m - most) * kLog2e) : 0.0f;
-    sum = warp_sum(sum);
-    if (lane == 0) s.warp_max[warp] = most, s.warp_sum[warp] = sum;
-    if (threadIdx.x == 0) s.near = 0, s.found = 0;
+// The end of a slice: its maximum, its sum of exponentials and its `top` greatest
+// logits in order, into place `unit` of the first CTA.  All threads.
+//
+// Of the maxima of 128 pairs of threads the top-th greatest is a lower bound of the
+// slice's top-th greatest logit, and only threads whose own maximum reaches it hold
+// any that do: few more than `top`.  They read the one or two eights again that hold
+// them; for one with more, its warp reads all of its words.  What reaches the bound
+// is put in order by counting.
+template <typename T>
+__device__ __forceinline__ void beam_slice_end(const BeamArgs& a, const BeamSlice<T>& slice, int unit, const BeamRunning& run,
+                                               uint64_t* lists, BeamShared& s) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float m = run.most;
+    const float g = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    if ((threadIdx.x & 1) == 0) s.group_max[threadIdx.x >> 1] = g;
+    // NaN stays NaN in these, to be seen at the end
+    const float most = warp_max(m), scale = warp_max(run.scale);
+    const float all = warp_sum(run.total() * exp2_fast(run.scale - scale));
+    if (lane == 0) s.warp_max[warp] = most, s.warp_scale[warp] = scale, s.warp_sum[warp] = all;
+    if (threadIdx.x == 0) s.found = 0;
     __syncthreads();
-    if (warp == 0) {
-        constexpr int W = kBeamThreads / 32;
-        const float wm = lane < W ? s.warp_max[lane] : -INFINITY;
-        const float top_max = warp_max(wm);
-        const float ws = warp_sum(lane < W && wm > -INFINITY ? s.warp_sum[lane] * exp2_fast((wm - top_max) * kLog2e) : 0.0f);
-        if (lane == 0) store_peer(reinterpret_cast<uint64_t*>(&s.stats[unit]), 0, pack2(top_max, ws));
-    }
-    if (threadIdx.x < kBeamGroups) {
-        const float mine = s.group_max[threadIdx.x];
+    {  // two threads a group, each comparing with half of the groups
+        const int group = (int)threadIdx.x >> 1, half = (int)threadIdx.x & 1;
+        const float mine = s.group_max[group];
         int rank = 0;
 #pragma unroll 8
-        for (int i = 0; i < kBeamGroups; i += 4) {
+        for (int i = half * (kBeamGroups / 2); i < (half + 1) * (kBeamGroups / 2); i += 4) {
             const float4 o = *reinterpret_cast<const float4*>(&s.group_max[i]);
             const float other[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                rank += other[k] > mine || (other[k] == mine && i + k < (int)threadIdx.x);
+            for (int k = 0; k < 4; ++k) rank += other[k] > mine || (other[k] == mine && i + k < group);
         }
+        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
         if (rank == a.top - 1) s.bound = mine;
+    }
+    if (warp == kBeamWarps - 1) {
+        const float wm = warp_max(lane < kBeamWarps ? s.warp_max[lane] : -INFINITY);
+        const float ws = lane < kBeamWarps ? s.warp_scale[lane] : -INFINITY, top_scale = warp_max(ws);
+        const float sum = warp_sum(lane < kBeamWarps ? s.warp_sum[lane] * exp2_fast(ws - top_scale) : 0.0f);
+        if (lane == 0) {
+            s.most = wm;
+            s.slow = wm > -INFINITY && !(fabsf(wm) <= kBeamPlain && sum > 0.0f && sum < INFINITY);
+            store_stats(s, unit, wm > -INFINITY ? (double)top_scale * (1.0 / (double)kLog2e) : -INFINITY, wm > -INFINITY ? sum : 0.0f);
+        }
     }
     __syncthreads();
     const float bound = s.bound;
-    if (m >= bound && m > -INFINITY) s.who[atomicAdd(&s.near, 1)] = (uint16_t)threadIdx.x;
-    __syncthreads();
-    const int near = s.near;
-    for (int k = warp; k < near; k += kBeamThreads / 32) {
-        for (uint32_t j = v0 + s.who[k] + lane * kBeamThreads; j < v1; j += 32 * kBeamThreads) {
-            float x[N];
-            logits_of(row.load(j), x, T{});
+    const int words = slice.words();
+    auto found_one = [&](float x, int i) {
+        const int at = atomicAdd(&s.found, 1);
+        if (at < kBeamCandidates) s.key[at] = beam_key(x, slice.first + i);
+    };
+    // two eights' logits (the second's first word past the end where there is none): all of them, then a look at each
+    auto look = [&](int first, int second) {
+        uint32_t w[2 * kBeamGroup];
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (x[i] >= bound && x[i] > -INFINITY) {
-                    const int at = atomicAdd(&s.found, 1);
-                    if (at < kBeamCandidates) s.key[at] = beam_key(x[i], j * N + i);
-                }
+        for (int i = 0; i < 2 * kBeamGroup; ++i)
+            w[i] = slice.word((i < kBeamGroup ? first : second) + i % kBeamGroup * kBeamThreads);
+#pragma unroll
+        for (int i = 0; i < 2 * kBeamGroup; ++i) {
+            const int at = ((i < kBeamGroup ? first : second) + i % kBeamGroup * kBeamThreads) * WordOf<T>::kPer;
+            const float2 x = word_values(w[i], T{});
+            if (x.x >= bound && x.x > -INFINITY) found_one(x.x, at);
+            if (x.y >= bound && x.y > -INFINITY) found_one(x.y, at + 1);
+        }
+    };
+    const bool thrice = run.third >= bound && run.third > -INFINITY;
+    if (!thrice && m >= bound && m > -INFINITY)
+        look(run.where * kBeamGroup * kBeamThreads + (int)threadIdx.x,
+             run.second >= bound && run.second > -INFINITY ? run.next * kBeamGroup * kBeamThreads + (int)threadIdx.x : words);
+    for (unsigned todo = __ballot_sync(0xffffffffu, thrice); todo != 0; todo &= todo - 1)
+        for (int w = warp * 32 + __ffs(todo) - 1 + lane * kBeamThreads; w < words; w += 64 * kBeamGroup * kBeamThreads) {
+            uint32_t v[2 * kBeamGroup];
+#pragma unroll
+            for (int i = 0; i < 2 * kBeamGroup; ++i) v[i] = slice.word(w + 32 * i * kBeamThreads);
+#pragma unroll
+            for (int i = 0; i < 2 * kBeamGroup; ++i) {
+                const int at = (w + 32 * i * kBeamThreads) * WordOf<T>::kPer;
+                const float2 x = word_values(v[i], T{});
+                if (x.x >= bound && x.x > -INFINITY) found_one(x.x, at);
+                if (x.y >= bound && x.y > -INFINITY) found_one(x.y, at + 1);
+            }
+        }
+    __syncthreads();
+    if (s.slow) {
+        float sum = 0.0f;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < slice.n; i += kBeamThreads) {
+            const float x = slice.at(i);
+            if (x > -INFINITY) sum += exp2_fast((x - s.most) * kLog2e);
+        }
+        sum = warp_sum(sum);
+        if (lane == 0) s.warp_sum[warp] = sum;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            float all_warps = 0.0f;
+            for (int i = 0; i < kBeamWarps; ++i) all_warps += s.warp_sum[i];
+            store_stats(s, unit, (double)s.most, all_warps);
         }
     }
-    __syncthreads();
     int found = s.found;
     if (found > kBeamCandidates) {
-        const uint64_t edge = settle_edge(row, v0, v1, a.top, s);
+        const uint64_t edge = settle_edge(slice, a.top, s);
         if (threadIdx.x == 0) s.found = 0;
         __syncthreads();
-        for (uint32_t j = v0 + threadIdx.x; j < v1; j += kBeamThreads) {
-            float x[N];
-            logits_of(row.load(j), x, T{});
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint64_t key = beam_key(x[i], j * N + i);
-                if (x[i] > -INFINITY && (key & RowVectors<T>::kKeyBits) >= edge) {
-                    const int at = atomicAdd(&s.found, 1);  // `top` of them: keys differ
-                    if (at < kBeamCandidates) s.key[at] = key;
-                }
+        for (int i = threadIdx.x; i < slice.n; i += kBeamThreads) {
+            const float x = slice.at(i);
+            const uint64_t key = beam_key(x, slice.first + i);
+            if (x > -INFINITY && (key & WordOf<T>::kKeyBits) >= edge) {
+                const int at = atomicAdd(&s.found, 1);  // `top` of them: keys differ
+                if (at < kBeamCandidates) s.key[at] = key;
             }
         }
         __syncthreads();
@@ -327,6 +407,7 @@ __device__ __forceinline__ void beam_slice(const BeamArgs& a, const T* logits, i
     for (int c = threadIdx.x; c < found; c += kBeamThreads) {
         const uint64_t mine = s.key[c];
         int rank = 0;
+#pragma unroll 4
         for (int o = 0; o < found; ++o) rank += s.key[o] > mine;
         if (rank < a.top) store_peer(list + rank, 0, mine);
     }
@@ -334,34 +415,94 @@ __device__ __forceinline__ void beam_slice(const BeamArgs& a, const T* logits, i
     __syncthreads();  // s is used again
 }
 
+// Bytes of BeamShared before the ring.
+__host__ __device__ constexpr int beam_ring_offset() { return ((int)sizeof(BeamShared) + 127) / 128 * 128; }
+
 // A cluster to each sequence; its slices ("units", beam by beam) go to the CTAs in
-// turn, and the first CTA joins them: the beams' logarithms of their sums, the
-// scores of the slices' best continuations in 64 bits, and the lists merged by one
-// warp, a winner at a time.
+// turn.  A CTA streams the chunks of its slices through a ring in shared memory,
+// filled by bulk copies (of whole aligned 16 bytes around a chunk, whatever the
+// row's address), each thread keeping a running maximum and sum of its words.  The
+// first CTA joins the slices: the beams' logarithms of their sums, the scores of
+// the slices' best continuations in 64 bits, and the best of all.
 template <typename T>
-__global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const BeamArgs a) {
+__global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const BeamArgs a) {
     wait_for_stream();
-    extern __shared__ __align__(16) unsigned char s_raw[];
+    extern __shared__ __align__(128) unsigned char s_raw[];
     BeamShared& s = *reinterpret_cast<BeamShared*>(s_raw);
-    uint64_t* lists = reinterpret_cast<uint64_t*>(s_raw + sizeof(BeamShared));
+    unsigned char* ring = s_raw + beam_ring_offset();
+    uint64_t* lists = reinterpret_cast<uint64_t*>(ring + a.stages * kBeamStageBytes);
     const uint32_t ctas = cluster_size(), rank = cluster_rank();
     const int64_t b = blockIdx.x / ctas;
     const int units = a.beams * a.parts;
-    if (ctas > 1) cluster_sync();  // the first CTA has started: its shared memory may be written
-    for (int u = (int)rank; u < units; u += (int)ctas) {
-        const int beam = u / a.parts, part = u - beam * a.parts;
-        const float score = a.scores == nullptr ? 0.0f : a.scores[b * a.beams + beam];
-        const bool ended = a.finished != nullptr && a.finished[b * a.beams + beam] != 0;
-        // a beam that has ended, or whose score is -inf or NaN, has no logits to look at
-        if (ended || !(score > -INFINITY)) {
-            for (int r = threadIdx.x; r < a.top; r += kBeamThreads) store_peer(lists + u * a.top + r, 0, 0ull);
-            if (threadIdx.x == 0) store_peer(reinterpret_cast<uint64_t*>(&s.stats[u]), 0, pack2(-INFINITY, 0.0f));
-            continue;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < a.stages; ++i) mbar_init(&s.full[i], 1);
+        fence_barrier_init();
+    }
+    if (threadIdx.x < 32) {  // the slices of this CTA that have logits to look at
+        int live = 0;
+        for (int u0 = (int)rank; u0 < units; u0 += 32 * (int)ctas) {
+            const int u = u0 + (int)threadIdx.x * (int)ctas;
+            bool looks = false;
+            if (u < units) {
+                const int beam = u / a.parts;
+                const float score = a.scores == nullptr ? 0.0f : a.scores[b * a.beams + beam];
+                const bool ended = a.finished != nullptr && a.finished[b * a.beams + beam] != 0;
+                looks = !ended && score > -INFINITY && u % a.parts * a.slice < a.vocab;
+            }
+            const unsigned there = __ballot_sync(0xffffffffu, looks);
+            if (looks) s.unit[live + __popc(there & ((1u << threadIdx.x) - 1))] = (uint8_t)u;
+            live += __popc(there);
         }
-        const T* row = static_cast<const T*>(a.logits) + b * a.batch_stride + beam * a.beam_stride;
-        beam_slice<T>(a, row, part, u, lists, s);
+        if (threadIdx.x == 0) s.live = live;
+    }
+    // slices without logits to look at leave these as they are
+    if (rank == 0) {
+        for (int i = threadIdx.x; i < units; i += kBeamThreads) s.base[i] = -INFINITY, s.sum[i] = 0;
+        for (int i = threadIdx.x; i < units * a.top; i += kBeamThreads) lists[i] = 0;
+    }
+    __syncthreads();
+    if (ctas > 1) cluster_arrive();  // and wait before the first store to the first CTA's shared memory
+
+    const int live = s.live;
+    const uint64_t policy = l2_policy_evict_first();
+    // thread 0: where the next chunk starts, and bytes left of its slice
+    int next_slice = 0, left = 0;
+    uintptr_t from = 0;
+    auto fill = [&](int stage) {
+        if (left <= 0) {
+            if (next_slice >= live) return;
+            const BeamSlice<T> slice(a, b, s.unit[next_slice++]);
+            from = reinterpret_cast<uintptr_t>(slice.row + slice.first);
+            left = slice.n * (int)sizeof(T);
+        }
+        const uint32_t skip = (uint32_t)(from & 15), whole = (skip + (uint32_t)min(kBeamChunk * 4, left) + 15) & ~15u;
+        mbar_arrive_expect_tx(&s.full[stage], whole);
+        bulk_copy_g2s(ring + stage * kBeamStageBytes, reinterpret_cast<const void*>(from - skip), whole, &s.full[stage], policy);
+        from += kBeamChunk * 4, left -= kBeamChunk * 4;
+    };
+    if (threadIdx.x == 0)
+        for (int i = 0; i < a.stages; ++i) fill(i);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int k = 0; k < live; ++k) {
+        const int unit = s.unit[k];
+        const BeamSlice<T> slice(a, b, unit);
+        const int chunks = slice.chunks();
+        BeamRunning run;
+        for (int c = 0; c < chunks; ++c) {
+            mbar_wait_bounded(&s.full[stage], phase, a.err);
+            const uint32_t skip = (uint32_t)((reinterpret_cast<uintptr_t>(slice.row + slice.first)) & 15);  // chunks are whole 16 bytes
+            const int left = slice.n - c * kBeamChunk * WordOf<T>::kPer, logits = min(left, kBeamChunk * WordOf<T>::kPer);
+            beam_chunk<T>(ring + stage * kBeamStageBytes, skip, (logits + WordOf<T>::kPer - 1) / WordOf<T>::kPer, logits, c, run);
+            __syncthreads();
+            if (threadIdx.x == 0) fill(stage);
+            if (++stage == a.stages) stage = 0, phase ^= 1;
+        }
+        if (k == 0 && ctas > 1) cluster_wait();
+        beam_slice_end<T>(a, slice, unit, run, lists, s);
     }
     if (ctas > 1) {
+        if (live == 0) cluster_wait();
         cluster_sync();
         if (rank != 0) return;
     } else {
@@ -370,14 +511,18 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const Beam
     uint64_t* images = lists + units * a.top;
     if (threadIdx.x < a.beams) {
         const int i = threadIdx.x;
-        float most = -INFINITY;
-        for (int p = 0; p < a.parts; ++p) most = fmaxf(most, s.stats[i * a.parts + p].x);
+        double most = -INFINITY;
+        for (int p = 0; p < a.parts; ++p) most = fmax(most, s.base[i * a.parts + p]);
         float sum = 0.0f;
         for (int p = 0; p < a.parts; ++p) {
-            const float2 st = s.stats[i * a.parts + p];
-            if (st.x > -INFINITY) sum += st.y * exp2_fast((st.x - most) * kLog2e);
+            const float part = __uint_as_float((uint32_t)s.sum[i * a.parts + p]);
+            const double base = s.base[i * a.parts + p];
+            if (base > -INFINITY) sum += base == most ? part : part * exp2_fast((float)(base - most) * kLog2e);
         }
-        s.lse[i] = (double)most + log((double)sum);
+        // the logarithm of a sum as its exponent's and its fraction's, of which only the latter is rounded to 32 bits
+        const int exponent = (int)(__float_as_uint(sum) >> 23) - 127;
+        const float fraction = __uint_as_float((__float_as_uint(sum) & 0x7fffffu) | 0x3f800000u);
+        s.lse[i] = sum > 0.0f ? most + (exponent * 0.6931471805599453 + (double)logf(fraction)) : (double)NAN;
         s.score[i] = a.scores == nullptr ? 0.0f : a.scores[b * a.beams + i];
     }
     __syncthreads();
@@ -395,6 +540,22 @@ __global__ void __launch_bounds__(kBeamThreads, 2) beam_select_kernel(const Beam
         images[c] = image;
     }
     __syncthreads();
+    const int n = units * a.top;
+    if (n <= kBeamCounted) {
+        // the place of a continuation is the number of those before it
+        for (int c = threadIdx.x; c < n; c += kBeamThreads) {
+            const uint64_t mine = images[c];
+            int rank = 0;
+#pragma unroll 4
+            for (int o = 0; o < n; ++o) rank += images[o] > mine || (images[o] == mine && o < c);
+            if (rank >= a.top) continue;
+            const int64_t to = b * a.top + rank;
+            a.out_scores[to] = mine != 0 ? (float)image64_score(mine) : -INFINITY;
+            a.out_parents[to] = mine != 0 ? c / a.top / a.parts : -1;
+            a.out_tokens[to] = mine != 0 ? (int32_t)~(uint32_t)lists[c] : -1;
+        }
+        return;
+    }
     if (threadIdx.x >= 32) return;
     const int lane = threadIdx.x;
     int at[2];
