@@ -31,7 +31,8 @@ static om_status prepare_beam(const DeviceState* d) {
                  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       (int)beam_smem(kBeamMaxStages, kMaxBeams, kMaxBeamTop)) == cudaSuccess &&
                  cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
-        for (auto* kern : {beam_gather_kernel<kBeamsInRegisters, true>})
+        for (const void* kern : {(const void*)beam_gather_kernel<kBeamsInRegisters, true, kFewBeamArrays>,
+                                 (const void*)beam_gather_kernel<kBeamsInRegisters, true, kMaxBeamArrays>})
             ok = ok && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             kMaxBeams * kBeamGatherThreads * 16) == cudaSuccess;
         if (!ok) {
@@ -74,6 +75,27 @@ static int beam_vector(const om_beam_array& c) {
                             c.dst_entry})
         low |= (uint64_t)s;
     return (low & 15) == 0 ? 16 : (low & 3) == 0 ? 4 : (low & 1) == 0 ? 2 : 1;
+}
+
+template <int MOST>
+static cudaError_t launch_gather(const BeamGatherShape& shape, const om_beam_array* arrays, int64_t ctas, cudaStream_t st) {
+    BeamGatherArgs<MOST> a;
+    static_cast<BeamGatherShape&>(a) = shape;
+    for (int i = 0; i < shape.count; ++i) a.arrays[i] = arrays[i], a.vector[i] = (unsigned char)beam_vector(arrays[i]);
+    const bool staged = a.in_place && a.beams > kBeamsInRegisters;
+    auto* kern = staged                          ? beam_gather_kernel<kBeamsInRegisters, true, MOST>
+                 : a.beams <= 4                  ? beam_gather_kernel<4, false, MOST>
+                 : (a.beams <= 8 || !a.in_place) ? beam_gather_kernel<8, false, MOST>
+                                                 : beam_gather_kernel<kBeamsInRegisters, false, MOST>;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = early_attribute();
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kBeamGatherThreads);
+    cfg.dynamicSmemBytes = staged ? (size_t)a.beams * kBeamGatherThreads * 16 : 0;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return counted([&] { cudaLaunchKernelEx(&cfg, kern, a); });
 }
 
 }  // namespace om
@@ -127,7 +149,6 @@ om_status om_beam_gather(const int32_t* parents, int64_t batch, int64_t beams, i
         return OM_ERANGE;
     if (batch == 0 || entries == 0) return OM_OK;
     if (parents == nullptr || misaligned4(parents) || misaligned4(starts) || misaligned4(lengths)) return OM_EINVAL;
-    BeamGatherArgs a{};
     int64_t spans[kMaxBeamArrays], src_spans[kMaxBeamArrays], bytes = 0;
     const int64_t counts[4] = {batch, beams, heads, entries};
     int in_place = 0;
@@ -152,14 +173,12 @@ om_status om_beam_gather(const int32_t* parents, int64_t batch, int64_t beams, i
         bool same = c.src == c.dst;
         for (int k = 0; k < 4; ++k) same = same && (from[k] == to[k] || counts[k] == 1);
         in_place += same;
-        a.arrays[i] = c;
-        a.vector[i] = (unsigned char)beam_vector(c);
-        bytes = std::max(bytes, c.entry_bytes / a.vector[i] * entries);  // columns of a row
+        bytes = std::max(bytes, c.entry_bytes / beam_vector(c) * entries);  // columns of a row
     }
     if (in_place != 0 && in_place != count) return OM_EINVAL;
     for (int i = 0; i < count; ++i)
         for (int j = 0; j < count; ++j) {
-            const om_beam_array &c = a.arrays[i], &o = a.arrays[j];
+            const om_beam_array &c = arrays[i], &o = arrays[j];
             auto dst_meets = [&](const void* p, int64_t span, int64_t sb, int64_t sn, int64_t sh, int64_t se) {
                 return arrays_meet(c.dst, spans[i], c.entry_bytes, counts, {c.dst_batch, c.dst_beam, c.dst_head, c.dst_entry},
                                    p, span, o.entry_bytes, counts, {sb, sn, sh, se});
@@ -168,33 +187,20 @@ om_status om_beam_gather(const int32_t* parents, int64_t batch, int64_t beams, i
                 return OM_EINVAL;
             if (i < j && dst_meets(o.dst, spans[j], o.dst_batch, o.dst_beam, o.dst_head, o.dst_entry)) return OM_EINVAL;
         }
-    a.parents = parents;
-    a.starts = starts;
-    a.lengths = lengths;
-    a.entries = entries;
-    a.rows = batch * heads;
-    a.beams = (int)beams;
-    a.heads = (int)heads;
-    a.count = count;
-    a.in_place = in_place != 0;
     DeviceState* d = nullptr;
     om_status s = device_state(&d);
     if (s == OM_OK) s = prepare_beam(d);
     if (s != OM_OK) return s;
     // CTAs of a row: four waves of 8 an SM over all rows, but a column a thread at most
-    const int64_t jobs = a.rows * count;
+    const int64_t jobs = batch * heads * count;
     const int64_t parts = std::min((bytes + kBeamGatherThreads - 1) / kBeamGatherThreads,
                                    std::max<int64_t>(1, 32 * (int64_t)d->sm_count / jobs));
     if (jobs * parts > INT32_MAX) return OM_ERANGE;
-    a.parts = (int)parts;
-    const bool staged = a.in_place && beams > kBeamsInRegisters;
-    auto* kern = staged          ? beam_gather_kernel<kBeamsInRegisters, true>
-                 : beams <= 4    ? beam_gather_kernel<4, false>
-                 : (beams <= 8 || !a.in_place) ? beam_gather_kernel<8, false>
-                                 : beam_gather_kernel<kBeamsInRegisters, false>;
-    const size_t smem = staged ? (size_t)beams * kBeamGatherThreads * 16 : 0;
-    const cudaError_t e = counted(
-        [&] { launch_early(kern, (unsigned)(jobs * parts), kBeamGatherThreads, smem, (cudaStream_t)stream, a); });
+    const BeamGatherShape shape{parents, starts,     lengths, entries,    batch * heads, (int)beams,
+                                (int)heads, count, (int)parts, in_place != 0};
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = count <= kFewBeamArrays ? launch_gather<kFewBeamArrays>(shape, arrays, jobs * parts, st)
+                                                  : launch_gather<kMaxBeamArrays>(shape, arrays, jobs * parts, st);
     return e == cudaSuccess ? OM_OK : cuda_fail(e);
 }
 

@@ -603,13 +603,18 @@ constexpr int kMaxBeamArrays = 64;
 constexpr int kBeamGatherThreads = 128;
 constexpr int kBeamsInRegisters = 16;
 
-struct BeamGatherArgs {
-    om_beam_array arrays[kMaxBeamArrays];
-    unsigned char vector[kMaxBeamArrays];
+struct BeamGatherShape {
     const int32_t *parents, *starts, *lengths;
     int64_t entries, rows;  // rows: batch * heads
     int beams, heads, count, parts, in_place;
 };
+// MOST: arrays that the launch carries (what it carries costs its caller time).
+template <int MOST>
+struct BeamGatherArgs : BeamGatherShape {
+    om_beam_array arrays[MOST];
+    unsigned char vector[MOST];
+};
+constexpr int kFewBeamArrays = 4;
 
 // A column of the beams (the same bytes of one entry in each) belongs to one
 // thread, which loads what its beams get before it stores any of it: so the move
@@ -620,7 +625,7 @@ struct BeamGatherArgs {
 // BEAMS: beams loaded together (all of them in place).  STAGED: in place with
 // more than that many, through shared memory.
 template <typename V, int BEAMS, bool STAGED>
-__device__ __forceinline__ void gather_columns(const BeamGatherArgs& a, const om_beam_array& c, int64_t b, int64_t h,
+__device__ __forceinline__ void gather_columns(const BeamGatherShape& a, const om_beam_array& c, int64_t b, int64_t h,
                                                int part, int64_t lo, int64_t hi) {
     extern __shared__ __align__(16) unsigned char s_stage[];
     const int64_t per = c.entry_bytes / (int)sizeof(V), total = (hi - lo) * per;
@@ -669,8 +674,8 @@ __device__ __forceinline__ void gather_columns(const BeamGatherArgs& a, const om
     }
 }
 
-template <int BEAMS, bool STAGED>
-__global__ void __launch_bounds__(kBeamGatherThreads) beam_gather_kernel(const __grid_constant__ BeamGatherArgs a) {
+template <int BEAMS, bool STAGED, int MOST>
+__global__ void __launch_bounds__(kBeamGatherThreads) beam_gather_kernel(const __grid_constant__ BeamGatherArgs<MOST> a) {
     wait_for_stream();
     const int64_t job = blockIdx.x / a.parts;
     const int part = (int)(blockIdx.x - job * a.parts), k = (int)(job / a.rows);

@@ -72,14 +72,17 @@ def _state_entry(shape, strides, name: str, batch: int, beams: int) -> int:
 
 
 @functools.lru_cache(maxsize=256)
-def _state_geometry(parents_shape, *arrays):
-    """Checks the arrays' shapes and strides (each array: element size, then
-    shape, strides of source and of output) and returns, as om_beam_array wants
-    them, every array's bytes per entry and strides in bytes, then heads, entries
-    and a packer.  Of the shapes alone, so it is kept from call to call."""
+def _state_geometry(parents_shape, in_place, *arrays):
+    """Checks the arrays' shapes and strides (each array: element size, shape and
+    strides, then those of the output if there is another) and returns, as
+    om_beam_array wants them, every array's bytes per entry and strides in bytes,
+    then heads, entries and a packer.  Of the shapes alone, so it is kept from call
+    to call."""
     batch, beams = parents_shape
-    words, common = [], None
-    for size, shape, src_strides, dst_shape, dst_strides in zip(*[iter(arrays)] * 5):
+    words, common, step = [], None, 3 if in_place else 5
+    for i in range(0, len(arrays), step):
+        size, shape, src_strides = arrays[i:i + 3]
+        dst_shape, dst_strides = (shape, src_strides) if in_place else arrays[i + 3:i + 5]
         inner = _state_entry(shape, src_strides, "array", batch, beams)
         if dst_shape != shape or _state_entry(dst_shape, dst_strides, "out", batch, beams) != inner:
             raise ValueError(f"out must have shape {tuple(shape)} (got {tuple(dst_shape)})")
@@ -105,18 +108,24 @@ def om_beam_gather(parents, arrays, starts=None, lengths=None, out=None, stream=
     _dense(parents, "parents", shape, torch.int32)
     if not arrays:
         raise ValueError("no arrays to move")
-    out = arrays if out is None else tuple(out)
+    in_place = out is None
+    out = arrays if in_place else tuple(out)
     if len(out) != len(arrays):
         raise ValueError("out must hold one tensor for each array")
     start_ptr = _row_ints(starts, "starts", shape[0])
     length_ptr = _lengths(lengths, shape[0])
-    handle = _launch_stream(stream, "parents starts lengths array", parents, starts, lengths, *arrays, *out)
+    tensors = arrays if in_place else arrays + out
+    handle = _launch_stream(stream, "parents starts lengths array", parents, starts, lengths, *tensors)
     key = []
-    for src, dst in zip(arrays, out):
-        if dst.dtype != src.dtype:
-            raise ValueError(f"out must be {src.dtype} (got {dst.dtype})")
-        key += (src.element_size(), src.shape, src.stride(), dst.shape, dst.stride())
-    words, heads, entries, pack = _state_geometry(shape, *key)
+    if in_place:
+        for t in arrays:
+            key += (t.element_size(), t.shape, t.stride())
+    else:
+        for src, dst in zip(arrays, out):
+            if dst.dtype != src.dtype:
+                raise ValueError(f"out must be {src.dtype} (got {dst.dtype})")
+            key += (src.element_size(), src.shape, src.stride(), dst.shape, dst.stride())
+    words, heads, entries, pack = _state_geometry(shape, in_place, *key)
     table = []
     for src, dst, fixed in zip(arrays, out, words):
         table += (src.data_ptr(), dst.data_ptr(), *fixed)
