@@ -506,19 +506,18 @@ __global__ void __launch_bounds__(kEmbedSumThreads) embed_sum_kernel(const Embed
 
 // Long runs: the pieces' sums in order.  A run of more than kEmbedPiece places
 // holds a multiple of kEmbedPiece after its start; the first of them is the one
-// that its CTA looks at.  The four warps take a quarter of the pieces each, and
-// their sums are added in order.
+// whose CTA adds them.  A CTA looks at a few multiples, and each of its warps has
+// 128 columns.
 constexpr int kEmbedJoinThreads = 128;
-constexpr int kEmbedJoinColumns = 128;  // four to a lane
-constexpr int kEmbedJoinPlaces = 8;     // multiples of kEmbedPiece that a CTA looks at
+constexpr int kEmbedJoinColumns = 4 * kEmbedJoinThreads;  // four to a lane
+constexpr int kEmbedJoinPlaces = 4;
 
 template <typename O>
 __global__ void __launch_bounds__(kEmbedJoinThreads) embed_join_kernel(const EmbedBackArgs a, int tiles) {
     wait_for_stream();
-    __shared__ float s_sum[kEmbedJoinThreads / 32][kEmbedJoinColumns];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
     const int64_t group = blockIdx.x / tiles;
-    const int column = (int)(blockIdx.x - group * tiles) * kEmbedJoinColumns;
+    const int column = (int)(blockIdx.x - group * tiles) * kEmbedJoinColumns + (int)(threadIdx.x >> 5) * 128 + lane;
     bool mine = false;
     if (lane < kEmbedJoinPlaces) {
         const int64_t at = (group * kEmbedJoinPlaces + lane + 1) * kEmbedPiece, lo = at - kEmbedPiece;
@@ -529,46 +528,41 @@ __global__ void __launch_bounds__(kEmbedJoinThreads) embed_join_kernel(const Emb
         }
     }
     for (unsigned todo = __ballot_sync(0xffffffffu, mine); todo != 0; todo &= todo - 1) {
-        const int64_t at = (group * kEmbedJoinPlaces + __ffs(todo)) * kEmbedPiece;
-        const uint32_t key = a.keys[at];
-        const int64_t start = first_place_warp(a.keys, at - kEmbedPiece, at, key);
+        const int64_t at = (group * kEmbedJoinPlaces + __ffs(todo)) * kEmbedPiece, lo = at - kEmbedPiece;
+        const uint32_t key = a.keys[at], before = a.keys[lo + lane];
+        // keys rise, so that the run's places before this one are the last of these
+        const int64_t start = lo + __ffs(__ballot_sync(0xffffffffu, before == key)) - 1;
         const int64_t end = first_place_warp(a.keys, at, a.n, key + 1);
         if (end - start <= kEmbedPiece) continue;
-        const int64_t pieces = (end - start + kEmbedPiece - 1) / kEmbedPiece, share = (pieces + 3) / 4;
-        const int64_t p0 = min(warp * share, pieces), p1 = min(p0 + share, pieces);
+        const int64_t pieces = (end - start + kEmbedPiece - 1) / kEmbedPiece;
         // piece p starts in the block of kEmbedPiece places p blocks after the run's start
         const float* first = a.partial + piece_slot(start, true) * a.width;
         const float* others = a.partial + piece_slot(start, false) * a.width;
         const int64_t step = 2 * (int64_t)a.width;
         float sum[4] = {};
-        constexpr int U = 4;
-        for (int64_t p = p0; p < p1; p += U) {
+        constexpr int U = 8;
+        for (int64_t p = 0; p < pieces; p += U) {
             float v[U][4];
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int c = column + lane + 32 * k;
-                    v[u][k] = p + u < p1 && c < a.width ? (p + u == 0 ? first : others + (p + u) * step)[c] : 0.0f;
-                }
+                for (int k = 0; k < 4; ++k)
+                    v[u][k] = p + u < pieces && column + 32 * k < a.width
+                                  ? (p + u == 0 ? first : others + (p + u) * step)[column + 32 * k]
+                                  : 0.0f;
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) sum[k] += v[u][k];
         }
+        O* out = static_cast<O*>(a.grad_table) + (int64_t)key * a.table_stride;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s_sum[warp][lane + 32 * k] = sum[k];
-        __syncthreads();
-        const int c = column + (int)threadIdx.x;
-        if (c < a.width) {
-            float total = s_sum[0][threadIdx.x];
-#pragma unroll
-            for (int w = 1; w < kEmbedJoinThreads / 32; ++w) total += s_sum[w][threadIdx.x];
-            O* out = static_cast<O*>(a.grad_table) + (int64_t)key * a.table_stride + c;
-            total *= a.scale;
-            *out = from_float<O>(a.accumulate ? to_float(*out) + total : total);
+        for (int k = 0; k < 4; ++k) {
+            const int c = column + 32 * k;
+            if (c >= a.width) continue;
+            const float x = sum[k] * a.scale;
+            out[c] = from_float<O>(a.accumulate ? to_float(out[c]) + x : x);
         }
-        __syncthreads();
     }
 }
 
