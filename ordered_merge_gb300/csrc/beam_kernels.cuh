@@ -25,7 +25,7 @@ constexpr int kBeamGroup = 8;          // of them are looked at together
 constexpr int kBeamChunk = kBeamThreads * kBeamEach;
 constexpr int kBeamMaxStages = 4;      // chunks in shared memory
 constexpr int kBeamStageBytes = kBeamChunk * 4 + 32;
-constexpr int kBeamCluster = 16;
+constexpr int kBeamCluster = 8;
 // Continuations of all slices up to which the best are found by counting, each its
 // greater ones, instead of by one warp that takes a winner after the other (8 of 128:
 // 700 cycles against 4300).
@@ -103,10 +103,10 @@ struct BeamShared {
     uint64_t full[kBeamMaxStages];
     uint64_t key[kBeamCandidates];
     double lse[kMaxBeams];
-    double base[kMaxBeams];    // of each unit: the sum of exp(x - base)
+    float2 base[kMaxBeams];    // of each unit: the sum of exp(x - base), base in two parts
     uint64_t sum[kMaxBeams];   // (a float)
     float score[kMaxBeams];
-    float group_max[kBeamGroups];
+    uint32_t group_key[kBeamGroups];
     float warp_max[kBeamWarps];
     float warp_scale[kBeamWarps];
     float warp_sum[kBeamWarps];
@@ -133,8 +133,8 @@ __device__ __forceinline__ void store_peer(uint64_t* p, uint32_t rank, uint64_t 
 }
 
 // What a unit found, to the first CTA.
-__device__ __forceinline__ void store_stats(BeamShared& s, int unit, double base, float sum) {
-    store_peer(reinterpret_cast<uint64_t*>(&s.base[unit]), 0, (uint64_t)__double_as_longlong(base));
+__device__ __forceinline__ void store_stats(BeamShared& s, int unit, float base, float rest, float sum) {
+    store_peer(reinterpret_cast<uint64_t*>(&s.base[unit]), 0, pack2(base, rest));
     store_peer(&s.sum[unit], 0, (uint64_t)__float_as_uint(sum));
 }
 
@@ -300,8 +300,11 @@ __device__ __forceinline__ void beam_slice_end(const BeamArgs& a, const BeamSlic
                                                uint64_t* lists, BeamShared& s) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float m = run.most;
-    const float g = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    if ((threadIdx.x & 1) == 0) s.group_max[threadIdx.x >> 1] = g;
+    // a group's maximum, its last bits given up for the group's number: all differ, and a
+    // bound may be a little low
+    const uint32_t group_key = (score_image(fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1))) & ~(uint32_t)(kBeamGroups - 1)) |
+                               (threadIdx.x >> 1);
+    if ((threadIdx.x & 1) == 0) s.group_key[threadIdx.x >> 1] = group_key;
     // NaN stays NaN in these, to be seen at the end
     const float most = warp_max(m), scale = warp_max(run.scale);
     const float all = warp_sum(run.total() * exp2_fast(run.scale - scale));
@@ -309,18 +312,16 @@ __device__ __forceinline__ void beam_slice_end(const BeamArgs& a, const BeamSlic
     if (threadIdx.x == 0) s.found = 0;
     __syncthreads();
     {  // two threads a group, each comparing with half of the groups
-        const int group = (int)threadIdx.x >> 1, half = (int)threadIdx.x & 1;
-        const float mine = s.group_max[group];
         int rank = 0;
-#pragma unroll 8
-        for (int i = half * (kBeamGroups / 2); i < (half + 1) * (kBeamGroups / 2); i += 4) {
-            const float4 o = *reinterpret_cast<const float4*>(&s.group_max[i]);
-            const float other[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) rank += other[k] > mine || (other[k] == mine && i + k < group);
+        const uint4* others = reinterpret_cast<const uint4*>(s.group_key) + (threadIdx.x & 1) * (kBeamGroups / 8);
+#pragma unroll 4
+        for (int i = 0; i < kBeamGroups / 8; ++i) {
+            const uint4 o = others[i];
+            rank += (o.x > group_key) + (o.y > group_key) + (o.z > group_key) + (o.w > group_key);
         }
         rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-        if (rank == a.top - 1) s.bound = mine;
+        // (a logit is at least -inf, whose image the cut does not take below the others')
+        if (rank == a.top - 1) s.bound = image_score(max(group_key & ~(uint32_t)(kBeamGroups - 1), score_image(-INFINITY)));
     }
     if (warp == kBeamWarps - 1) {
         const float wm = warp_max(lane < kBeamWarps ? s.warp_max[lane] : -INFINITY);
@@ -329,47 +330,45 @@ __device__ __forceinline__ void beam_slice_end(const BeamArgs& a, const BeamSlic
         if (lane == 0) {
             s.most = wm;
             s.slow = wm > -INFINITY && !(fabsf(wm) <= kBeamPlain && sum > 0.0f && sum < INFINITY);
-            store_stats(s, unit, wm > -INFINITY ? (double)top_scale * (1.0 / (double)kLog2e) : -INFINITY, wm > -INFINITY ? sum : 0.0f);
+            // the scale over log2e, in two floats
+            constexpr double kBack = 1.0 / (double)kLog2e;
+            constexpr float kBackHigh = (float)kBack, kBackLow = (float)(kBack - (double)kBackHigh);
+            const float base = top_scale * kBackHigh, rest = fmaf(top_scale, kBackHigh, -base) + top_scale * kBackLow;
+            if (wm > -INFINITY) store_stats(s, unit, base, rest, sum);
+            else store_stats(s, unit, -INFINITY, 0.0f, 0.0f);
         }
     }
     __syncthreads();
     const float bound = s.bound;
     const int words = slice.words();
-    auto found_one = [&](float x, int i) {
-        const int at = atomicAdd(&s.found, 1);
-        if (at < kBeamCandidates) s.key[at] = beam_key(x, slice.first + i);
-    };
-    // two eights' logits (the second's first word past the end where there is none): all of them, then a look at each
-    auto look = [&](int first, int second) {
+    // 16 words, `step` apart within an eight (the second eight past the end where there is none):
+    // loaded together, then the few that reach the bound one by one
+    auto look = [&](int first, int second, int step) {
+        unsigned near = 0;
         uint32_t w[2 * kBeamGroup];
 #pragma unroll
-        for (int i = 0; i < 2 * kBeamGroup; ++i)
-            w[i] = slice.word((i < kBeamGroup ? first : second) + i % kBeamGroup * kBeamThreads);
+        for (int i = 0; i < 2 * kBeamGroup; ++i) w[i] = slice.word((i < kBeamGroup ? first : second) + i % kBeamGroup * step);
 #pragma unroll
         for (int i = 0; i < 2 * kBeamGroup; ++i) {
-            const int at = ((i < kBeamGroup ? first : second) + i % kBeamGroup * kBeamThreads) * WordOf<T>::kPer;
             const float2 x = word_values(w[i], T{});
-            if (x.x >= bound && x.x > -INFINITY) found_one(x.x, at);
-            if (x.y >= bound && x.y > -INFINITY) found_one(x.y, at + 1);
+            near |= (x.x >= bound && x.x > -INFINITY ? 1u << 2 * i : 0u) | (x.y >= bound && x.y > -INFINITY ? 2u << 2 * i : 0u);
+        }
+        for (; near != 0; near &= near - 1) {
+            const int bit = __ffs(near) - 1, i = bit >> 1;
+            const int word = (i < kBeamGroup ? first : second) + i % kBeamGroup * step;
+            const float2 x = word_values(slice.word(word), T{});
+            const int at = atomicAdd(&s.found, 1);
+            if (at < kBeamCandidates) s.key[at] = beam_key(bit & 1 ? x.y : x.x, slice.first + word * WordOf<T>::kPer + (bit & 1));
         }
     };
     const bool thrice = run.third >= bound && run.third > -INFINITY;
     if (!thrice && m >= bound && m > -INFINITY)
         look(run.where * kBeamGroup * kBeamThreads + (int)threadIdx.x,
-             run.second >= bound && run.second > -INFINITY ? run.next * kBeamGroup * kBeamThreads + (int)threadIdx.x : words);
+             run.second >= bound && run.second > -INFINITY ? run.next * kBeamGroup * kBeamThreads + (int)threadIdx.x : words,
+             kBeamThreads);
     for (unsigned todo = __ballot_sync(0xffffffffu, thrice); todo != 0; todo &= todo - 1)
-        for (int w = warp * 32 + __ffs(todo) - 1 + lane * kBeamThreads; w < words; w += 64 * kBeamGroup * kBeamThreads) {
-            uint32_t v[2 * kBeamGroup];
-#pragma unroll
-            for (int i = 0; i < 2 * kBeamGroup; ++i) v[i] = slice.word(w + 32 * i * kBeamThreads);
-#pragma unroll
-            for (int i = 0; i < 2 * kBeamGroup; ++i) {
-                const int at = (w + 32 * i * kBeamThreads) * WordOf<T>::kPer;
-                const float2 x = word_values(v[i], T{});
-                if (x.x >= bound && x.x > -INFINITY) found_one(x.x, at);
-                if (x.y >= bound && x.y > -INFINITY) found_one(x.y, at + 1);
-            }
-        }
+        for (int w = warp * 32 + __ffs(todo) - 1 + lane * kBeamThreads; w < words; w += 64 * kBeamGroup * kBeamThreads)
+            look(w, w + 32 * kBeamGroup * kBeamThreads, 32 * kBeamThreads);
     __syncthreads();
     if (s.slow) {
         float sum = 0.0f;
@@ -384,7 +383,7 @@ __device__ __forceinline__ void beam_slice_end(const BeamArgs& a, const BeamSlic
         if (threadIdx.x == 0) {
             float all_warps = 0.0f;
             for (int i = 0; i < kBeamWarps; ++i) all_warps += s.warp_sum[i];
-            store_stats(s, unit, (double)s.most, all_warps);
+            store_stats(s, unit, s.most, 0.0f, all_warps);
         }
     }
     int found = s.found;
@@ -434,12 +433,28 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
     const uint32_t ctas = cluster_size(), rank = cluster_rank();
     const int64_t b = blockIdx.x / ctas;
     const int units = a.beams * a.parts;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < a.stages; ++i) mbar_init(&s.full[i], 1);
-        fence_barrier_init();
-    }
+    const uint64_t policy = l2_policy_evict_first();
+    // thread 0: slices to come, where the next chunk starts, and bytes left of its slice
+    int live = 0, next_slice = 0;
+    int64_t left = 0;
+    uintptr_t from = 0;
+    auto fill = [&](int stage) {
+        if (left <= 0) {
+            if (next_slice >= live) return;
+            const BeamSlice<T> slice(a, b, s.unit[next_slice++]);
+            from = reinterpret_cast<uintptr_t>(slice.row + slice.first);
+            left = (int64_t)slice.n * (int)sizeof(T);
+        }
+        const uint32_t skip = (uint32_t)(from & 15), whole = (skip + (uint32_t)min((int64_t)kBeamChunk * 4, left) + 15) & ~15u;
+        mbar_arrive_expect_tx(&s.full[stage], whole);
+        bulk_copy_g2s(ring + stage * kBeamStageBytes, reinterpret_cast<const void*>(from - skip), whole, &s.full[stage], policy);
+        from += kBeamChunk * 4, left -= kBeamChunk * 4;
+    };
     if (threadIdx.x < 32) {  // the slices of this CTA that have logits to look at
-        int live = 0;
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < a.stages; ++i) mbar_init(&s.full[i], 1);
+            fence_barrier_init();
+        }
         for (int u0 = (int)rank; u0 < units; u0 += 32 * (int)ctas) {
             const int u = u0 + (int)threadIdx.x * (int)ctas;
             bool looks = false;
@@ -453,35 +468,18 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
             if (looks) s.unit[live + __popc(there & ((1u << threadIdx.x) - 1))] = (uint8_t)u;
             live += __popc(there);
         }
-        if (threadIdx.x == 0) s.live = live;
-    }
-    // slices without logits to look at leave these as they are
-    if (rank == 0) {
-        for (int i = threadIdx.x; i < units; i += kBeamThreads) s.base[i] = -INFINITY, s.sum[i] = 0;
-        for (int i = threadIdx.x; i < units * a.top; i += kBeamThreads) lists[i] = 0;
+        __syncwarp();
+        if (threadIdx.x == 0) {
+            s.live = live;
+            for (int i = 0; i < a.stages; ++i) fill(i);
+        }
+    } else if (rank == 0) {  // slices without logits to look at leave these as they are
+        for (int i = threadIdx.x - 32; i < units; i += kBeamThreads - 32) s.base[i] = make_float2(-INFINITY, 0.0f), s.sum[i] = 0;
+        for (int i = threadIdx.x - 32; i < units * a.top; i += kBeamThreads - 32) lists[i] = 0;
     }
     __syncthreads();
     if (ctas > 1) cluster_arrive();  // and wait before the first store to the first CTA's shared memory
-
-    const int live = s.live;
-    const uint64_t policy = l2_policy_evict_first();
-    // thread 0: where the next chunk starts, and bytes left of its slice
-    int next_slice = 0, left = 0;
-    uintptr_t from = 0;
-    auto fill = [&](int stage) {
-        if (left <= 0) {
-            if (next_slice >= live) return;
-            const BeamSlice<T> slice(a, b, s.unit[next_slice++]);
-            from = reinterpret_cast<uintptr_t>(slice.row + slice.first);
-            left = slice.n * (int)sizeof(T);
-        }
-        const uint32_t skip = (uint32_t)(from & 15), whole = (skip + (uint32_t)min(kBeamChunk * 4, left) + 15) & ~15u;
-        mbar_arrive_expect_tx(&s.full[stage], whole);
-        bulk_copy_g2s(ring + stage * kBeamStageBytes, reinterpret_cast<const void*>(from - skip), whole, &s.full[stage], policy);
-        from += kBeamChunk * 4, left -= kBeamChunk * 4;
-    };
-    if (threadIdx.x == 0)
-        for (int i = 0; i < a.stages; ++i) fill(i);
+    live = s.live;
     int stage = 0;
     uint32_t phase = 0;
     for (int k = 0; k < live; ++k) {
@@ -511,18 +509,21 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
     uint64_t* images = lists + units * a.top;
     if (threadIdx.x < a.beams) {
         const int i = threadIdx.x;
-        double most = -INFINITY;
-        for (int p = 0; p < a.parts; ++p) most = fmax(most, s.base[i * a.parts + p]);
+        float2 most = s.base[i * a.parts];
+        for (int p = 1; p < a.parts; ++p) {
+            const float2 base = s.base[i * a.parts + p];
+            if (base.x > most.x) most = base;
+        }
         float sum = 0.0f;
         for (int p = 0; p < a.parts; ++p) {
             const float part = __uint_as_float((uint32_t)s.sum[i * a.parts + p]);
-            const double base = s.base[i * a.parts + p];
-            if (base > -INFINITY) sum += base == most ? part : part * exp2_fast((float)(base - most) * kLog2e);
+            const float2 base = s.base[i * a.parts + p];
+            if (base.x > -INFINITY) sum += part * (base.x == most.x && base.y == most.y ? 1.0f : exp2_fast(((base.x - most.x) + (base.y - most.y)) * kLog2e));
         }
         // the logarithm of a sum as its exponent's and its fraction's, of which only the latter is rounded to 32 bits
         const int exponent = (int)(__float_as_uint(sum) >> 23) - 127;
         const float fraction = __uint_as_float((__float_as_uint(sum) & 0x7fffffu) | 0x3f800000u);
-        s.lse[i] = sum > 0.0f ? most + (exponent * 0.6931471805599453 + (double)logf(fraction)) : (double)NAN;
+        s.lse[i] = sum > 0.0f ? (double)most.x + ((double)(most.y + logf(fraction)) + exponent * 0.6931471805599453) : (double)NAN;
         s.score[i] = a.scores == nullptr ? 0.0f : a.scores[b * a.beams + i];
     }
     __syncthreads();
