@@ -571,10 +571,10 @@ om_status om_embed_lookup(int value_type, const void *table, int64_t rows,
  * every row (zeros where no token asks for it).  table_type is value_type or
  * OM_VALUE_F32; grad_table is rounded once.  ids outside [0, rows) count for
  * nothing.  The tokens are sorted stably and each row's terms added in 32 bits in
- * the order of i, in pieces of 32 that are then added in their order: the same
- * call repeats bit for bit.
- * Takes stream-ordered scratch from the library's pool: 16 n bytes and,
- * with n > 32, n * width / 4.  n <= 2^30, width <=
+ * the order of i, in pieces of 32 (of 128 where n > 16384) that are then added in
+ * their order: the same call repeats bit for bit.
+ * Takes stream-ordered scratch from the library's pool: 16 n bytes and, with n >
+ * 32, n * width / 4 (a quarter of that where n > 16384).  n <= 2^30, width <=
  * 2^20, n * width < 2^38, rows and strides as above, else OM_ERANGE.
  */
 om_status om_embed_lookup_backward(int value_type, const void *grad, int64_t n,

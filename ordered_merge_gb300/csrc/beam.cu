@@ -113,7 +113,7 @@ om_status om_beam_select(int value_type, const void* logits, int64_t batch, int6
         return OM_EINVAL;
     if (finished != nullptr && (end_id < 0 || end_id >= vocab)) return OM_EINVAL;
     if (beams > kMaxBeams || top > kMaxBeamTop || vocab > (1 << 30) || batch > (1 << 24) || batch_stride > kMaxStride ||
-        beam_stride > kMaxStride)
+        beam_stride > kMaxStride || too_far(batch, batch_stride))
         return OM_ERANGE;
     if (batch == 0) return OM_OK;
     if (logits == nullptr || out_scores == nullptr || out_parents == nullptr || out_tokens == nullptr ||

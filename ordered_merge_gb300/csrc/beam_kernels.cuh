@@ -115,6 +115,7 @@ struct BeamShared {
     float bound;
     int found;        // logits that reach the bound
     int count;        // (settling) those counted
+    int ties[kBeamWarps];
     int live;         // units of this CTA that have logits to look at
     uint8_t unit[kMaxBeams];
 };
@@ -168,9 +169,8 @@ struct BeamSlice {
     }
 };
 
-// The top-th greatest key of a slice too full of equal or near values for the
-// candidates' room (rows of one value, of few values not masked by the type's
-// lowest): its bits one after another, each by a count over the slice.  All threads.
+// The top-th greatest key of a slice too full of near values for the candidates'
+// room: its bits one after another, each by a count over the slice.  All threads.
 template <typename T>
 __device__ __noinline__ uint64_t settle_edge(const BeamSlice<T>& slice, int top, BeamShared& s) {
     uint64_t edge = 0;
@@ -198,6 +198,56 @@ __device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
     uint64_t p;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(x), "l"(y), "l"(z));
     return p;
+}
+
+// The candidates of a slice of which too many reach the bound.  Most often these are
+// ties with the bound itself (rows of one value; of few values and the type's lowest
+// for what is masked): then fewer than `top` are greater, and the first of the ties
+// fill up.  All threads; returns how many keys there are.
+template <typename T>
+__device__ __noinline__ int crowded_slice(const BeamSlice<T>& slice, int top, BeamShared& s) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float bound = s.bound;
+    if (threadIdx.x == 0) s.found = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = threadIdx.x; i < slice.n; i += kBeamThreads) {
+        const float x = slice.at(i);
+        if (x > bound) {
+            const int at = atomicAdd(&s.found, 1);
+            if (at < kBeamCandidates) s.key[at] = beam_key(x, slice.first + i);
+        }
+    }
+    __syncthreads();
+    int have = s.found;
+    if (have < top) {
+        for (int i0 = 0; i0 < slice.n && have < top; i0 += kBeamThreads) {
+            const int i = i0 + (int)threadIdx.x;
+            const unsigned ties = __ballot_sync(0xffffffffu, i < slice.n && slice.at(i) == bound);
+            if (lane == 0) s.ties[warp] = __popc(ties);
+            __syncthreads();
+            int before = have, all = 0;
+            for (int w = 0; w < kBeamWarps; ++w) before += w < warp ? s.ties[w] : 0, all += s.ties[w];
+            before += __popc(ties & ((1u << lane) - 1));
+            if ((ties >> lane & 1) && before < top) s.key[before] = beam_key(bound, slice.first + i);
+            have = min(have + all, top);
+            __syncthreads();
+        }
+        return have;
+    }
+    const uint64_t edge = settle_edge(slice, top, s);
+    if (threadIdx.x == 0) s.found = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < slice.n; i += kBeamThreads) {
+        const float x = slice.at(i);
+        const uint64_t key = beam_key(x, slice.first + i);
+        if (x > -INFINITY && (key & WordOf<T>::kKeyBits) >= edge) {
+            const int at = atomicAdd(&s.found, 1);  // `top` of them: keys differ
+            if (at < kBeamCandidates) s.key[at] = key;
+        }
+    }
+    __syncthreads();
+    return min(s.found, kBeamCandidates);
 }
 
 // What a thread keeps of the words it has seen, 8 at a time ("eights"): the greatest
@@ -387,21 +437,7 @@ __device__ __forceinline__ void beam_slice_end(const BeamArgs& a, const BeamSlic
         }
     }
     int found = s.found;
-    if (found > kBeamCandidates) {
-        const uint64_t edge = settle_edge(slice, a.top, s);
-        if (threadIdx.x == 0) s.found = 0;
-        __syncthreads();
-        for (int i = threadIdx.x; i < slice.n; i += kBeamThreads) {
-            const float x = slice.at(i);
-            const uint64_t key = beam_key(x, slice.first + i);
-            if (x > -INFINITY && (key & WordOf<T>::kKeyBits) >= edge) {
-                const int at = atomicAdd(&s.found, 1);  // `top` of them: keys differ
-                if (at < kBeamCandidates) s.key[at] = key;
-            }
-        }
-        __syncthreads();
-        found = min(s.found, kBeamCandidates);
-    }
+    if (found > kBeamCandidates) found = crowded_slice(slice, a.top, s);
     uint64_t* list = lists + unit * a.top;
     for (int c = threadIdx.x; c < found; c += kBeamThreads) {
         const uint64_t mine = s.key[c];

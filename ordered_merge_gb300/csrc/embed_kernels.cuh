@@ -103,13 +103,16 @@ struct EmbedBackArgs {
     int width, wide, accumulate;
     int tiles;            // column tiles of a row
     int window;           // sorted places of a warp
+    int piece;            // tokens of a long run that one warp sums
     int passes, bits;     // (sorting) digits of a key and bits of a digit
     int64_t sum_ctas;     // CTAs that sum; those after them write zeros
     int zero_rows;        // rows of a warp of them
     float scale;
 };
 
-constexpr int kEmbedPiece = 32;  // tokens of a run that one warp sums
+// Tokens of a run that one warp sums: of few tokens, and of many.
+constexpr int kEmbedPiece = 32;
+constexpr int kEmbedLongPiece = 128;
 
 // ---- the sort: one cluster, least digit first
 //
@@ -346,10 +349,12 @@ __device__ __forceinline__ int64_t first_place_warp(const uint32_t* keys, int64_
     return lo;
 }
 
-// The slot of a piece's sum in `partial`: pieces start at multiples of
-// kEmbedPiece from their run's start, so at most one piece that goes on a run and
-// one that starts a long run start in the same kEmbedPiece places.
-__device__ __forceinline__ int64_t piece_slot(int64_t at, bool first) { return 2 * (at / kEmbedPiece) + first; }
+// The slot of a piece's sum in `partial`: pieces start at multiples of a.piece from
+// their run's start, so at most one piece that goes on a run and one that starts a
+// long run start in the same a.piece places.
+__device__ __forceinline__ int64_t piece_slot(const EmbedBackArgs& a, int64_t at, bool first) {
+    return 2 * (int64_t)((uint32_t)at / (uint32_t)a.piece) + first;
+}
 
 // N sums of a lane to a row of the table's gradient (scaled), or as they are.
 template <typename O, int N>
@@ -397,7 +402,7 @@ __device__ __forceinline__ void zero_rows(const EmbedBackArgs& a, int64_t warp) 
 }
 
 // A warp looks after the pieces that start in its window of sorted places, for a
-// tile of 32 N columns.  A piece is a run of equal tokens, or up to kEmbedPiece
+// tile of 32 N columns.  A piece is a run of equal tokens, or up to a.piece
 // places of a longer one, counted from its start; so those of a window are
 // neighbours, and the warp streams their rows, 16 in flight through shared memory
 // (each lane copies and reads its own vectors: no barrier), adding each to the sum
@@ -436,7 +441,7 @@ __global__ void __launch_bounds__(kEmbedSumThreads) embed_sum_kernel(const Embed
         if (run_start && next_key != row) {
             store_sums<O, N>(a, row, column, sum);
         } else {
-            float* out = a.partial + piece_slot(at, run_start) * a.width + column;
+            float* out = a.partial + piece_slot(a, at, run_start) * a.width + column;
 #pragma unroll
             for (int k = 0; k < N; ++k) out[k] = sum[k];
         }
@@ -454,16 +459,16 @@ __global__ void __launch_bounds__(kEmbedSumThreads) embed_sum_kernel(const Embed
         const unsigned outside = __ballot_sync(0xffffffffu, key >= (uint32_t)a.rows);
         const unsigned firsts = __ballot_sync(0xffffffffu, first);
         // Further pieces of a long run among these places: only of the run that the first
-        // one is in the midst of (one that starts here has its next piece 32 places on).
+        // one is in the midst of (one that starts here has its next piece 32 places on at least).
         const uint32_t key0 = __shfl_sync(0xffffffffu, key, 0);
-        if (!(firsts & 1) && base >= kEmbedPiece - 31 && key0 < (uint32_t)a.rows) {
-            const int64_t back = max(base - kEmbedPiece + 1, (int64_t)0);
-            // where that run started, if it was less than a piece ago, or else by a search
+        if (!(firsts & 1) && key0 < (uint32_t)a.rows) {
+            // where that run started, if it was in the 32 places before, or else by a search
+            const int64_t back = max(base - 32, (int64_t)0);
             const unsigned there = __ballot_sync(0xffffffffu, back + lane < base && a.keys[back + lane] != key0);
             int64_t run;
             if (there != 0) run = back + 32 - __clz(there);
             else run = first_place_warp(a.keys, 0, back, key0);
-            if (mine < a.n && key == key0 && !first) starts = (mine - run) % kEmbedPiece == 0;
+            if (mine < a.n && key == key0 && !first) starts = (uint32_t)(mine - run) % (uint32_t)a.piece == 0;
         }
         const unsigned start = __ballot_sync(0xffffffffu, starts);
         const unsigned window = base > lo ? 0u : a.window >= 32 ? 0xffffffffu : (1u << a.window) - 1;
@@ -504,8 +509,8 @@ __global__ void __launch_bounds__(kEmbedSumThreads) embed_sum_kernel(const Embed
     }
 }
 
-// Long runs: the pieces' sums in order.  A run of more than kEmbedPiece places
-// holds a multiple of kEmbedPiece after its start; the first of them is the one
+// Long runs: the pieces' sums in order.  A run of more than a.piece places
+// holds a multiple of a.piece after its start; the first of them is the one
 // whose CTA adds them.  A CTA looks at a few multiples, and each of its warps has
 // 128 columns.
 constexpr int kEmbedJoinThreads = 128;
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(kEmbedJoinThreads) embed_join_kernel(const Emb
     const int column = (int)(blockIdx.x - group * tiles) * kEmbedJoinColumns + (int)(threadIdx.x >> 5) * 128 + lane;
     bool mine = false;
     if (lane < kEmbedJoinPlaces) {
-        const int64_t at = (group * kEmbedJoinPlaces + lane + 1) * kEmbedPiece, lo = at - kEmbedPiece;
+        const int64_t at = (group * kEmbedJoinPlaces + lane + 1) * a.piece, lo = at - a.piece;
         if (at < a.n) {
             const uint32_t key = a.keys[at], last = a.keys[at - 1], low = a.keys[lo];
             const uint32_t lower = lo > 0 ? a.keys[lo - 1] : 0xffffffffu;
@@ -528,19 +533,18 @@ __global__ void __launch_bounds__(kEmbedJoinThreads) embed_join_kernel(const Emb
         }
     }
     for (unsigned todo = __ballot_sync(0xffffffffu, mine); todo != 0; todo &= todo - 1) {
-        const int64_t at = (group * kEmbedJoinPlaces + __ffs(todo)) * kEmbedPiece, lo = at - kEmbedPiece;
-        const uint32_t key = a.keys[at], before = a.keys[lo + lane];
-        // keys rise, so that the run's places before this one are the last of these
-        const int64_t start = lo + __ffs(__ballot_sync(0xffffffffu, before == key)) - 1;
+        const int64_t at = (group * kEmbedJoinPlaces + __ffs(todo)) * a.piece;
+        const uint32_t key = a.keys[at];
+        const int64_t start = first_place_warp(a.keys, at - a.piece, at, key);
         const int64_t end = first_place_warp(a.keys, at, a.n, key + 1);
-        if (end - start <= kEmbedPiece) continue;
-        const int64_t pieces = (end - start + kEmbedPiece - 1) / kEmbedPiece;
-        // piece p starts in the block of kEmbedPiece places p blocks after the run's start
-        const float* first = a.partial + piece_slot(start, true) * a.width;
-        const float* others = a.partial + piece_slot(start, false) * a.width;
+        if (end - start <= a.piece) continue;
+        const int64_t pieces = (end - start + a.piece - 1) / a.piece;
+        // piece p starts in the block of a.piece places p blocks after the run's start
+        const float* first = a.partial + piece_slot(a, start, true) * a.width;
+        const float* others = a.partial + piece_slot(a, start, false) * a.width;
         const int64_t step = 2 * (int64_t)a.width;
         float sum[4] = {};
-        constexpr int U = 8;
+        constexpr int U = 16;
         for (int64_t p = 0; p < pieces; p += U) {
             float v[U][4];
 #pragma unroll

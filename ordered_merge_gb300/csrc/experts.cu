@@ -179,14 +179,18 @@ om_status om_expert_mlp(int value_type, const void* x, int64_t tokens, int64_t h
     cudaStream_t st = (cudaStream_t)stream;
     ExpertArgs a{};
     a.x = x, a.ids = ids, a.weights = weights, a.up = up, a.gate = gate, a.down = down, a.out = out;
-    a.x_stride = x_stride, a.out_stride = out_stride;
-    a.up_expert = up_expert, a.up_row = up_row, a.gate_expert = gate_expert, a.gate_row = gate_row;
-    a.down_expert = down_expert, a.down_row = down_row;
+    // a stride that takes no step says nothing about alignment
+    auto stride = [](int64_t count, int64_t s) { return count > 1 ? s : 0; };
+    a.x_stride = stride(tokens, x_stride), a.out_stride = out_stride;
+    a.up_expert = stride(experts, up_expert), a.up_row = stride(inner, up_row);
+    a.gate_expert = stride(experts, gate_expert), a.gate_row = stride(inner, gate_row);
+    a.down_expert = stride(experts, down_expert), a.down_row = stride(hidden, down_row);
     a.tokens = (int)tokens, a.picks = (int)picks, a.slots = (int)slots, a.experts = (int)experts;
     a.hidden = (int)hidden, a.inner = (int)inner, a.inner_pad = (int)((inner + 7) / 8 * 8), a.act = act;
     // whole vectors where every row starts on 16 bytes and holds a multiple of them
     bool vec = hidden % 8 == 0 && inner % 8 == 0;
-    for (const int64_t v : {x_stride, up_expert, up_row, gate_expert, gate_row, down_expert, down_row}) vec = vec && v % 8 == 0;
+    for (const int64_t v : {a.x_stride, a.up_expert, a.up_row, a.gate_expert, a.gate_row, a.down_expert, a.down_row})
+        vec = vec && v % 8 == 0;
     for (const void* p : {x, up, gate, down}) vec = vec && !misaligned(p, 16);
     const size_t half = (size_t)slots * a.inner_pad * 2;  // a multiple of 16
     cudaError_t e = scratch_alloc(pool, &a.high, 2 * half + (vec ? (size_t)slots * hidden * 4 : 0), st);

@@ -13,6 +13,9 @@ namespace om {
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 constexpr int64_t kMaxEntryStride = (int64_t)1 << 30;
 
+// Whether `count` steps of `stride` go further than any array (and than 64 bits hold with others beside).
+inline bool too_far(int64_t count, int64_t stride) { return count > 1 && stride > ((int64_t)1 << 58) / (count - 1); }
+
 // Bytes from the first to past the last of a strided array whose entries have
 // `bytes` bytes; *shared says whether entries share bytes (which an output's must not).
 template <int N>

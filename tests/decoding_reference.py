@@ -60,7 +60,7 @@ def check_beams(got, logits, top, scores=None, finished=None, end_id=0):
 
 
 def embed_backward(grad, ids, rows, scale=1.0, base=None):
-    """(gradient of the table, error bound of its sum in 32 bits): pieces of 32 terms, then the pieces."""
+    """(gradient of the table, error bound of its sum in 32 bits): pieces of 32 or 128 terms, then the pieces."""
     g, i = grad.double().flatten(0, -2), ids.flatten().long()
     there = (i >= 0) & (i < rows)
     g, i = g[there], i[there]
@@ -69,7 +69,7 @@ def embed_backward(grad, ids, rows, scale=1.0, base=None):
     size = torch.zeros_like(total).index_add_(0, i, g.abs())
     count = torch.bincount(i, minlength=rows).double()[:, None]
     total, size = total * scale, size * abs(scale)
-    error = E32 * (count.clamp(max=32) + count / 32 + 3) * size
+    error = E32 * (count.clamp(max=128) + count / 32 + 3) * size
     if base is not None:
         total = total + base.double()
         error = error + E32 * total.abs()

@@ -24,7 +24,8 @@ def test_beam_select_refusals(om):
                 dict(out=0x100000), dict(tok=0x100000 + 2396), dict(par=0x30000), dict(tok=0x40000 + 28), dict(out=0x10000),
                 dict(par=0x20004), dict(out=0x100000 - 28)):
         assert call(**bad) == om.OM_EINVAL, bad
-    for bad in (dict(n=65), dict(top=65), dict(v=(1 << 30) + 1), dict(b=(1 << 24) + 1), dict(bs=1 << 41), dict(ns=1 << 41)):
+    for bad in (dict(n=65), dict(top=65), dict(v=(1 << 30) + 1), dict(b=(1 << 24) + 1), dict(bs=1 << 41), dict(ns=1 << 41),
+                dict(b=1 << 24, bs=1 << 40)):
         assert call(**bad) == om.OM_ERANGE, bad
     assert call(b=0, x=None, out=None) == om.OM_OK
 
@@ -70,7 +71,7 @@ def test_embed_lookup_refusals(om):
                 dict(out=0x20001), dict(os=63), dict(out=0x100000), dict(out=0x10000), dict(out=0x100000 - 1278)):
         assert call(**bad) == om.OM_EINVAL, bad
     for bad in (dict(rows=(1 << 31) - 1), dict(n=1 << 31), dict(w=(1 << 24) + 1, ts=1 << 25, os=1 << 25), dict(ts=1 << 41),
-                dict(os=1 << 41)):
+                dict(os=1 << 41), dict(rows=1 << 30, ts=1 << 40), dict(n=1 << 30, os=1 << 40)):
         assert call(**bad) == om.OM_ERANGE, bad
     assert call(n=0, table=None, ids=None, out=None) == om.OM_OK
 
@@ -87,7 +88,7 @@ def test_embed_backward_refusals(om):
                 dict(table=0x10040)):
         assert call(**bad) == om.OM_EINVAL, bad
     for bad in (dict(rows=(1 << 31) - 1), dict(n=(1 << 30) + 1), dict(w=(1 << 20) + 1, gs=1 << 21, ts=1 << 21), dict(gs=1 << 41),
-                dict(ts=1 << 41), dict(n=1 << 22, w=1 << 20, gs=1 << 20, ts=1 << 20, grad=0x10000000000000, ids=0x20000000000000)):
+                dict(ts=1 << 41), dict(n=1 << 30, gs=1 << 40), dict(rows=1 << 30, ts=1 << 40), dict(n=1 << 22, w=1 << 20, gs=1 << 20, ts=1 << 20, grad=0x10000000000000, ids=0x20000000000000)):
         assert call(**bad) == om.OM_ERANGE, bad
     assert call(rows=0, table=None) == om.OM_OK
 

@@ -76,6 +76,21 @@ def test_constant_and_nearly_constant_rows(gpu, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("low", ["lowest", 0.0])
+def test_few_logits_above_many_equal_ones(gpu, dtype, low):
+    """A grammar's few tokens, all others at one value: the first of these fill up, wherever they are."""
+    low = torch.finfo(dtype).min if low == "lowest" else low
+    for vocab, top in ((2000, 8), (70001, 20), (131071, 64)):
+        logits = torch.full((3, 2, vocab), low, dtype=dtype, device="cuda")
+        for b in range(3):
+            at = torch.randperm(vocab, generator=torch.Generator(device="cuda").manual_seed(b), device="cuda")[:5 * b + 1]
+            logits[b, :, at] = torch.arange(5.0 * b + 1, device="cuda").to(dtype) + 1
+        logits[2, 0, :vocab // 2] = -INF
+        logits[1, 1, :600] = float("nan")
+        _check(gpu, logits, top, torch.tensor([[-1.0, -1.25], [-2.0, -1.0], [-1.0, -1.0]], device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_ascending_rows(gpu, dtype):
     """The greatest logits all at the end, in one thread's part, and equal in groups."""
     ramp = (torch.arange(30011, device="cuda") // 7).float() / 400
@@ -100,6 +115,17 @@ def test_masked_logits(gpu, dtype, vocab):
     logits[3, :, :5] = torch.arange(5.0, device="cuda").to(dtype)
     out, parents, tokens = _check(gpu, logits, 20, scores)
     assert torch.all(parents[2] == -1) and torch.all(parents[3, 15:] == -1) and torch.all(parents[3, :15] >= 0)
+
+
+def test_large_logits(gpu):
+    """Magnitudes at which a product with log2 e rounds to more than a step of the sum, and the greatest of all."""
+    for size in (1e3, 9.9e5, 1.1e6, 1e20, 1e38):
+        logits, scores = _logits(2, 3, 5001, torch.float32)
+        _check(gpu, logits / 12 * size, 6, scores)
+        _check(gpu, logits + size, 6, scores)
+        _check(gpu, logits - size, 6, scores)
+        logits[:, :, 3000:] = -torch.finfo(torch.float32).max
+        _check(gpu, logits + size, 6, scores)
 
 
 def test_infinite_logits_and_scores(gpu):

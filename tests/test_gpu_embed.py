@@ -130,6 +130,21 @@ def test_backward_many_tokens(gpu):
         _check_backward(gpu, grad, IDS[kind](n, rows, gen), rows)
 
 
+@pytest.mark.parametrize("n", [8191, 8192, 8193, 16384, 16385, 40_000, 262_144, 262_145])
+def test_backward_ways_of_sorting(gpu, n):
+    """Tokens up to which they are counted, sorted by one cluster, and merged; short and long pieces."""
+    gen = _gen(n)
+    for rows, width in ((3000, 16), (1, 8), (600_000, 4)):
+        grad = torch.randn(n, width, generator=gen, device="cuda")
+        for kind in ("skewed", "one", "outside"):
+            _check_backward(gpu, grad, IDS[kind](n, rows, gen), rows)
+    # a run that ends, and one that starts, at every place around a piece's end
+    lengths = torch.arange(1, 2 * int((2 * n) ** 0.5), device="cuda")
+    ids = torch.repeat_interleave(torch.arange(len(lengths), device="cuda"), lengths)[:n]
+    ids = ids[torch.randperm(len(ids), generator=gen, device="cuda")].contiguous()
+    _check_backward(gpu, torch.randn(len(ids), 8, generator=gen, device="cuda"), ids, len(lengths))
+
+
 def test_backward_strided_table_and_guards(gpu):
     gen = _gen(11)
     for shift in range(5):
