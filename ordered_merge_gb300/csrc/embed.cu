@@ -47,7 +47,7 @@ static om_status prepare_embed(const DeviceState* d) {
     std::lock_guard<std::mutex> lk(mu);
     if (!ready[d->dev]) {
         if (cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-            cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kEmbedSortSmem) !=
+            cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)embed_sort_smem(kEmbedSortMost / kEmbedCluster)) !=
                 cudaSuccess) {
             cudaGetLastError();
             return OM_ECUDA;
@@ -83,7 +83,7 @@ static cudaError_t launch_backward(EmbedBackArgs a, int sm_count, cudaStream_t s
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(cluster_for(a.n));
             cfg.blockDim = dim3(kEmbedSortThreads);
-            cfg.dynamicSmemBytes = kEmbedSortSmem;
+            cfg.dynamicSmemBytes = embed_sort_smem((a.n + cfg.gridDim.x - 1) / cfg.gridDim.x);
             cfg.stream = st;
             cudaLaunchAttribute attr[2] = {early_attribute()};
             attr[1].id = cudaLaunchAttributeClusterDimension;

@@ -49,6 +49,10 @@ constexpr int kEmbedUnroll = 4;
 
 // CTAs of two warps take a tile of 256 vectors: several short rows or a piece of
 // a long one.  All tokens first, then all vectors: two trips to memory.
+//
+// Bound by memory: 65536 rows of 2048 bf16 out of 131072, 0.41 GB with each row that
+// is asked for read once, 71.7 us (5.7 TB/s; CTAs of 64 to 256 threads and 2 to 8
+// vectors a thread come to the same or more).
 template <typename T, int N>
 __global__ void __launch_bounds__(kEmbedThreads) embed_lookup_kernel(const EmbedArgs a) {
     wait_for_stream();
@@ -72,8 +76,15 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_lookup_kernel(const Embed
     for (int u = 0; u < kEmbedUnroll; ++u) {
 #pragma unroll
         for (int k = 0; k < N; ++k) v[u].v[k] = from_float<T>(0.0f);
-        if (row[u] >= 0)
-            v[u] = *reinterpret_cast<const V*>(static_cast<const T*>(a.table) + row[u] * a.table_stride + piece[u]);
+        if (row[u] >= 0) {
+            const T* from = static_cast<const T*>(a.table) + row[u] * a.table_stride + piece[u];
+            if constexpr (sizeof(V) == 16) {  // volatile, so that all are on their way together (75.8 us otherwise)
+                const uint4 bits = load_once(reinterpret_cast<const uint4*>(from));
+                v[u] = *reinterpret_cast<const V*>(&bits);
+            } else {
+                v[u] = *reinterpret_cast<const V*>(from);
+            }
+        }
     }
 #pragma unroll
     for (int u = 0; u < kEmbedUnroll; ++u) {
@@ -119,13 +130,18 @@ constexpr int kEmbedLongPiece = 128;
 // As in the grouping of slots by id: a place is the sum of the places of lower
 // digits, those of its own in the chunks of the CTAs before, in the parts of the
 // warps before, and before it in its warp's part.  Counts go through the cluster's
-// shared memory.
-
+// shared memory.  A chunk is put in order in shared memory and leaves it in runs of
+// equal digits.
+//
+// Bound by the 16 SMs that a cluster has: 65537 tokens, two digits of 9 bits, 25.9 us,
+// of which ranking takes 10.5 (nine votes for 32 tokens), counting 2.6, the cluster's
+// meetings and sums 6.  (Stores straight from the lanes, a line each: 27.1.)
 constexpr int kEmbedCluster = 16;
 constexpr int kEmbedSortThreads = 1024;
 constexpr int kEmbedSortWarps = kEmbedSortThreads / 32;
 constexpr int kEmbedDigits = 512;
-constexpr size_t kEmbedSortSmem = (size_t)(kEmbedSortWarps + 2) * kEmbedDigits * 4;
+// Shared memory for a CTA's chunk of the tokens: the counts, and the chunk in order.
+inline size_t embed_sort_smem(int64_t chunk) { return (size_t)(kEmbedSortWarps + 3) * kEmbedDigits * 4 + (size_t)chunk * 8; }
 
 struct EmbedDigits {
     const EmbedBackArgs& a;
@@ -147,9 +163,10 @@ struct EmbedDigits {
 __global__ void __launch_bounds__(kEmbedSortThreads) embed_sort_kernel(const EmbedBackArgs a) {
     wait_for_stream();
     extern __shared__ int s_next[];  // [warps][digits]: a warp's counts, then its next place less the CTA's first
-    __shared__ int s_part[kEmbedSortWarps];
+    __shared__ int2 s_part[kEmbedSortWarps];
     int* s_count = s_next + kEmbedSortWarps * kEmbedDigits;
-    int* s_first = s_count + kEmbedDigits;
+    int* s_first = s_count + kEmbedDigits;  // a digit's first place, less its first in the chunk
+    int* s_local = s_first + kEmbedDigits;  // and that
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t ctas = cluster_size(), rank = cluster_rank();
     const int64_t chunk = (a.n + ctas - 1) / ctas;
@@ -157,6 +174,8 @@ __global__ void __launch_bounds__(kEmbedSortThreads) embed_sort_kernel(const Emb
     const int64_t part = ((hi - lo + kEmbedSortWarps - 1) / kEmbedSortWarps + 31) / 32 * 32;
     const int64_t wlo = min(lo + warp * part, hi), whi = min(wlo + part, hi);
     int* next = s_next + warp * kEmbedDigits;
+    uint32_t* s_key = reinterpret_cast<uint32_t*>(s_local + kEmbedDigits);
+    uint32_t* s_slot = s_key + chunk;
     constexpr int U = 4;
     for (int pass = 0; pass < a.passes; ++pass) {
         // the last pass ends in keys and slots
@@ -165,7 +184,7 @@ __global__ void __launch_bounds__(kEmbedSortThreads) embed_sort_kernel(const Emb
                                pass == 0 ? nullptr : even ? a.other_slots : a.slots, pass * a.bits};
         uint32_t* to_keys = even ? a.keys : a.other_keys;
         uint32_t* to_slots = even ? a.slots : a.other_slots;
-        for (int d = lane; d < kEmbedDigits; d += 32) next[d] = 0;
+        for (int d = lane; d < kEmbedDigits / 4; d += 32) reinterpret_cast<int4*>(next)[d] = make_int4(0, 0, 0, 0);
         __syncwarp();
         for (int64_t i0 = wlo + lane; i0 < whi; i0 += 32 * U) {
             uint32_t key[U];
@@ -188,27 +207,30 @@ __global__ void __launch_bounds__(kEmbedSortThreads) embed_sort_kernel(const Emb
         }
         if (ctas > 1) cluster_sync();
         else __syncthreads();
-        int total = 0, before = 0, run = 0;
+        // a digit's total, what lies before this CTA's, and the sums of both over lower digits
+        int total = 0, before = 0, mine = 0, run = 0, local = 0;
         if (threadIdx.x < kEmbedDigits) {
-#pragma unroll 4
-            for (uint32_t r = 0; r < ctas; ++r) {
-                const int c = peer_word(s_count + threadIdx.x, r);
-                total += c;
-                before += r < rank ? c : 0;
-            }
-            run = total;
+            mine = s_count[threadIdx.x];
+            int count[kEmbedCluster];
+#pragma unroll
+            for (uint32_t r = 0; r < kEmbedCluster; ++r) count[r] = r < ctas ? peer_word(s_count + threadIdx.x, r) : 0;
+#pragma unroll
+            for (uint32_t r = 0; r < kEmbedCluster; ++r) total += count[r], before += r < rank ? count[r] : 0;
+            run = total, local = mine;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const int up = __shfl_up_sync(0xffffffffu, run, d);
-                if (lane >= d) run += up;
+                const int up = __shfl_up_sync(0xffffffffu, run, d), up_local = __shfl_up_sync(0xffffffffu, local, d);
+                if (lane >= d) run += up, local += up_local;
             }
-            if (lane == 31) s_part[warp] = run;
+            if (lane == 31) s_part[warp] = make_int2(run, local);
         }
         __syncthreads();
         if (threadIdx.x < kEmbedDigits) {
-            int lower = 0;
-            for (int w = 0; w < warp; ++w) lower += s_part[w];
-            s_first[threadIdx.x] = lower + run - total + before;
+            const int2 sums = lane < warp ? s_part[lane] : make_int2(0, 0);  // 16 warps at most
+            const int lower = __reduce_add_sync(0xffffffffu, sums.x) + run - total;
+            const int lower_local = __reduce_add_sync(0xffffffffu, sums.y) + local - mine;
+            s_local[threadIdx.x] = lower_local;
+            s_first[threadIdx.x] = lower + before - lower_local;
         }
         __syncthreads();
         const unsigned before_me = (1u << lane) - 1;
@@ -236,11 +258,15 @@ __global__ void __launch_bounds__(kEmbedSortThreads) embed_sort_kernel(const Emb
                 __syncwarp();
                 if (live && place == 0) next[g] = at + __popc(same);
                 __syncwarp();
-                if (live) {
-                    __stcg(to_keys + s_first[g] + at, key[u]);
-                    __stcg(to_slots + s_first[g] + at, slot[u]);
-                }
+                if (live) s_key[s_local[g] + at] = key[u], s_slot[s_local[g] + at] = slot[u];
             }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < (int)(hi - lo); i += kEmbedSortThreads) {
+            const uint32_t key = s_key[i];
+            const int to = s_first[from.digit(key)] + i;
+            __stcg(to_keys + to, key);
+            __stcg(to_slots + to, s_slot[i]);
         }
         __threadfence();
         if (ctas > 1) cluster_sync();  // what this pass wrote the next one reads; no CTA leaves, or counts anew, before
