@@ -118,7 +118,7 @@ static cudaError_t launch_backward(EmbedBackArgs a, int sm_count, cudaStream_t s
                  : values == 2    ? embed_sum_kernel<T, O, 2>
                                   : embed_sum_kernel<T, O, 1>;
     e = counted([&] { launch_early(kern, (unsigned)ctas, kEmbedSumThreads, 0, st, a); });
-    const int64_t joins = (a.n - 1) / a.piece;  // multiples of it in (0, n)
+    const int64_t joins = (a.n - 1) >> a.piece_bits;  // multiples of a piece's length in (0, n)
     if (e == cudaSuccess && joins > 0) {
         const int tiles = (a.width + kEmbedJoinColumns - 1) / kEmbedJoinColumns;
         const int64_t groups = (joins + kEmbedJoinPlaces - 1) / kEmbedJoinPlaces;
@@ -188,8 +188,8 @@ om_status om_embed_lookup_backward(int value_type, const void* grad, int64_t n, 
     cudaStream_t st = (cudaStream_t)stream;
     unsigned char* scratch = nullptr;
     const size_t list = ((size_t)n * 4 + 255) & ~(size_t)255;
-    a.piece = n <= kEmbedFewTokens ? kEmbedPiece : kEmbedLongPiece;
-    const size_t sums = n > a.piece ? (size_t)(2 * ((n - 1) / a.piece + 1)) * (size_t)width * 4 : 0;
+    a.piece_bits = n <= kEmbedFewTokens ? kEmbedPieceBits : kEmbedLongPieceBits;
+    const size_t sums = n > 1 << a.piece_bits ? (size_t)(2 * (((n - 1) >> a.piece_bits) + 1)) * (size_t)width * 4 : 0;
     if (n > 0) {
         cudaMemPool_t pool = nullptr;
         s = scratch_pool(d, &pool);

@@ -114,16 +114,16 @@ struct EmbedBackArgs {
     int width, wide, accumulate;
     int tiles;            // column tiles of a row
     int window;           // sorted places of a warp
-    int piece;            // tokens of a long run that one warp sums
+    int piece_bits;       // tokens of a long run that one warp sums: 1 << piece_bits
     int passes, bits;     // (sorting) digits of a key and bits of a digit
     int64_t sum_ctas;     // CTAs that sum; those after them write zeros
     int zero_rows;        // rows of a warp of them
     float scale;
 };
 
-// Tokens of a run that one warp sums: of few tokens, and of many.
-constexpr int kEmbedPiece = 32;
-constexpr int kEmbedLongPiece = 128;
+// Tokens of a run that one warp sums (a power of two of them): of few tokens, and of many.
+constexpr int kEmbedPieceBits = 5;
+constexpr int kEmbedLongPieceBits = 7;
 
 // ---- the sort: one cluster, least digit first
 //
@@ -375,11 +375,11 @@ __device__ __forceinline__ int64_t first_place_warp(const uint32_t* keys, int64_
     return lo;
 }
 
-// The slot of a piece's sum in `partial`: pieces start at multiples of a.piece from
+// The slot of a piece's sum in `partial`: pieces start at multiples of their length from
 // their run's start, so at most one piece that goes on a run and one that starts a
-// long run start in the same a.piece places.
+// long run start in the same places between two multiples.
 __device__ __forceinline__ int64_t piece_slot(const EmbedBackArgs& a, int64_t at, bool first) {
-    return 2 * (int64_t)((uint32_t)at / (uint32_t)a.piece) + first;
+    return 2 * (at >> a.piece_bits) + first;
 }
 
 // N sums of a lane to a row of the table's gradient (scaled), or as they are.
@@ -428,7 +428,7 @@ __device__ __forceinline__ void zero_rows(const EmbedBackArgs& a, int64_t warp) 
 }
 
 // A warp looks after the pieces that start in its window of sorted places, for a
-// tile of 32 N columns.  A piece is a run of equal tokens, or up to a.piece
+// tile of 32 N columns.  A piece is a run of equal tokens, or 32 (128)
 // places of a longer one, counted from its start; so those of a window are
 // neighbours, and the warp streams their rows, 16 in flight through shared memory
 // (each lane copies and reads its own vectors: no barrier), adding each to the sum
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kEmbedSumThreads) embed_sum_kernel(const Embed
             int64_t run;
             if (there != 0) run = back + 32 - __clz(there);
             else run = first_place_warp(a.keys, 0, back, key0);
-            if (mine < a.n && key == key0 && !first) starts = (uint32_t)(mine - run) % (uint32_t)a.piece == 0;
+            if (mine < a.n && key == key0 && !first) starts = ((mine - run) & ((1 << a.piece_bits) - 1)) == 0;
         }
         const unsigned start = __ballot_sync(0xffffffffu, starts);
         const unsigned window = base > lo ? 0u : a.window >= 32 ? 0xffffffffu : (1u << a.window) - 1;
@@ -535,8 +535,8 @@ __global__ void __launch_bounds__(kEmbedSumThreads) embed_sum_kernel(const Embed
     }
 }
 
-// Long runs: the pieces' sums in order.  A run of more than a.piece places
-// holds a multiple of a.piece after its start; the first of them is the one
+// Long runs: the pieces' sums in order.  A run longer than a piece
+// holds a multiple of its length after its start; the first of them is the one
 // whose CTA adds them.  A CTA looks at a few multiples, and each of its warps has
 // 128 columns.
 constexpr int kEmbedJoinThreads = 128;
@@ -546,12 +546,12 @@ constexpr int kEmbedJoinPlaces = 4;
 template <typename O>
 __global__ void __launch_bounds__(kEmbedJoinThreads) embed_join_kernel(const EmbedBackArgs a, int tiles) {
     wait_for_stream();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, piece = 1 << a.piece_bits;
     const int64_t group = blockIdx.x / tiles;
     const int column = (int)(blockIdx.x - group * tiles) * kEmbedJoinColumns + (int)(threadIdx.x >> 5) * 128 + lane;
     bool mine = false;
     if (lane < kEmbedJoinPlaces) {
-        const int64_t at = (group * kEmbedJoinPlaces + lane + 1) * a.piece, lo = at - a.piece;
+        const int64_t at = (group * kEmbedJoinPlaces + lane + 1) * piece, lo = at - piece;
         if (at < a.n) {
             const uint32_t key = a.keys[at], last = a.keys[at - 1], low = a.keys[lo];
             const uint32_t lower = lo > 0 ? a.keys[lo - 1] : 0xffffffffu;
@@ -559,13 +559,13 @@ __global__ void __launch_bounds__(kEmbedJoinThreads) embed_join_kernel(const Emb
         }
     }
     for (unsigned todo = __ballot_sync(0xffffffffu, mine); todo != 0; todo &= todo - 1) {
-        const int64_t at = (group * kEmbedJoinPlaces + __ffs(todo)) * a.piece;
+        const int64_t at = (group * kEmbedJoinPlaces + __ffs(todo)) * piece;
         const uint32_t key = a.keys[at];
-        const int64_t start = first_place_warp(a.keys, at - a.piece, at, key);
+        const int64_t start = first_place_warp(a.keys, at - piece, at, key);
         const int64_t end = first_place_warp(a.keys, at, a.n, key + 1);
-        if (end - start <= a.piece) continue;
-        const int64_t pieces = (end - start + a.piece - 1) / a.piece;
-        // piece p starts in the block of a.piece places p blocks after the run's start
+        if (end - start <= piece) continue;
+        const int64_t pieces = (end - start + piece - 1) >> a.piece_bits;
+        // piece p starts in the block of places p blocks after the run's start
         const float* first = a.partial + piece_slot(a, start, true) * a.width;
         const float* others = a.partial + piece_slot(a, start, false) * a.width;
         const int64_t step = 2 * (int64_t)a.width;
