@@ -459,6 +459,12 @@ __host__ __device__ constexpr int beam_ring_offset() { return ((int)sizeof(BeamS
 // row's address), each thread keeping a running maximum and sum of its words.  The
 // first CTA joins the slices: the beams' logarithms of their sums, the scores of
 // the slices' best continuations in 64 bits, and the best of all.
+//
+// 64 sequences of 8 beams over 131071 bf16 logits, 0.13 GB: 38.7 us, of which 20 stream
+// at the memory's rate and the rest are a chain that all CTAs walk at once: first
+// loads (3), a slice's bound and its candidates, read once more (6), the cluster's
+// meeting (2), the joining (2).  One prompt of 4 beams is that chain, about 8 us.
+// (Vectors loaded straight into registers, rows realigned by shifts: 70 us.)
 template <typename T>
 __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const BeamArgs a) {
     wait_for_stream();
@@ -658,7 +664,8 @@ constexpr int kFewBeamArrays = 4;
 // works in place for every map of beams to parents, with no barrier.  A beam
 // that keeps its own place is not touched in place.
 //
-// Bound by memory.
+// Bound by memory: 64 beams' keys and values of 8 heads, 2.5 K entries of 256 bytes each
+// on average, 1.11 GB, 165 us (6.7 TB/s, the copy rate).
 // BEAMS: beams loaded together (all of them in place).  STAGED: in place with
 // more than that many, through shared memory.
 template <typename V, int BEAMS, bool STAGED>

@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(kEmbedSortThreads) embed_sort_kernel(const Emb
 // The same for few tokens, by all SMs and without a pass over digits: the place of
 // a token is the number of smaller ones and of equal ones before it.  A CTA counts
 // for 32 tokens, a lane each; its warps share out what they are compared with, which
-// lies in shared memory.
+// lies in shared memory.  4096 tokens: 5.5 us; by a cluster's digits 12, and with one
+// CTA's in shared memory 10.
 constexpr int64_t kEmbedSmallMost = 8192;
 constexpr int kEmbedSmallThreads = 512;
 
@@ -437,7 +438,9 @@ __device__ __forceinline__ void zero_rows(const EmbedBackArgs& a, int64_t warp) 
 //
 // Zeros: a warp searches the sorted tokens for its rows.
 //
-// Bound by memory.
+// Bound by memory: 65537 tokens into 131072 rows of 2048, bf16 to f32, 1.34 GB, 188 us
+// (7.1 TB/s).  (Rows in registers, eight at a time, took 128 us for the sums alone,
+// which take 83 so; the zeros apart from them, beside the sort, as much in all.)
 template <typename T, typename O, int N>
 __global__ void __launch_bounds__(kEmbedSumThreads) embed_sum_kernel(const EmbedBackArgs a) {
     wait_for_stream();
@@ -538,7 +541,8 @@ __global__ void __launch_bounds__(kEmbedSumThreads) embed_sum_kernel(const Embed
 // Long runs: the pieces' sums in order.  A run longer than a piece
 // holds a multiple of its length after its start; the first of them is the one
 // whose CTA adds them.  A CTA looks at a few multiples, and each of its warps has
-// 128 columns.
+// 128 columns.  13 us for the 65537 tokens above, of a run of 3000 and many shorter
+// ones: a chain of loads, most of them from memory.
 constexpr int kEmbedJoinThreads = 128;
 constexpr int kEmbedJoinColumns = 4 * kEmbedJoinThreads;  // four to a lane
 constexpr int kEmbedJoinPlaces = 4;
