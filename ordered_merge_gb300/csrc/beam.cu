@@ -29,7 +29,8 @@ static om_status prepare_beam(const DeviceState* d) {
         for (auto* kern : {beam_select_kernel<float>, beam_select_kernel<__nv_bfloat16>, beam_select_kernel<__half>})
             ok = ok &&
                  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      (int)beam_smem(kBeamMaxStages, kMaxBeams, kMaxBeamTop)) == cudaSuccess;
+                                      (int)beam_smem(kBeamMaxStages, kMaxBeams, kMaxBeamTop)) == cudaSuccess &&
+                 cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
         for (const void* kern : {(const void*)beam_gather_kernel<kBeamsInRegisters, true, kFewBeamArrays>,
                                  (const void*)beam_gather_kernel<kBeamsInRegisters, true, kMaxBeamArrays>})
             ok = ok && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -45,11 +46,14 @@ static om_status prepare_beam(const DeviceState* d) {
 
 template <typename T>
 static cudaError_t launch_beam(BeamArgs a, int64_t batch, int sm_count, cudaStream_t st) {
-    // CTAs of a cluster: as many as fill the SMs (two each), while slices stay long enough.
-    // (16 rows of 5 x 50021: clusters of 16 took 1.6 us longer than 8.)
+    // CTAs of a cluster: as many as fill the SMs (two each), while slices stay long enough;
+    // 16 only for few sequences with much to read.  (8 and 16: 1 x 4 x 131071 bf16 16.6
+    // and 14.5 us, 1 x 16 53.9 and 39.1, 4 x 8 22.9 and 20.9, but 1 x 4 x 32768 10.4 and
+    // 11.4, 8 x 8 x 131071 23.3 and 26.4, 16 x 8 x 50021 18.6 and 25.9.)
     const int64_t most = a.beams * std::max<int64_t>(1, a.vocab / kBeamLeastSlice);
+    const bool wide = batch <= 4 && (int64_t)a.beams * a.vocab > kBeamCluster * (int64_t)32768;
     int ctas = 1;
-    while (ctas < kBeamCluster && batch * ctas < 2 * (int64_t)sm_count && ctas < most) ctas *= 2;
+    while (ctas < (wide ? 2 * kBeamCluster : kBeamCluster) && batch * ctas < 2 * (int64_t)sm_count && ctas < most) ctas *= 2;
     a.parts = std::max(1, ctas / a.beams);
     a.slice = (int)((((int64_t)a.vocab + a.parts - 1) / a.parts + 7) / 8 * 8);
     cudaLaunchConfig_t cfg = {};

@@ -112,7 +112,7 @@ struct BeamShared {
     float warp_sum[kBeamWarps];
     float most;       // of the slice
     int slow;         // its sum is to be made again
-    float bound;
+    uint32_t bound;   // image of a lower bound of the slice's top-th greatest
     int found;        // logits that reach the bound
     int count;        // (settling) those counted
     int ties[kBeamWarps];
@@ -198,56 +198,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
     uint64_t p;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(x), "l"(y), "l"(z));
     return p;
-}
-
-// The candidates of a slice of which too many reach the bound.  Most often these are
-// ties with the bound itself (rows of one value; of few values and the type's lowest
-// for what is masked): then fewer than `top` are greater, and the first of the ties
-// fill up.  All threads; returns how many keys there are.
-template <typename T>
-__device__ __noinline__ int crowded_slice(const BeamSlice<T>& slice, int top, BeamShared& s) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float bound = s.bound;
-    if (threadIdx.x == 0) s.found = 0;
-    __syncthreads();
-#pragma unroll 4
-    for (int i = threadIdx.x; i < slice.n; i += kBeamThreads) {
-        const float x = slice.at(i);
-        if (x > bound) {
-            const int at = atomicAdd(&s.found, 1);
-            if (at < kBeamCandidates) s.key[at] = beam_key(x, slice.first + i);
-        }
-    }
-    __syncthreads();
-    int have = s.found;
-    if (have < top) {
-        for (int i0 = 0; i0 < slice.n && have < top; i0 += kBeamThreads) {
-            const int i = i0 + (int)threadIdx.x;
-            const unsigned ties = __ballot_sync(0xffffffffu, i < slice.n && slice.at(i) == bound);
-            if (lane == 0) s.ties[warp] = __popc(ties);
-            __syncthreads();
-            int before = have, all = 0;
-            for (int w = 0; w < kBeamWarps; ++w) before += w < warp ? s.ties[w] : 0, all += s.ties[w];
-            before += __popc(ties & ((1u << lane) - 1));
-            if ((ties >> lane & 1) && before < top) s.key[before] = beam_key(bound, slice.first + i);
-            have = min(have + all, top);
-            __syncthreads();
-        }
-        return have;
-    }
-    const uint64_t edge = settle_edge(slice, top, s);
-    if (threadIdx.x == 0) s.found = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < slice.n; i += kBeamThreads) {
-        const float x = slice.at(i);
-        const uint64_t key = beam_key(x, slice.first + i);
-        if (x > -INFINITY && (key & WordOf<T>::kKeyBits) >= edge) {
-            const int at = atomicAdd(&s.found, 1);  // `top` of them: keys differ
-            if (at < kBeamCandidates) s.key[at] = key;
-        }
-    }
-    __syncthreads();
-    return min(s.found, kBeamCandidates);
 }
 
 // What a thread keeps of the words it has seen, 8 at a time ("eights"): the greatest
@@ -337,29 +287,116 @@ __device__ __forceinline__ void beam_chunk(const unsigned char* stage, uint32_t 
     }
 }
 
+// 16 words, `step` apart within an eight (the second eight past the end where there is
+// none): loaded together, then the few that reach the bound (exceed it: STRICT) one by one.
+template <typename T, bool STRICT>
+__device__ __forceinline__ void look_at(const BeamSlice<T>& slice, float bound, BeamShared& s, int first, int second, int step) {
+    auto reaches = [&](float x) { return STRICT ? x > bound : x >= bound && x > -INFINITY; };
+    unsigned near = 0;
+    uint32_t w[2 * kBeamGroup];
+#pragma unroll
+    for (int i = 0; i < 2 * kBeamGroup; ++i) w[i] = slice.word((i < kBeamGroup ? first : second) + i % kBeamGroup * step);
+#pragma unroll
+    for (int i = 0; i < 2 * kBeamGroup; ++i) {
+        const float2 x = word_values(w[i], T{});
+        near |= (reaches(x.x) ? 1u << 2 * i : 0u) | (reaches(x.y) ? 2u << 2 * i : 0u);
+    }
+    for (; near != 0; near &= near - 1) {
+        const int bit = __ffs(near) - 1, i = bit >> 1;
+        const int word = (i < kBeamGroup ? first : second) + i % kBeamGroup * step;
+        const float2 x = word_values(slice.word(word), T{});
+        const int at = atomicAdd(&s.found, 1);
+        if (at < kBeamCandidates) s.key[at] = beam_key(bit & 1 ? x.y : x.x, slice.first + word * WordOf<T>::kPer + (bit & 1));
+    }
+}
+
+// Threads whose maximum reaches the bound read the one or two eights again that hold
+// what does; for one with more, its warp reads all of its words.  A warp with many
+// such threads leaves the slice to crowded_slice.
+constexpr int kBeamCrowd = 8;
+
+template <typename T, bool STRICT>
+__device__ __forceinline__ void look_again(const BeamSlice<T>& slice, const BeamRunning& run, float bound, BeamShared& s) {
+    auto reaches = [&](float x) { return STRICT ? x > bound : x >= bound && x > -INFINITY; };
+    const int lane = threadIdx.x & 31, words = slice.words();
+    unsigned todo = __ballot_sync(0xffffffffu, reaches(run.third));
+    if (__popc(todo) > kBeamCrowd) {
+        if (lane == 0) atomicAdd(&s.found, kBeamCandidates + 1);
+        return;
+    }
+    if (!(todo >> lane & 1) && reaches(run.most))
+        look_at<T, STRICT>(slice, bound, s, run.where * kBeamGroup * kBeamThreads + (int)threadIdx.x,
+                           reaches(run.second) ? run.next * kBeamGroup * kBeamThreads + (int)threadIdx.x : words, kBeamThreads);
+    for (; todo != 0; todo &= todo - 1)
+        for (int w = ((int)threadIdx.x & ~31) + __ffs(todo) - 1 + lane * kBeamThreads; w < words; w += 64 * kBeamGroup * kBeamThreads)
+            look_at<T, STRICT>(slice, bound, s, w, w + 32 * kBeamGroup * kBeamThreads, 32 * kBeamThreads);
+}
+
+// The candidates of a slice of which too many reach the bound.  Most often these are
+// ties with the bound itself (rows of one value; of few values and a low one for what
+// is masked): then fewer than `top` exceed it, and the first of the ties, in order,
+// fill up.  All threads; returns how many keys there are.
+template <typename T>
+__device__ __noinline__ int crowded_slice(const BeamSlice<T>& slice, const BeamRunning& run, float bound, int top, BeamShared& s) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __syncthreads();  // all have read s.found
+    if (threadIdx.x == 0) s.found = 0;
+    __syncthreads();
+    look_again<T, true>(slice, run, bound, s);
+    __syncthreads();
+    int have = s.found;
+    if (have >= top && have <= kBeamCandidates) return have;
+    if (have < top) {
+        for (int i0 = 0; i0 < slice.n && have < top && bound > -INFINITY; i0 += kBeamThreads) {
+            const int i = i0 + (int)threadIdx.x;
+            const unsigned ties = __ballot_sync(0xffffffffu, i < slice.n && slice.at(i) == bound);
+            if (lane == 0) s.ties[warp] = __popc(ties);
+            __syncthreads();
+            int before = have, all = 0;
+            for (int w = 0; w < kBeamWarps; ++w) before += w < warp ? s.ties[w] : 0, all += s.ties[w];
+            before += __popc(ties & ((1u << lane) - 1));
+            if ((ties >> lane & 1) && before < top) s.key[before] = beam_key(bound, slice.first + i);
+            have = min(have + all, top);
+            __syncthreads();
+        }
+        return have;
+    }
+    const uint64_t edge = settle_edge(slice, top, s);
+    if (threadIdx.x == 0) s.found = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < slice.n; i += kBeamThreads) {
+        const float x = slice.at(i);
+        const uint64_t key = beam_key(x, slice.first + i);
+        if (x > -INFINITY && (key & WordOf<T>::kKeyBits) >= edge) {
+            const int at = atomicAdd(&s.found, 1);  // `top` of them: keys differ
+            if (at < kBeamCandidates) s.key[at] = key;
+        }
+    }
+    __syncthreads();
+    return min(s.found, kBeamCandidates);
+}
+
 // The end of a slice: its maximum, its sum of exponentials and its `top` greatest
 // logits in order, into place `unit` of the first CTA.  All threads.
 //
 // Of the maxima of 128 pairs of threads the top-th greatest is a lower bound of the
 // slice's top-th greatest logit, and only threads whose own maximum reaches it hold
-// any that do: few more than `top`.  They read the one or two eights again that hold
-// them; for one with more, its warp reads all of its words.  What reaches the bound
-// is put in order by counting.
+// any that do: few more than `top`.  They look again, and what reaches the bound is
+// put in order by counting.
 template <typename T>
 __device__ __forceinline__ void beam_slice_end(const BeamArgs& a, const BeamSlice<T>& slice, int unit, const BeamRunning& run,
                                                uint64_t* lists, BeamShared& s) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float m = run.most;
-    // a group's maximum, its last bits given up for the group's number: all differ, and a
-    // bound may be a little low
-    const uint32_t group_key = (score_image(fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1))) & ~(uint32_t)(kBeamGroups - 1)) |
-                               (threadIdx.x >> 1);
+    // groups are ranked by their maxima, the last bits given up for the group's number: all differ
+    const float group_max = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const uint32_t group_key = (score_image(group_max) & ~(uint32_t)(kBeamGroups - 1)) | (threadIdx.x >> 1);
     if ((threadIdx.x & 1) == 0) s.group_key[threadIdx.x >> 1] = group_key;
     // NaN stays NaN in these, to be seen at the end
     const float most = warp_max(m), scale = warp_max(run.scale);
     const float all = warp_sum(run.total() * exp2_fast(run.scale - scale));
     if (lane == 0) s.warp_max[warp] = most, s.warp_scale[warp] = scale, s.warp_sum[warp] = all;
-    if (threadIdx.x == 0) s.found = 0;
+    if (threadIdx.x == 0) s.found = 0, s.bound = 0xffffffffu;
     __syncthreads();
     {  // two threads a group, each comparing with half of the groups
         int rank = 0;
@@ -370,8 +407,9 @@ __device__ __forceinline__ void beam_slice_end(const BeamArgs& a, const BeamSlic
             rank += (o.x > group_key) + (o.y > group_key) + (o.z > group_key) + (o.w > group_key);
         }
         rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-        // (a logit is at least -inf, whose image the cut does not take below the others')
-        if (rank == a.top - 1) s.bound = image_score(max(group_key & ~(uint32_t)(kBeamGroups - 1), score_image(-INFINITY)));
+        // the least maximum of those groups: a logit of the slice
+        const uint32_t least = __reduce_min_sync(0xffffffffu, rank < a.top ? score_image(group_max) : 0xffffffffu);
+        if (lane == 0) atomicMin(&s.bound, least);
     }
     if (warp == kBeamWarps - 1) {
         const float wm = warp_max(lane < kBeamWarps ? s.warp_max[lane] : -INFINITY);
@@ -389,36 +427,8 @@ __device__ __forceinline__ void beam_slice_end(const BeamArgs& a, const BeamSlic
         }
     }
     __syncthreads();
-    const float bound = s.bound;
-    const int words = slice.words();
-    // 16 words, `step` apart within an eight (the second eight past the end where there is none):
-    // loaded together, then the few that reach the bound one by one
-    auto look = [&](int first, int second, int step) {
-        unsigned near = 0;
-        uint32_t w[2 * kBeamGroup];
-#pragma unroll
-        for (int i = 0; i < 2 * kBeamGroup; ++i) w[i] = slice.word((i < kBeamGroup ? first : second) + i % kBeamGroup * step);
-#pragma unroll
-        for (int i = 0; i < 2 * kBeamGroup; ++i) {
-            const float2 x = word_values(w[i], T{});
-            near |= (x.x >= bound && x.x > -INFINITY ? 1u << 2 * i : 0u) | (x.y >= bound && x.y > -INFINITY ? 2u << 2 * i : 0u);
-        }
-        for (; near != 0; near &= near - 1) {
-            const int bit = __ffs(near) - 1, i = bit >> 1;
-            const int word = (i < kBeamGroup ? first : second) + i % kBeamGroup * step;
-            const float2 x = word_values(slice.word(word), T{});
-            const int at = atomicAdd(&s.found, 1);
-            if (at < kBeamCandidates) s.key[at] = beam_key(bit & 1 ? x.y : x.x, slice.first + word * WordOf<T>::kPer + (bit & 1));
-        }
-    };
-    const bool thrice = run.third >= bound && run.third > -INFINITY;
-    if (!thrice && m >= bound && m > -INFINITY)
-        look(run.where * kBeamGroup * kBeamThreads + (int)threadIdx.x,
-             run.second >= bound && run.second > -INFINITY ? run.next * kBeamGroup * kBeamThreads + (int)threadIdx.x : words,
-             kBeamThreads);
-    for (unsigned todo = __ballot_sync(0xffffffffu, thrice); todo != 0; todo &= todo - 1)
-        for (int w = warp * 32 + __ffs(todo) - 1 + lane * kBeamThreads; w < words; w += 64 * kBeamGroup * kBeamThreads)
-            look(w, w + 32 * kBeamGroup * kBeamThreads, 32 * kBeamThreads);
+    const float bound = image_score(s.bound);
+    look_again<T, false>(slice, run, bound, s);
     __syncthreads();
     if (s.slow) {
         float sum = 0.0f;
@@ -437,7 +447,7 @@ __device__ __forceinline__ void beam_slice_end(const BeamArgs& a, const BeamSlic
         }
     }
     int found = s.found;
-    if (found > kBeamCandidates) found = crowded_slice(slice, a.top, s);
+    if (found > kBeamCandidates) found = crowded_slice(slice, run, bound, a.top, s);
     uint64_t* list = lists + unit * a.top;
     for (int c = threadIdx.x; c < found; c += kBeamThreads) {
         const uint64_t mine = s.key[c];

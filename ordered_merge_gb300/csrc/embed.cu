@@ -57,13 +57,6 @@ static om_status prepare_embed(const DeviceState* d) {
     return OM_OK;
 }
 
-// CTAs of a cluster that goes over n tokens: a CTA for 1024, up to 16.
-static unsigned cluster_for(int64_t n) {
-    unsigned ctas = 1;
-    while (ctas < kEmbedCluster && ctas * 1024 < n) ctas *= 2;
-    return ctas;
-}
-
 template <typename T, typename O>
 static cudaError_t launch_backward(EmbedBackArgs a, int sm_count, cudaStream_t st) {
     constexpr int kMostT = 16 / (int)sizeof(T), kMostO = 16 / (int)sizeof(O);
@@ -81,13 +74,13 @@ static cudaError_t launch_backward(EmbedBackArgs a, int sm_count, cudaStream_t s
             e = counted([&] { launch_early(embed_sort_small_kernel, blocks, kEmbedSmallThreads, smem, st, a); });
         } else {
             cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(cluster_for(a.n));
+            cfg.gridDim = dim3(kEmbedCluster);
             cfg.blockDim = dim3(kEmbedSortThreads);
-            cfg.dynamicSmemBytes = embed_sort_smem((a.n + cfg.gridDim.x - 1) / cfg.gridDim.x);
+            cfg.dynamicSmemBytes = embed_sort_smem((a.n + kEmbedCluster - 1) / kEmbedCluster);
             cfg.stream = st;
             cudaLaunchAttribute attr[2] = {early_attribute()};
             attr[1].id = cudaLaunchAttributeClusterDimension;
-            attr[1].val.clusterDim.x = cfg.gridDim.x;
+            attr[1].val.clusterDim.x = kEmbedCluster;
             attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
             cfg.attrs = attr;
             cfg.numAttrs = 2;

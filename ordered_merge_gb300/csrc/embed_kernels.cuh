@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kEmbedSortThreads) embed_sort_kernel(const Emb
     int* s_first = s_count + kEmbedDigits;  // a digit's first place, less its first in the chunk
     int* s_local = s_first + kEmbedDigits;  // and that
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t ctas = cluster_size(), rank = cluster_rank();
-    const int64_t chunk = (a.n + ctas - 1) / ctas;
+    const uint32_t rank = cluster_rank();
+    const int64_t chunk = (a.n + kEmbedCluster - 1) / kEmbedCluster;
     const int64_t lo = min((int64_t)rank * chunk, a.n), hi = min(lo + chunk, a.n);
     const int64_t part = ((hi - lo + kEmbedSortWarps - 1) / kEmbedSortWarps + 31) / 32 * 32;
     const int64_t wlo = min(lo + warp * part, hi), whi = min(wlo + part, hi);
@@ -205,15 +205,14 @@ __global__ void __launch_bounds__(kEmbedSortThreads) embed_sort_kernel(const Emb
             }
             s_count[threadIdx.x] = run;
         }
-        if (ctas > 1) cluster_sync();
-        else __syncthreads();
+        cluster_sync();
         // a digit's total, what lies before this CTA's, and the sums of both over lower digits
         int total = 0, before = 0, mine = 0, run = 0, local = 0;
         if (threadIdx.x < kEmbedDigits) {
             mine = s_count[threadIdx.x];
             int count[kEmbedCluster];
 #pragma unroll
-            for (uint32_t r = 0; r < kEmbedCluster; ++r) count[r] = r < ctas ? peer_word(s_count + threadIdx.x, r) : 0;
+            for (uint32_t r = 0; r < kEmbedCluster; ++r) count[r] = peer_word(s_count + threadIdx.x, r);
 #pragma unroll
             for (uint32_t r = 0; r < kEmbedCluster; ++r) total += count[r], before += r < rank ? count[r] : 0;
             run = total, local = mine;
@@ -269,8 +268,7 @@ __global__ void __launch_bounds__(kEmbedSortThreads) embed_sort_kernel(const Emb
             __stcg(to_slots + to, s_slot[i]);
         }
         __threadfence();
-        if (ctas > 1) cluster_sync();  // what this pass wrote the next one reads; no CTA leaves, or counts anew, before
-        else __syncthreads();
+        cluster_sync();  // what this pass wrote the next one reads; no CTA leaves, or counts anew, before
     }
 }
 

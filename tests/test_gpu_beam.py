@@ -36,6 +36,15 @@ def test_select_shapes(gpu, batch, beams, top):
     _check(gpu, logits, top, scores)
 
 
+@pytest.mark.parametrize("batch,beams,vocab,top", [(1, 16, 131071, 32), (1, 3, 131072, 6), (4, 8, 70001, 16), (5, 8, 70001, 16),
+                                                   (2, 5, 60000, 10), (1, 64, 20011, 64), (1, 1, 400003, 5)])
+def test_select_few_sequences(gpu, batch, beams, vocab, top):
+    """Shapes on both sides of the rule for wide clusters."""
+    for dtype in (torch.float32, torch.bfloat16):
+        logits, scores = _logits(batch, beams, vocab, dtype)
+        _check(gpu, logits, top, scores)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_select_no_scores_is_greedy_choice(gpu, dtype):
     logits, _ = _logits(9, 1, 32001, dtype)
@@ -76,12 +85,12 @@ def test_constant_and_nearly_constant_rows(gpu, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("low", ["lowest", 0.0])
+@pytest.mark.parametrize("low", ["lowest", 0.0, -1e9])
 def test_few_logits_above_many_equal_ones(gpu, dtype, low):
     """A grammar's few tokens, all others at one value: the first of these fill up, wherever they are."""
     low = torch.finfo(dtype).min if low == "lowest" else low
     for vocab, top in ((2000, 8), (70001, 20), (131071, 64)):
-        logits = torch.full((3, 2, vocab), low, dtype=dtype, device="cuda")
+        logits = torch.full((3, 2, vocab), low, device="cuda").to(dtype)  # (-1e9 is -inf in 16 bits with 5 of exponent)
         for b in range(3):
             at = torch.randperm(vocab, generator=torch.Generator(device="cuda").manual_seed(b), device="cuda")[:5 * b + 1]
             logits[b, :, at] = torch.arange(5.0 * b + 1, device="cuda").to(dtype) + 1
