@@ -603,12 +603,11 @@ typedef enum {
  * and weights hold tokens * picks values, dense.
  * Sums run in 32 bits; h goes to the second product as the sum of two values of
  * value_type; out is rounded once.  An h beyond f16's range is infinite there.
- * Only the weights of experts that are asked for are read, each once where no
- * more than 8 tokens (16 or 32, where experts have more than 4 or 8 on average)
- * ask for it.  The
- * same call repeats bit for bit.  Takes stream-ordered scratch from the library's
- * pool: 4 * tokens * picks * (inner + hidden) bytes.  One cooperative launch, of a
- * CTA on every SM.  out shares no byte with the inputs.
+ * Only the weights of experts that are asked for are read, once for every 8 tokens
+ * that ask for them.  The same call repeats bit for bit.  Takes stream-ordered
+ * scratch from the library's pool: 4 * tokens * picks * (inner + hidden) bytes.
+ * One cooperative launch, of two CTAs on every SM.  out shares no byte with the
+ * inputs.
  * At most 64 tokens, 32 picks, 1024 experts, hidden and inner 2^20, strides
  * 2^40, else OM_ERANGE.  Whole 16-byte vectors where hidden, inner, strides and
  * addresses allow them; single values (several times slower) otherwise.

@@ -314,11 +314,15 @@ __global__ void __launch_bounds__(kExpertWarps * 32) expert_down_kernel(const Ex
 // block at once, and the next block's before the sums of this one are put together
 // in shared memory: 64 KB a CTA are on their way most of the time.
 // Bound by memory where many experts are read: 64 tokens through 8 of 128 gated
-// experts of 2048 x 1024, 1.59 GB, 260 us (6.1 TB/s, 90 % of the copy rate).  (Rings in
+// experts of 2048 x 1024, 1.59 GB, 257 us (6.2 TB/s, 91 % of the copy rate).  (Rings in
 // shared memory were slower: filled by bulk copies of 512-byte pieces of rows, 90
 // cycles apiece, 984 us, by 16-byte copies of producer warps 327.)  One token, 0.1 GB,
 // 28.7 us: 10 and 5 of them at the copy rate, the rest the launch and first loads (5),
 // the barriers (2.5), uneven shares of 512 items among 304 CTAs (3) and the last sums.
+//
+// An expert with more than 8 tokens takes its weights again, from the L2 cache: 64
+// tokens of 4 of 16 experts 76.7 us (16 tokens at a time 81.7, 32 at a time 95), of 8
+// of 64 experts 173 (180, 283).
 //
 // First all items of the up (and gate) products, then, after a barrier of the
 // grid, those of the down products, whose first weights are asked for inside the
@@ -328,6 +332,8 @@ __global__ void __launch_bounds__(kExpertWarps * 32) expert_down_kernel(const Ex
 constexpr int kLayerSteps = 4;                                     // of a warp in a block
 constexpr int kLayerColumns = 32 * kExpertWarps * kLayerSteps;     // of a block
 constexpr int kLayerThreads = kExpertWarps * 32;
+constexpr int kLayerCtas = 2;     // of an SM: they need their 128 registers a thread
+constexpr int kLayerTokens = 8;   // taken at once
 
 struct LayerShared {
     uint16_t order[kExpertMaxTokens * kExpertMaxPicks];  // the slots, by expert
@@ -366,17 +372,16 @@ struct LayerProduct {
 };
 
 // A warp's way through the blocks of a product.
-template <typename T, int NT, int TILES, typename P>
+template <typename T, int TILES, typename P>
 struct LayerWork {
-    static constexpr int COLS = 8 * NT, S = kLayerSteps;
-    static constexpr bool kAhead = NT == 1;  // the tokens' rows are loaded with the weights (with more there is no room)
+    static constexpr int S = kLayerSteps;
     const P& p;
     const LayerShared& s;
     const int tiles, items, columns;
     int item, tile, expert, q, end, c;  // the block: first slot in order, those of its expert, first column
     const T* rows[TILES];               // this lane's, in the tiles, at its columns of the first step
-    const T* tokens[NT];
-    uint4 w[S][TILES][2], x[kAhead ? S : 1][NT][P::kSets];
+    const T* token;                     // and of its token, if there is one
+    uint4 w[S][TILES][2], x[S][P::kSets];
 
     __device__ __forceinline__ LayerWork(const P& product, const LayerShared& shared)
         : p(product), s(shared), tiles((product.result() + P::kRows - 1) / P::kRows), items(shared.experts * tiles),
@@ -387,7 +392,7 @@ struct LayerWork {
     __device__ __forceinline__ int lane_column() const { return 32 * (int)(threadIdx.x >> 5) + 8 * (int)(threadIdx.x & 3); }
     __device__ __forceinline__ bool here() const { return item < items; }
     __device__ __forceinline__ bool last_columns() const { return c + kLayerColumns >= columns; }
-    __device__ __forceinline__ int count() const { return min(COLS, end - q); }
+    __device__ __forceinline__ int count() const { return min(kLayerTokens, end - q); }
     __device__ __forceinline__ void start_item() {
         const int k = item / tiles;
         tile = item - k * tiles, expert = s.expert[k], q = s.start[k], end = s.start[k + 1], c = 0;
@@ -401,16 +406,13 @@ struct LayerWork {
         start_tokens();
     }
     __device__ __forceinline__ void start_tokens() {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int i = q + 8 * n + ((int)(threadIdx.x & 31) >> 2);
-            tokens[n] = i < end && 8 * n < COLS ? p.token(s.order[i]) + lane_column() : nullptr;
-        }
+        const int i = q + ((int)(threadIdx.x & 31) >> 2);
+        token = i < end ? p.token(s.order[i]) + lane_column() : nullptr;
     }
     __device__ __forceinline__ void next() {
         c += kLayerColumns;
         if (c < columns) return;
-        c = 0, q += COLS;
+        c = 0, q += kLayerTokens;
         if (q < end) {
             start_tokens();
             return;
@@ -440,72 +442,56 @@ struct LayerWork {
         }
     }
     // Behind the barrier of the grid h is there; other SMs wrote it, so past the L1 cache.
-    __device__ __forceinline__ uint4 load_token(int n, int set, int k) const {
-        if (!P::kSecond) return *reinterpret_cast<const uint4*>(tokens[n] + k);
-        const T* from = tokens[n] + k + (set == 0 ? 0 : static_cast<const T*>(p.a.low) - static_cast<const T*>(p.a.high));
-        return load_l2(reinterpret_cast<const uint4*>(from));
-    }
-    __device__ __forceinline__ void load_tokens(int u, uint4 (&to)[NT][P::kSets]) const {
-        const int k = c + u * 32 * kExpertWarps;
+    __device__ __forceinline__ void load_tokens() {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int u = 0; u < S; ++u)
 #pragma unroll
             for (int set = 0; set < P::kSets; ++set) {
-                to[n][set] = make_uint4(0, 0, 0, 0);
-                if (tokens[n] != nullptr && k + lane_column() < columns) to[n][set] = load_token(n, set, k);
+                const int k = c + u * 32 * kExpertWarps;
+                x[u][set] = make_uint4(0, 0, 0, 0);
+                if (token == nullptr || k + lane_column() >= columns) continue;
+                const T* from = token + k + (set == 0 ? 0 : static_cast<const T*>(p.a.low) - static_cast<const T*>(p.a.high));
+                if constexpr (P::kSecond) x[u][set] = load_l2(reinterpret_cast<const uint4*>(from));
+                else x[u][set] = *reinterpret_cast<const uint4*>(from);
             }
     }
-    __device__ __forceinline__ void load_all_tokens() {
-        if constexpr (kAhead) {
-#pragma unroll
-            for (int u = 0; u < S; ++u) load_tokens(u, x[u]);
-        }
-    }
-    __device__ __forceinline__ void multiply(float (&d)[TILES][NT][4]) {
-        const int warp_column = c + 32 * (int)(threadIdx.x >> 5), n_here = count();
+    __device__ __forceinline__ void multiply(float (&d)[TILES][4]) {
+        const int warp_column = c + 32 * (int)(threadIdx.x >> 5);
 #pragma unroll
         for (int u = 0; u < S; ++u) {
             if (warp_column + u * 32 * kExpertWarps >= columns) break;
-            if constexpr (!kAhead) load_tokens(u, x[0]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (8 * n >= n_here) break;
+            for (int set = 0; set < P::kSets; ++set)
 #pragma unroll
-                for (int set = 0; set < P::kSets; ++set)
-#pragma unroll
-                    for (int m = 0; m < TILES; ++m) mma_step<T>(d[m][n], w[u][m][0], w[u][m][1], x[kAhead ? u : 0][n][set]);
-            }
+                for (int m = 0; m < TILES; ++m) mma_step<T>(d[m], w[u][m][0], w[u][m][1], x[u][set]);
         }
     }
 };
 
 // All blocks of a product; done(slot in order, first row, sums of the TILES tiles)
 // takes an item's sums.  The first block's weights are there.
-template <typename T, int NT, int TILES, typename P, typename F>
-__device__ __forceinline__ void layer_product(LayerWork<T, NT, TILES, P>& work, float* sums, int& turn, F&& done) {
-    constexpr int COLS = 8 * NT;
+template <typename T, int TILES, typename P, typename F>
+__device__ __forceinline__ void layer_product(LayerWork<T, TILES, P>& work, float* sums, int& turn, F&& done) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    float d[TILES][NT][4] = {};
+    float d[TILES][4] = {};
     while (work.here()) {
         work.multiply(d);
         const bool last = work.last_columns();
         const int q = work.q, count = work.count(), row = work.tile * P::kRows;
         work.next();
-        if (work.here()) work.load_weights(), work.load_all_tokens();
+        if (work.here()) work.load_weights(), work.load_tokens();
         if (!last) continue;
         // lane's sums: rows g, g and g + 8, g + 8, tokens 2t, 2t + 1.  Two turns of the memory:
         // one barrier an item.
-        float* mine = sums + turn * kExpertWarps * TILES * COLS * kExpertRows;
+        float* mine = sums + turn * kExpertWarps * TILES * kLayerTokens * kExpertRows;
         turn ^= 1;
 #pragma unroll
-        for (int m = 0; m < TILES; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float* to = mine + ((warp * TILES + m) * COLS + 8 * n + 2 * t) * kExpertRows + g;
-                to[0] = d[m][n][0], to[kExpertRows] = d[m][n][1];
-                to[8] = d[m][n][2], to[kExpertRows + 8] = d[m][n][3];
-                d[m][n][0] = d[m][n][1] = d[m][n][2] = d[m][n][3] = 0.0f;
-            }
+        for (int m = 0; m < TILES; ++m) {
+            float* to = mine + ((warp * TILES + m) * kLayerTokens + 2 * t) * kExpertRows + g;
+            to[0] = d[m][0], to[kExpertRows] = d[m][1];
+            to[8] = d[m][2], to[kExpertRows + 8] = d[m][3];
+            d[m][0] = d[m][1] = d[m][2] = d[m][3] = 0.0f;
+        }
         __syncthreads();
         for (int i = threadIdx.x; i < count * kExpertRows; i += kLayerThreads) {
             float v[TILES];
@@ -513,27 +499,20 @@ __device__ __forceinline__ void layer_product(LayerWork<T, NT, TILES, P>& work, 
             for (int m = 0; m < TILES; ++m) {
                 v[m] = 0.0f;
 #pragma unroll
-                for (int k = 0; k < kExpertWarps; ++k) v[m] += mine[(k * TILES + m) * COLS * kExpertRows + i];
+                for (int k = 0; k < kExpertWarps; ++k) v[m] += mine[(k * TILES + m) * kLayerTokens * kExpertRows + i];
             }
             done(q + i / kExpertRows, row + i % kExpertRows, v);
         }
     }
 }
 
-template <int NT, int UP, int DOWN>
-constexpr size_t layer_smem_bytes() {
-    return (size_t)2 * kExpertWarps * (UP > DOWN ? UP : DOWN) * 8 * NT * kExpertRows * 4;
-}
-
-// CTAs of an SM: two need their 128 registers a thread.
-constexpr int layer_ctas(int nt) { return nt <= 2 ? 2 : 1; }
-
-// NT: tokens taken at once, in eights.  UP, DOWN: 16-row tiles of an item.
-template <typename T, bool GATED, int NT, int UP, int DOWN>
-__global__ void __launch_bounds__(kLayerThreads, layer_ctas(NT)) expert_layer_kernel(const ExpertArgs a) {
+template <typename T, bool GATED>
+__global__ void __launch_bounds__(kLayerThreads, kLayerCtas) expert_layer_kernel(const ExpertArgs a) {
     wait_for_stream();
-    static_assert(!GATED || UP == 2, "up and gate tiles");
-    extern __shared__ __align__(16) float s_sums[];
+    // 16-row tiles of an item: up and gate, or two of up; one of down, beside whose 16 rows
+    // each token has two (items of 32 rows were 1 to 5 % slower)
+    constexpr int UP = 2, DOWN = 1;
+    __shared__ float s_sums[2 * kExpertWarps * UP * kLayerTokens * kExpertRows];
     __shared__ LayerShared s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // the slots by expert
@@ -577,9 +556,9 @@ __global__ void __launch_bounds__(kLayerThreads, layer_ctas(NT)) expert_layer_ke
     int turn = 0;
     {
         const LayerProduct<T, false, GATED, UP> product{a};
-        LayerWork<T, NT, UP, LayerProduct<T, false, GATED, UP>> work(product, s);
-        if (work.here()) work.load_weights(), work.load_all_tokens();
-        layer_product<T, NT, UP>(work, s_sums, turn, [&](int q, int row, const float (&v)[UP]) {
+        LayerWork<T, UP, LayerProduct<T, false, GATED, UP>> work(product, s);
+        if (work.here()) work.load_weights(), work.load_tokens();
+        layer_product<T, UP>(work, s_sums, turn, [&](int q, int row, const float (&v)[UP]) {
             const int64_t to = (int64_t)s.order[q] * a.inner_pad;
 #pragma unroll
             for (int m = 0; m < (GATED ? 1 : UP); ++m) {
@@ -597,12 +576,12 @@ __global__ void __launch_bounds__(kLayerThreads, layer_ctas(NT)) expert_layer_ke
     }
     {
         const LayerProduct<T, true, false, DOWN> product{a};
-        LayerWork<T, NT, DOWN, LayerProduct<T, true, false, DOWN>> work(product, s);
+        LayerWork<T, DOWN, LayerProduct<T, true, false, DOWN>> work(product, s);
         const unsigned token = layer_arrive();
         if (work.here()) work.load_weights();
         layer_wait(token);
-        if (work.here()) work.load_all_tokens();
-        layer_product<T, NT, DOWN>(work, s_sums, turn, [&](int q, int row, const float (&v)[DOWN]) {
+        if (work.here()) work.load_tokens();
+        layer_product<T, DOWN>(work, s_sums, turn, [&](int q, int row, const float (&v)[DOWN]) {
             const int slot = s.order[q];
 #pragma unroll
             for (int m = 0; m < DOWN; ++m)

@@ -28,35 +28,6 @@ static auto up_kernel(bool gated, bool many) {
                  : (many ? expert_up_kernel<T, false, kManyTiles> : expert_up_kernel<T, false, kFewTiles>);
 }
 
-// The one-launch kernel by the tokens that an expert has on average: how many are
-// taken at once, and the rows of an item.
-enum LayerWay { kLayerOne, kLayerFew, kLayerEight, kLayerMany };
-
-static int layer_way(int slots, int experts) {
-    return slots <= experts ? kLayerOne : slots <= 4 * experts ? kLayerFew : slots <= 8 * experts ? kLayerEight : kLayerMany;
-}
-
-template <typename T, bool GATED, int WAY>
-static auto layer_of() {
-    if constexpr (WAY == kLayerOne) return expert_layer_kernel<T, GATED, 1, 2, 1>;
-    else if constexpr (WAY == kLayerFew) return expert_layer_kernel<T, GATED, 1, 2, 2>;
-    else if constexpr (WAY == kLayerEight) return expert_layer_kernel<T, GATED, 2, 2, 2>;
-    else return expert_layer_kernel<T, GATED, 4, 2, 2>;
-}
-template <typename T>
-static auto layer_kernel(bool gated, int way) {
-    return way == kLayerOne     ? (gated ? layer_of<T, true, kLayerOne>() : layer_of<T, false, kLayerOne>())
-           : way == kLayerFew   ? (gated ? layer_of<T, true, kLayerFew>() : layer_of<T, false, kLayerFew>())
-           : way == kLayerEight ? (gated ? layer_of<T, true, kLayerEight>() : layer_of<T, false, kLayerEight>())
-                                : (gated ? layer_of<T, true, kLayerMany>() : layer_of<T, false, kLayerMany>());
-}
-static size_t layer_smem(int way) {
-    return way == kLayerOne     ? layer_smem_bytes<1, 2, 1>()
-           : way == kLayerFew   ? layer_smem_bytes<1, 2, 2>()
-           : way == kLayerEight ? layer_smem_bytes<2, 2, 2>()
-                                : layer_smem_bytes<4, 2, 2>();
-}
-
 // Once per device: the kernels' shared-memory limits.
 static om_status prepare_experts(const DeviceState* d) {
     static std::mutex mu;
@@ -70,10 +41,6 @@ static om_status prepare_experts(const DeviceState* d) {
         for (const bool gated : {false, true}) {
             limit(up_kernel<__half>(gated, true), up_smem(2, kManyTiles));
             limit(up_kernel<__nv_bfloat16>(gated, true), up_smem(2, kManyTiles));
-            for (const int way : {kLayerOne, kLayerFew, kLayerEight, kLayerMany}) {
-                limit(layer_kernel<__half>(gated, way), layer_smem(way));
-                limit(layer_kernel<__nv_bfloat16>(gated, way), layer_smem(way));
-            }
         }
         if (!ok) {
             cudaGetLastError();
@@ -119,18 +86,16 @@ static cudaError_t launch_odd_rows(ExpertArgs a, int sm_count, cudaStream_t st) 
 // Rows that bulk copies can take.
 template <typename T>
 static cudaError_t launch_layer(const ExpertArgs& a, int sm_count, cudaStream_t st) {
-    const int way = layer_way(a.slots, a.experts);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(sm_count * layer_ctas(way == kLayerMany ? 4 : 1)));
+    cfg.gridDim = dim3((unsigned)(sm_count * kLayerCtas));
     cfg.blockDim = dim3(kLayerThreads);
-    cfg.dynamicSmemBytes = layer_smem(way);
     cfg.stream = st;
     cudaLaunchAttribute attr[1] = {};
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto* kern = layer_kernel<T>(a.gate != nullptr, way);
+    auto* kern = a.gate != nullptr ? expert_layer_kernel<T, true> : expert_layer_kernel<T, false>;
     return counted([&] { cudaLaunchKernelEx(&cfg, kern, a); });
 }
 
