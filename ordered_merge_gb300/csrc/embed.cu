@@ -146,7 +146,7 @@ om_status om_embed_lookup(int value_type, const void* table, int64_t rows, int64
     DeviceState* d = nullptr;
     const om_status s = device_state(&d);
     if (s != OM_OK) return s;
-    const EmbedArgs a{table, ids, out, rows, n, table_stride, out_stride, (int)width, id_bytes == 8, 0, 0, scale};
+    const EmbedArgs a{table, ids, out, rows, n, table_stride, out_stride, (int)width, id_bytes == 8, scale};
     const cudaError_t e =
         with_value_type(value_type, [&](auto v) { return launch_lookup<decltype(v)>(a, (cudaStream_t)stream); });
     return e == cudaSuccess ? OM_OK : cuda_fail(e);

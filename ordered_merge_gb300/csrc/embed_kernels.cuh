@@ -40,7 +40,6 @@ struct EmbedArgs {
     void* out;
     int64_t rows, n, table_stride, out_stride;  // strides in values
     int width, wide;
-    int tiles, tile_vectors;  // of a row, and vectors of a tile
     float scale;
 };
 

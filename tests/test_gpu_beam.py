@@ -100,6 +100,20 @@ def test_few_logits_above_many_equal_ones(gpu, dtype, low):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+def test_great_logits_at_a_regular_distance(gpu, dtype):
+    """More great logits than candidates have room, all in the words of a few threads, so that the bound is low."""
+    vocab = 30001
+    logits, scores = _logits(3, 16, vocab, dtype)
+    word = torch.arange(vocab, device="cuda") // (1 if dtype == torch.float32 else 2)
+    for few in (3, 10, 30):
+        great = word % 256 < few
+        x = torch.where(great, logits + 100, logits)
+        _check(gpu, x, 64, scores)
+        x[0, 3] = torch.where(great, 50.0, -50.0).to(dtype)
+        _check(gpu, x, 64, scores)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_ascending_rows(gpu, dtype):
     """The greatest logits all at the end, in one thread's part, and equal in groups."""
     ramp = (torch.arange(30011, device="cuda") // 7).float() / 400
