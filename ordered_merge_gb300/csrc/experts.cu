@@ -83,7 +83,7 @@ static cudaError_t launch_odd_rows(ExpertArgs a, int sm_count, cudaStream_t st) 
     return counted([&] { cudaLaunchKernelEx(&cfg, expert_down_kernel<T>, a); });
 }
 
-// Rows that bulk copies can take.
+// Rows of whole aligned vectors.
 template <typename T>
 static cudaError_t launch_layer(const ExpertArgs& a, int sm_count, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
