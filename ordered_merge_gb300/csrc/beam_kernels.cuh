@@ -114,16 +114,19 @@ struct BeamShared {
     int slow;         // its sum is to be made again
     uint32_t bound;   // image of a lower bound of the slice's top-th greatest
     int found;        // logits that reach the bound
+    int eights;       // eights that hold some
+    uint32_t eight[2 * kBeamThreads];  // which, times 256, and whose
     int count;        // (settling) those counted
     int ties[kBeamWarps];
-    int live;         // units of this CTA that have logits to look at
-    uint8_t unit[kMaxBeams];
+    int live, dead;   // units of this CTA that have logits to look at, and others
+    uint8_t unit[kMaxBeams];  // the former from the front, the latter from the back
 };
 // After it the ring's stages and, in the first CTA of a cluster, the units' lists,
 // [units][top] keys, then the images of the continuations' scores in the same places.
 
-// The two halves of cluster_sync.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+// The two halves of a meeting of the cluster that hands no data on.  (The half that
+// does waits for a trip to memory, 2.3 us while all CTAs' first chunks are on their way.)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // A word pair of CTA `rank`'s shared memory, at the address p has in this CTA's.
@@ -287,32 +290,29 @@ __device__ __forceinline__ void beam_chunk(const unsigned char* stage, uint32_t 
     }
 }
 
-// 16 words, `step` apart within an eight (the second eight past the end where there is
-// none): loaded together, then the few that reach the bound (exceed it: STRICT) one by one.
-template <typename T, bool STRICT>
-__device__ __forceinline__ void look_at(const BeamSlice<T>& slice, float bound, BeamShared& s, int first, int second, int step) {
+// U words, `step` apart, from `first` on: loaded together, then what of them reaches
+// the bound (exceeds it: STRICT) one by one.
+template <typename T, bool STRICT, int U, typename F>
+__device__ __forceinline__ void look_at(const BeamSlice<T>& slice, float bound, BeamShared& s, F&& word_of) {
     auto reaches = [&](float x) { return STRICT ? x > bound : x >= bound && x > -INFINITY; };
-    unsigned near = 0;
-    uint32_t w[2 * kBeamGroup];
+    uint32_t w[U];
 #pragma unroll
-    for (int i = 0; i < 2 * kBeamGroup; ++i) w[i] = slice.word((i < kBeamGroup ? first : second) + i % kBeamGroup * step);
+    for (int i = 0; i < U; ++i) w[i] = slice.word(word_of(i));
 #pragma unroll
-    for (int i = 0; i < 2 * kBeamGroup; ++i) {
+    for (int i = 0; i < U; ++i) {
         const float2 x = word_values(w[i], T{});
-        near |= (reaches(x.x) ? 1u << 2 * i : 0u) | (reaches(x.y) ? 2u << 2 * i : 0u);
-    }
-    for (; near != 0; near &= near - 1) {
-        const int bit = __ffs(near) - 1, i = bit >> 1;
-        const int word = (i < kBeamGroup ? first : second) + i % kBeamGroup * step;
-        const float2 x = word_values(slice.word(word), T{});
-        const int at = atomicAdd(&s.found, 1);
-        if (at < kBeamCandidates) s.key[at] = beam_key(bit & 1 ? x.y : x.x, slice.first + word * WordOf<T>::kPer + (bit & 1));
+        auto keep = [&](float v, int second) {
+            const int at = atomicAdd(&s.found, 1);
+            if (at < kBeamCandidates) s.key[at] = beam_key(v, slice.first + word_of(i) * WordOf<T>::kPer + second);
+        };
+        if (reaches(x.x)) keep(x.x, 0);
+        if (WordOf<T>::kPer == 2 && reaches(x.y)) keep(x.y, 1);
     }
 }
 
-// Threads whose maximum reaches the bound read the one or two eights again that hold
-// what does; for one with more, its warp reads all of its words.  A warp with many
-// such threads leaves the slice to crowded_slice.
+// The one or two eights of a thread that hold what reaches the bound are listed, and
+// read again by all threads, a word each; where a thread has more, its warp reads all of
+// its words.  A warp with many such threads leaves the slice to crowded_slice.
 constexpr int kBeamCrowd = 8;
 
 template <typename T, bool STRICT>
@@ -322,14 +322,47 @@ __device__ __forceinline__ void look_again(const BeamSlice<T>& slice, const Beam
     unsigned todo = __ballot_sync(0xffffffffu, reaches(run.third));
     if (__popc(todo) > kBeamCrowd) {
         if (lane == 0) atomicAdd(&s.found, kBeamCandidates + 1);
-        return;
+        todo = 0;
+    } else if (!(todo >> lane & 1) && reaches(run.most)) {
+        const int at = atomicAdd(&s.eights, reaches(run.second) ? 2 : 1);
+        s.eight[at] = (uint32_t)run.where << 8 | threadIdx.x;
+        if (reaches(run.second)) s.eight[at + 1] = (uint32_t)run.next << 8 | threadIdx.x;
     }
-    if (!(todo >> lane & 1) && reaches(run.most))
-        look_at<T, STRICT>(slice, bound, s, run.where * kBeamGroup * kBeamThreads + (int)threadIdx.x,
-                           reaches(run.second) ? run.next * kBeamGroup * kBeamThreads + (int)threadIdx.x : words, kBeamThreads);
-    for (; todo != 0; todo &= todo - 1)
-        for (int w = ((int)threadIdx.x & ~31) + __ffs(todo) - 1 + lane * kBeamThreads; w < words; w += 64 * kBeamGroup * kBeamThreads)
-            look_at<T, STRICT>(slice, bound, s, w, w + 32 * kBeamGroup * kBeamThreads, 32 * kBeamThreads);
+    for (; todo != 0; todo &= todo - 1) {
+        const int from = ((int)threadIdx.x & ~31) + __ffs(todo) - 1 + lane * kBeamThreads;
+        for (int w = from; w < words; w += 64 * kBeamGroup * kBeamThreads)
+            look_at<T, STRICT, 2 * kBeamGroup>(slice, bound, s, [&](int i) { return w + i * 32 * kBeamThreads; });
+    }
+    __syncthreads();
+    const int all = s.eights * kBeamGroup;
+    auto word_of = [&](int i) {
+        const uint32_t e = s.eight[min(i, all - 1) / kBeamGroup];
+        const int word = ((int)(e >> 8) * kBeamGroup + i % kBeamGroup) * kBeamThreads + (int)(e & 255);
+        return i < all ? word : words;
+    };
+    if (all <= kBeamThreads) {
+        if ((int)threadIdx.x < all) look_at<T, STRICT, 1>(slice, bound, s, [&](int) { return word_of(threadIdx.x); });
+    } else if (s.found <= kBeamCandidates) {
+        for (int i0 = threadIdx.x; i0 < all; i0 += 4 * kBeamThreads)
+            look_at<T, STRICT, 4>(slice, bound, s, [&](int i) { return word_of(i0 + i * kBeamThreads); });
+    }
+}
+
+// How many of n numbers (or equal ones before it) are greater than number c of them,
+// by `lanes` neighbouring threads (a power of two) together.  Whole warps.
+__device__ __forceinline__ int place_of(const uint64_t* numbers, int n, int c, int lanes) {
+    const uint64_t mine = numbers[min(c, n - 1)];
+    int place = 0;
+#pragma unroll 4
+    for (int o = (int)threadIdx.x & (lanes - 1); o < n; o += lanes) place += numbers[o] + (o < c) > mine;
+    for (int d = 1; d < lanes; d <<= 1) place += __shfl_xor_sync(0xffffffffu, place, d);
+    return place;
+}
+// As many lanes for each of n as there are threads.
+__device__ __forceinline__ int place_lanes(int n) {
+    int lanes = 1;
+    while (lanes < 32 && 2 * lanes * n <= kBeamThreads) lanes *= 2;
+    return lanes;
 }
 
 // The candidates of a slice of which too many reach the bound.  Most often these are
@@ -340,7 +373,7 @@ template <typename T>
 __device__ __noinline__ int crowded_slice(const BeamSlice<T>& slice, const BeamRunning& run, float bound, int top, BeamShared& s) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     __syncthreads();  // all have read s.found
-    if (threadIdx.x == 0) s.found = 0;
+    if (threadIdx.x == 0) s.found = 0, s.eights = 0;
     __syncthreads();
     look_again<T, true>(slice, run, bound, s);
     __syncthreads();
@@ -396,7 +429,7 @@ __device__ __forceinline__ void beam_slice_end(const BeamArgs& a, const BeamSlic
     const float most = warp_max(m), scale = warp_max(run.scale);
     const float all = warp_sum(run.total() * exp2_fast(run.scale - scale));
     if (lane == 0) s.warp_max[warp] = most, s.warp_scale[warp] = scale, s.warp_sum[warp] = all;
-    if (threadIdx.x == 0) s.found = 0, s.bound = 0xffffffffu;
+    if (threadIdx.x == 0) s.found = 0, s.eights = 0, s.bound = 0xffffffffu;
     __syncthreads();
     {  // two threads a group, each comparing with half of the groups
         int rank = 0;
@@ -449,12 +482,10 @@ __device__ __forceinline__ void beam_slice_end(const BeamArgs& a, const BeamSlic
     int found = s.found;
     if (found > kBeamCandidates) found = crowded_slice(slice, run, bound, a.top, s);
     uint64_t* list = lists + unit * a.top;
-    for (int c = threadIdx.x; c < found; c += kBeamThreads) {
-        const uint64_t mine = s.key[c];
-        int rank = 0;
-#pragma unroll 4
-        for (int o = 0; o < found; ++o) rank += s.key[o] > mine;
-        if (rank < a.top) store_peer(list + rank, 0, mine);
+    const int lanes = place_lanes(found), each = kBeamThreads / lanes, own = (int)threadIdx.x / lanes;
+    for (int c0 = 0; c0 < found; c0 += each) {
+        const int c = c0 + own, place = place_of(s.key, found, c, lanes);
+        if (c < found && place < a.top && own * lanes == (int)threadIdx.x) store_peer(list + place, 0, s.key[c]);
     }
     for (int r = found + threadIdx.x; r < a.top; r += kBeamThreads) store_peer(list + r, 0, 0ull);
     __syncthreads();  // s is used again
@@ -487,7 +518,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
     const int units = a.beams * a.parts;
     const uint64_t policy = l2_policy_evict_first();
     // thread 0: slices to come, where the next chunk starts, and bytes left of its slice
-    int live = 0, next_slice = 0;
+    int live = 0, dead = 0, next_slice = 0;
     int64_t left = 0;
     uintptr_t from = 0;
     auto fill = [&](int stage) {
@@ -518,16 +549,15 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
             }
             const unsigned there = __ballot_sync(0xffffffffu, looks);
             if (looks) s.unit[live + __popc(there & ((1u << threadIdx.x) - 1))] = (uint8_t)u;
-            live += __popc(there);
+            const unsigned rest = __ballot_sync(0xffffffffu, u < units && !looks);
+            if (rest >> threadIdx.x & 1) s.unit[kMaxBeams - 1 - dead - __popc(rest & ((1u << threadIdx.x) - 1))] = (uint8_t)u;
+            live += __popc(there), dead += __popc(rest);
         }
         __syncwarp();
         if (threadIdx.x == 0) {
-            s.live = live;
+            s.live = live, s.dead = dead;
             for (int i = 0; i < a.stages; ++i) fill(i);
         }
-    } else if (rank == 0) {  // slices without logits to look at leave these as they are
-        for (int i = threadIdx.x - 32; i < units; i += kBeamThreads - 32) s.base[i] = make_float2(-INFINITY, 0.0f), s.sum[i] = 0;
-        for (int i = threadIdx.x - 32; i < units * a.top; i += kBeamThreads - 32) lists[i] = 0;
     }
     __syncthreads();
     if (ctas > 1) cluster_arrive();  // and wait before the first store to the first CTA's shared memory
@@ -551,8 +581,14 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
         if (k == 0 && ctas > 1) cluster_wait();
         beam_slice_end<T>(a, slice, unit, run, lists, s);
     }
+    if (live == 0 && ctas > 1) cluster_wait();
+    dead = s.dead;
+    for (int i = threadIdx.x; i < dead * (a.top + 1); i += kBeamThreads) {
+        const int unit = s.unit[kMaxBeams - 1 - i / (a.top + 1)], r = i % (a.top + 1);
+        if (r < a.top) store_peer(lists + unit * a.top + r, 0, 0ull);
+        else store_stats(s, unit, -INFINITY, 0.0f, 0.0f);
+    }
     if (ctas > 1) {
-        if (live == 0) cluster_wait();
         cluster_sync();
         if (rank != 0) return;
     } else {
@@ -579,32 +615,31 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
         s.score[i] = a.scores == nullptr ? 0.0f : a.scores[b * a.beams + i];
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < units * a.top; c += kBeamThreads) {
-        const int beam = c / a.top / a.parts;
+    const int n = units * a.top, per = a.top * a.parts;
+    for (int c = threadIdx.x; c < n; c += kBeamThreads) {
+        const int beam = c / per;
         uint64_t image = 0;
         if (lists[c] != 0) {
             const double v = (double)s.score[beam] + ((double)image_score((uint32_t)(lists[c] >> 32)) - s.lse[beam]);
             if ((float)v > -INFINITY) image = score_image64(v);
         }
-        if (c % (a.top * a.parts) == 0 && a.finished != nullptr && a.finished[b * a.beams + beam] != 0) {
+        if (c == beam * per && a.finished != nullptr && a.finished[b * a.beams + beam] != 0) {
             lists[c] = (uint32_t)~(uint32_t)a.end_id;
             if (s.score[beam] > -INFINITY) image = score_image64((double)s.score[beam]);
         }
         images[c] = image;
     }
     __syncthreads();
-    const int n = units * a.top;
     if (n <= kBeamCounted) {
         // the place of a continuation is the number of those before it
-        for (int c = threadIdx.x; c < n; c += kBeamThreads) {
+        const int lanes = place_lanes(n), each = kBeamThreads / lanes, own = (int)threadIdx.x / lanes;
+        for (int c0 = 0; c0 < n; c0 += each) {
+            const int c = c0 + own, place = place_of(images, n, c, lanes);
+            if (c >= n || place >= a.top || own * lanes != (int)threadIdx.x) continue;
             const uint64_t mine = images[c];
-            int rank = 0;
-#pragma unroll 4
-            for (int o = 0; o < n; ++o) rank += images[o] > mine || (images[o] == mine && o < c);
-            if (rank >= a.top) continue;
-            const int64_t to = b * a.top + rank;
+            const int64_t to = b * a.top + place;
             a.out_scores[to] = mine != 0 ? (float)image64_score(mine) : -INFINITY;
-            a.out_parents[to] = mine != 0 ? c / a.top / a.parts : -1;
+            a.out_parents[to] = mine != 0 ? c / per : -1;
             a.out_tokens[to] = mine != 0 ? (int32_t)~(uint32_t)lists[c] : -1;
         }
         return;
