@@ -16,7 +16,7 @@ constexpr int kMaxBeamTop = 64;
 
 // ------------------------------------------------------------ selection --
 
-constexpr int kBeamThreads = 256;
+constexpr int kBeamThreadBits = 8, kBeamThreads = 1 << kBeamThreadBits;
 constexpr int kBeamWarps = kBeamThreads / 32;
 constexpr int kBeamGroups = 128;       // pairs of threads, of whose maxima the top-th bounds the selection
 constexpr int kBeamCandidates = 512;   // entries of a slice that may reach that bound
@@ -105,7 +105,8 @@ struct BeamShared {
     double lse[kMaxBeams];
     float2 base[kMaxBeams];    // of each unit: the sum of exp(x - base), base in two parts
     uint64_t sum[kMaxBeams];   // (a float)
-    float score[kMaxBeams];
+    float score[kMaxBeams];    // (first CTA) of each beam, and whether it is finished
+    uint8_t ended[kMaxBeams];
     uint32_t group_key[kBeamGroups];
     float warp_max[kBeamWarps];
     float warp_scale[kBeamWarps];
@@ -123,6 +124,12 @@ struct BeamShared {
 };
 // After it the ring's stages and, in the first CTA of a cluster, the units' lists,
 // [units][top] keys, then the images of the continuations' scores in the same places.
+
+__device__ __forceinline__ uint32_t cluster_index() {
+    uint32_t i;
+    asm("mov.u32 %0, %%clusterid.x;" : "=r"(i));
+    return i;
+}
 
 // The two halves of a meeting of the cluster that hands no data on.  (The half that
 // does waits for a trip to memory, 2.3 us while all CTAs' first chunks are on their way.)
@@ -255,35 +262,38 @@ struct BeamRunning {
 // A thread's words of a chunk of `words`, word i of which starts `offset` bytes into
 // the stage and 4 i on.  Which words a thread has does not depend on the row's
 // address, so that equal rows have equal sums and equal continuations tie.
-template <typename T>
-__device__ __forceinline__ void beam_chunk(const unsigned char* stage, uint32_t offset, int words, int logits, int chunk,
-                                           BeamRunning& run) {
-    const uint32_t* s = reinterpret_cast<const uint32_t*>(stage) + offset / 4 + threadIdx.x;
-    const bool odd = offset & 2;  // 16-bit logits between two words
+template <typename T, bool ODD>  // ODD: 16-bit logits between two words
+__device__ __forceinline__ void beam_whole_chunk(const uint32_t* s, int chunk, BeamRunning& run) {
     constexpr int W = kBeamGroup;
-    const bool whole = words == kBeamChunk && logits == words * WordOf<T>::kPer;
 #pragma unroll
     for (int j = 0; j < kBeamEach / W; ++j) {
         uint32_t w[W];
-        if (whole) {
 #pragma unroll
-            for (int i = 0; i < W; ++i) w[i] = s[(j * W + i) * kBeamThreads];
-            if (odd) {
+        for (int i = 0; i < W; ++i) w[i] = s[(j * W + i) * kBeamThreads];
+        if constexpr (ODD) {
 #pragma unroll
-                for (int i = 0; i < W; ++i) w[i] = __byte_perm(w[i], s[(j * W + i) * kBeamThreads + 1], 0x5432);
-            }
-        } else {
-            if (j * W * kBeamThreads >= words) break;
+            for (int i = 0; i < W; ++i) w[i] = __byte_perm(w[i], s[(j * W + i) * kBeamThreads + 1], 0x5432);
+        }
+        run.add(w, chunk * (kBeamEach / W) + j, T{});
+    }
+}
+template <typename T>
+__device__ __forceinline__ void beam_last_chunk(const uint32_t* s, bool odd, int logits, int chunk, BeamRunning& run) {
+    constexpr int W = kBeamGroup;
+    const int words = (logits + WordOf<T>::kPer - 1) / WordOf<T>::kPer;
+#pragma unroll 1
+    for (int j = 0; j < kBeamEach / W; ++j) {
+        uint32_t w[W];
+        if (j * W * kBeamThreads >= words) break;
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const int at = (j * W + i) * kBeamThreads + (int)threadIdx.x;
-                w[i] = WordOf<T>::kNone;
-                if (at < words) {
-                    w[i] = s[(j * W + i) * kBeamThreads];
-                    const bool half = sizeof(T) == 2 && 2 * at + 1 == logits;  // its second value is none of the row's
-                    if (odd) w[i] = __byte_perm(w[i], half ? 0u : s[(j * W + i) * kBeamThreads + 1], 0x5432);
-                    if (half) w[i] = (w[i] & 0xffffu) | (WordOf<T>::kNone & 0xffff0000u);
-                }
+        for (int i = 0; i < W; ++i) {
+            const int at = (j * W + i) * kBeamThreads + (int)threadIdx.x;
+            w[i] = WordOf<T>::kNone;
+            if (at < words) {
+                w[i] = s[(j * W + i) * kBeamThreads];
+                const bool half = sizeof(T) == 2 && 2 * at + 1 == logits;  // its second value is none of the row's
+                if (odd) w[i] = __byte_perm(w[i], half ? 0u : s[(j * W + i) * kBeamThreads + 1], 0x5432);
+                if (half) w[i] = (w[i] & 0xffffu) | (WordOf<T>::kNone & 0xffff0000u);
             }
         }
         run.add(w, chunk * (kBeamEach / W) + j, T{});
@@ -349,8 +359,9 @@ __device__ __forceinline__ void look_again(const BeamSlice<T>& slice, const Beam
 }
 
 // How many of n numbers (or equal ones before it) are greater than number c of them,
-// by `lanes` neighbouring threads (a power of two) together.  Whole warps.
-__device__ __forceinline__ int place_of(const uint64_t* numbers, int n, int c, int lanes) {
+// by 2^bits neighbouring threads together.  Whole warps.
+__device__ __forceinline__ int place_of(const uint64_t* numbers, int n, int c, int bits) {
+    const int lanes = 1 << bits;
     const uint64_t mine = numbers[min(c, n - 1)];
     int place = 0;
 #pragma unroll 4
@@ -358,12 +369,8 @@ __device__ __forceinline__ int place_of(const uint64_t* numbers, int n, int c, i
     for (int d = 1; d < lanes; d <<= 1) place += __shfl_xor_sync(0xffffffffu, place, d);
     return place;
 }
-// As many lanes for each of n as there are threads.
-__device__ __forceinline__ int place_lanes(int n) {
-    int lanes = 1;
-    while (lanes < 32 && 2 * lanes * n <= kBeamThreads) lanes *= 2;
-    return lanes;
-}
+// As many threads for each of n as there are, in bits.
+__device__ __forceinline__ int place_bits(int n) { return min(max(__clz(max(n - 1, 1)) - (32 - kBeamThreadBits), 0), 5); }
 
 // The candidates of a slice of which too many reach the bound.  Most often these are
 // ties with the bound itself (rows of one value; of few values and a low one for what
@@ -482,10 +489,10 @@ __device__ __forceinline__ void beam_slice_end(const BeamArgs& a, const BeamSlic
     int found = s.found;
     if (found > kBeamCandidates) found = crowded_slice(slice, run, bound, a.top, s);
     uint64_t* list = lists + unit * a.top;
-    const int lanes = place_lanes(found), each = kBeamThreads / lanes, own = (int)threadIdx.x / lanes;
-    for (int c0 = 0; c0 < found; c0 += each) {
-        const int c = c0 + own, place = place_of(s.key, found, c, lanes);
-        if (c < found && place < a.top && own * lanes == (int)threadIdx.x) store_peer(list + place, 0, s.key[c]);
+    const int bits = place_bits(found), own = (int)threadIdx.x >> bits;
+    for (int c0 = 0; c0 < found; c0 += kBeamThreads >> bits) {
+        const int c = c0 + own, place = place_of(s.key, found, c, bits);
+        if (c < found && place < a.top && own << bits == (int)threadIdx.x) store_peer(list + place, 0, s.key[c]);
     }
     for (int r = found + threadIdx.x; r < a.top; r += kBeamThreads) store_peer(list + r, 0, 0ull);
     __syncthreads();  // s is used again
@@ -514,24 +521,27 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
     unsigned char* ring = s_raw + beam_ring_offset();
     uint64_t* lists = reinterpret_cast<uint64_t*>(ring + a.stages * kBeamStageBytes);
     const uint32_t ctas = cluster_size(), rank = cluster_rank();
-    const int64_t b = blockIdx.x / ctas;
+    const int64_t b = cluster_index();
     const int units = a.beams * a.parts;
     const uint64_t policy = l2_policy_evict_first();
-    // thread 0: slices to come, where the next chunk starts, and bytes left of its slice
-    int live = 0, dead = 0, next_slice = 0;
-    int64_t left = 0;
+    // thread 0: slices to come, where the next copy starts, how many there are of its slice, their bytes and the last one's
+    int live = 0, dead = 0, next_slice = 0, copies = 0;
+    uint32_t bytes = 0, last_bytes = 0;
     uintptr_t from = 0;
     auto fill = [&](int stage) {
-        if (left <= 0) {
+        if (copies == 0) {
             if (next_slice >= live) return;
             const BeamSlice<T> slice(a, b, s.unit[next_slice++]);
             from = reinterpret_cast<uintptr_t>(slice.row + slice.first);
-            left = (int64_t)slice.n * (int)sizeof(T);
+            const uint32_t skip = (uint32_t)(from & 15);
+            from -= skip, copies = slice.chunks();
+            bytes = kBeamChunk * 4 + (skip != 0 ? 16 : 0);
+            last_bytes = (uint32_t)((int64_t)slice.n * (int)sizeof(T) - (int64_t)(copies - 1) * (kBeamChunk * 4) + skip + 15) & ~15u;
         }
-        const uint32_t skip = (uint32_t)(from & 15), whole = (skip + (uint32_t)min((int64_t)kBeamChunk * 4, left) + 15) & ~15u;
-        mbar_arrive_expect_tx(&s.full[stage], whole);
-        bulk_copy_g2s(ring + stage * kBeamStageBytes, reinterpret_cast<const void*>(from - skip), whole, &s.full[stage], policy);
-        from += kBeamChunk * 4, left -= kBeamChunk * 4;
+        const uint32_t now = --copies == 0 ? last_bytes : bytes;
+        mbar_arrive_expect_tx(&s.full[stage], now);
+        bulk_copy_g2s(ring + stage * kBeamStageBytes, reinterpret_cast<const void*>(from), now, &s.full[stage], policy);
+        from += kBeamChunk * 4;
     };
     if (threadIdx.x < 32) {  // the slices of this CTA that have logits to look at
         if (threadIdx.x == 0) {
@@ -558,6 +568,10 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
             s.live = live, s.dead = dead;
             for (int i = 0; i < a.stages; ++i) fill(i);
         }
+    } else if (rank == 0 && (int)threadIdx.x - 32 < a.beams) {  // for the end
+        const int i = (int)threadIdx.x - 32;
+        s.score[i] = a.scores == nullptr ? 0.0f : a.scores[b * a.beams + i];
+        s.ended[i] = a.finished != nullptr && a.finished[b * a.beams + i] != 0;
     }
     __syncthreads();
     if (ctas > 1) cluster_arrive();  // and wait before the first store to the first CTA's shared memory
@@ -569,11 +583,16 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
         const BeamSlice<T> slice(a, b, unit);
         const int chunks = slice.chunks();
         BeamRunning run;
-        for (int c = 0; c < chunks; ++c) {
+        const uint32_t skip = (uint32_t)(reinterpret_cast<uintptr_t>(slice.row + slice.first) & 15);  // chunks are whole 16 bytes
+        const uint32_t* words = reinterpret_cast<const uint32_t*>(ring + (skip & ~3u)) + threadIdx.x;
+        const bool odd = skip & 2;
+        int left = slice.n;
+        for (int c = 0; c < chunks; ++c, left -= kBeamChunk * WordOf<T>::kPer) {
             mbar_wait_bounded(&s.full[stage], phase, a.err);
-            const uint32_t skip = (uint32_t)((reinterpret_cast<uintptr_t>(slice.row + slice.first)) & 15);  // chunks are whole 16 bytes
-            const int left = slice.n - c * kBeamChunk * WordOf<T>::kPer, logits = min(left, kBeamChunk * WordOf<T>::kPer);
-            beam_chunk<T>(ring + stage * kBeamStageBytes, skip, (logits + WordOf<T>::kPer - 1) / WordOf<T>::kPer, logits, c, run);
+            const uint32_t* mine = words + stage * (kBeamStageBytes / 4);
+            if (left < kBeamChunk * WordOf<T>::kPer) beam_last_chunk<T>(mine, odd, left, c, run);
+            else if (sizeof(T) == 2 && odd) beam_whole_chunk<T, sizeof(T) == 2>(mine, c, run);
+            else beam_whole_chunk<T, false>(mine, c, run);
             __syncthreads();
             if (threadIdx.x == 0) fill(stage);
             if (++stage == a.stages) stage = 0, phase ^= 1;
@@ -612,7 +631,6 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
         const int exponent = (int)(__float_as_uint(sum) >> 23) - 127;
         const float fraction = __uint_as_float((__float_as_uint(sum) & 0x7fffffu) | 0x3f800000u);
         s.lse[i] = sum > 0.0f ? (double)most.x + ((double)(most.y + logf(fraction)) + exponent * 0.6931471805599453) : (double)NAN;
-        s.score[i] = a.scores == nullptr ? 0.0f : a.scores[b * a.beams + i];
     }
     __syncthreads();
     const int n = units * a.top, per = a.top * a.parts;
@@ -623,7 +641,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
             const double v = (double)s.score[beam] + ((double)image_score((uint32_t)(lists[c] >> 32)) - s.lse[beam]);
             if ((float)v > -INFINITY) image = score_image64(v);
         }
-        if (c == beam * per && a.finished != nullptr && a.finished[b * a.beams + beam] != 0) {
+        if (c == beam * per && s.ended[beam]) {
             lists[c] = (uint32_t)~(uint32_t)a.end_id;
             if (s.score[beam] > -INFINITY) image = score_image64((double)s.score[beam]);
         }
@@ -632,10 +650,10 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
     __syncthreads();
     if (n <= kBeamCounted) {
         // the place of a continuation is the number of those before it
-        const int lanes = place_lanes(n), each = kBeamThreads / lanes, own = (int)threadIdx.x / lanes;
-        for (int c0 = 0; c0 < n; c0 += each) {
-            const int c = c0 + own, place = place_of(images, n, c, lanes);
-            if (c >= n || place >= a.top || own * lanes != (int)threadIdx.x) continue;
+        const int bits = place_bits(n), own = (int)threadIdx.x >> bits;
+        for (int c0 = 0; c0 < n; c0 += kBeamThreads >> bits) {
+            const int c = c0 + own, place = place_of(images, n, c, bits);
+            if (c >= n || place >= a.top || own << bits != (int)threadIdx.x) continue;
             const uint64_t mine = images[c];
             const int64_t to = b * a.top + place;
             a.out_scores[to] = mine != 0 ? (float)image64_score(mine) : -INFINITY;
