@@ -47,9 +47,9 @@ static om_status prepare_beam(const DeviceState* d) {
 template <typename T>
 static cudaError_t launch_beam(BeamArgs a, int64_t batch, int sm_count, cudaStream_t st) {
     // CTAs of a cluster: as many as fill the SMs (two each), while slices stay long enough;
-    // 16 only for few sequences with much to read.  (8 and 16: 1 x 4 x 131071 bf16 16.6
-    // and 14.5 us, 1 x 16 53.9 and 39.1, 4 x 8 22.9 and 20.9, but 1 x 4 x 32768 10.4 and
-    // 11.4, 8 x 8 x 131071 23.3 and 26.4, 16 x 8 x 50021 18.6 and 25.9.)
+    // 16 only for few sequences with much to read.  (8 and 16: 1 x 4 x 131071 bf16 12.4
+    // and 11.0 us, 4 x 8 17.5 and 17.0, but 1 x 4 x 32768 8.1 and 8.3, 8 x 8 x 131071 17.8
+    // and 21.7, 16 x 8 x 50021 13.7 and 23.3.)
     const int64_t most = a.beams * std::max<int64_t>(1, a.vocab / kBeamLeastSlice);
     const bool wide = batch <= 4 && (int64_t)a.beams * a.vocab > kBeamCluster * (int64_t)32768;
     int ctas = 1;

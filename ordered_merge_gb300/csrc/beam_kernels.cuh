@@ -26,10 +26,11 @@ constexpr int kBeamChunk = kBeamThreads * kBeamEach;
 constexpr int kBeamMaxStages = 4;      // chunks in shared memory
 constexpr int kBeamStageBytes = kBeamChunk * 4 + 32;
 constexpr int kBeamCluster = 8;
-// Continuations of all slices up to which the best are found by counting, each its
-// greater ones, instead of by one warp that takes a winner after the other (8 of 128:
-// 700 cycles against 4300).
-constexpr int kBeamCounted = 512;
+// Continuations of all slices times slices up to which the best are found by counting,
+// each its greater ones, instead of by one warp that takes a winner after the other (whole
+// calls, counted and taken: 8 slices of 32, 14.8 and 18.2 us; 10 of 20, 16.3 and 17.6; but 12
+// of 24, 24.5 and 20.5, 16 of 16, 12.7 and 12.2, 8 of 64, 30.2 and 28.8, 64 of 8, 35.1 and 20.1).
+constexpr int kBeamCounted = 2048;
 
 struct BeamArgs {
     const void* logits;
@@ -508,10 +509,11 @@ __host__ __device__ constexpr int beam_ring_offset() { return ((int)sizeof(BeamS
 // first CTA joins the slices: the beams' logarithms of their sums, the scores of
 // the slices' best continuations in 64 bits, and the best of all.
 //
-// 64 sequences of 8 beams over 131071 bf16 logits, 0.13 GB: 38.7 us, of which 20 stream
-// at the memory's rate and the rest are a chain that all CTAs walk at once: first
-// loads (3), a slice's bound and its candidates, read once more (6), the cluster's
-// meeting (2), the joining (2).  One prompt of 4 beams is that chain, about 8 us.
+// 64 sequences of 8 beams over 131071 bf16 logits, 0.13 GB: 34.2 us, of which 20 would
+// stream it at the memory's rate.  The first loads take 2.5, the stream 18 on SMs with
+// three of the 512 CTAs and 21 (27 at most) on those with four, a slice's bound and its
+// candidates, read once more, 3, the cluster's meeting and the joining 3.  One prompt of 4
+// beams is that chain, about 8 us.
 // (Vectors loaded straight into registers, rows realigned by shifts: 70 us.)
 template <typename T>
 __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const BeamArgs a) {
@@ -648,7 +650,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
         images[c] = image;
     }
     __syncthreads();
-    if (n <= kBeamCounted) {
+    if (n * units <= kBeamCounted) {
         // the place of a continuation is the number of those before it
         const int bits = place_bits(n), own = (int)threadIdx.x >> bits;
         for (int c0 = 0; c0 < n; c0 += kBeamThreads >> bits) {
