@@ -556,8 +556,9 @@ om_status om_beam_gather(const int32_t *parents, int64_t batch, int64_t beams,
  * `width` values each, multiplied in 32 bits and rounded once.  Rows of the table
  * (of the output) are table_stride (out_stride) values apart.  ids holds n
  * integers of id_bytes (4 or 8) bytes; one outside [0, rows) gives a row of zeros.
- * out shares no byte with the inputs.  rows < 2^31 - 1, n < 2^31, width <= 2^24,
- * strides <= 2^40, else OM_ERANGE.  No scratch.
+ * out shares no byte with the inputs.  Whole aligned 16 bytes around a row's values
+ * are read.  rows < 2^31 - 1, n < 2^31, width <= 2^24, strides <= 2^40, else
+ * OM_ERANGE.  No scratch.
  */
 om_status om_embed_lookup(int value_type, const void *table, int64_t rows,
                           int64_t width, int64_t table_stride, const void *ids,

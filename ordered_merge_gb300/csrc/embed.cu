@@ -24,12 +24,13 @@ static int vector_values(int value, const void* p, int64_t stride, int64_t width
 template <typename T>
 static cudaError_t launch_lookup(EmbedArgs a, cudaStream_t st) {
     constexpr int kMost = 16 / (int)sizeof(T);
-    const int n = std::min(vector_values(sizeof(T), a.table, a.table_stride, a.width),
-                           vector_values(sizeof(T), a.out, a.out_stride, a.width));
-    const int step = n == kMost ? kMost : n >= 2 ? 2 : 1;
-    const int64_t vectors = a.n * (a.width / step), ctas = (vectors + kEmbedThreads * kEmbedUnroll - 1) / (kEmbedThreads * kEmbedUnroll);
+    const int values = std::min(vector_values(sizeof(T), a.table, a.table_stride, a.width),
+                                vector_values(sizeof(T), a.out, a.out_stride, a.width));
+    const bool whole = values == kMost;  // vectors of every row
+    const int64_t vectors = a.n * (whole ? a.width / kMost : ((int64_t)a.width * (int)sizeof(T) + 30) / 16);
+    const int64_t ctas = (vectors + kEmbedThreads * kEmbedUnroll - 1) / (kEmbedThreads * kEmbedUnroll);
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-    auto* kern = step == kMost ? embed_lookup_kernel<T, kMost> : step == 2 ? embed_lookup_kernel<T, 2> : embed_lookup_kernel<T, 1>;
+    auto* kern = whole ? embed_lookup_kernel<T> : embed_lookup_odd_kernel<T>;
     return counted([&] { launch_early(kern, (unsigned)ctas, kEmbedThreads, 0, st, a); });
 }
 

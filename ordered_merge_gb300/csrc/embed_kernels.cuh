@@ -52,9 +52,10 @@ constexpr int kEmbedUnroll = 4;
 // Bound by memory: 65536 rows of 2048 bf16 out of 131072, 0.41 GB with each row that
 // is asked for read once, 71.7 us (5.7 TB/s; CTAs of 64 to 256 threads and 2 to 8
 // vectors a thread come to the same or more).
-template <typename T, int N>
+template <typename T>
 __global__ void __launch_bounds__(kEmbedThreads) embed_lookup_kernel(const EmbedArgs a) {
     wait_for_stream();
+    constexpr int N = 16 / (int)sizeof(T);
     using V = ValueVec<T, N>;
     const int per = a.width / N;
     const uint32_t total_tile = kEmbedThreads * kEmbedUnroll;
@@ -77,12 +78,8 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_lookup_kernel(const Embed
         for (int k = 0; k < N; ++k) v[u].v[k] = from_float<T>(0.0f);
         if (row[u] >= 0) {
             const T* from = static_cast<const T*>(a.table) + row[u] * a.table_stride + piece[u];
-            if constexpr (sizeof(V) == 16) {  // volatile, so that all are on their way together (75.8 us otherwise)
-                const uint4 bits = load_once(reinterpret_cast<const uint4*>(from));
-                v[u] = *reinterpret_cast<const V*>(&bits);
-            } else {
-                v[u] = *reinterpret_cast<const V*>(from);
-            }
+            const uint4 bits = load_once(reinterpret_cast<const uint4*>(from));  // volatile, so that all are on their way together (75.8 us otherwise)
+            v[u] = *reinterpret_cast<const V*>(&bits);
         }
     }
 #pragma unroll
@@ -93,6 +90,73 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_lookup_kernel(const Embed
             for (int k = 0; k < N; ++k) v[u].v[k] = from_float<T>(to_float(v[u].v[k]) * a.scale);
         }
         store_streaming(reinterpret_cast<V*>(static_cast<T*>(a.out) + token[u] * a.out_stride + piece[u]), v[u]);
+    }
+}
+
+// The same for rows that 16-byte vectors do not fit: a thread writes a whole aligned
+// vector of the output, from the one or two aligned vectors of the table that hold its
+// bytes; at a row's ends value by value.  65536 rows of 2047 bf16 122 us, of 2044 121 (by
+// single values 527, by vectors of 8 bytes 264); 32768 of 2047 f32 117 (264), of 2046 116 (133).
+template <typename T>
+__global__ void __launch_bounds__(kEmbedThreads) embed_lookup_odd_kernel(const EmbedArgs a) {
+    wait_for_stream();
+    constexpr int kValues = 16 / (int)sizeof(T);
+    const int64_t length = (int64_t)a.width * (int)sizeof(T);
+    const int per = (int)((length + 30) / 16);  // vectors that a row touches, at most
+    int64_t token[kEmbedUnroll];
+    int piece[kEmbedUnroll];
+#pragma unroll
+    for (int u = 0; u < kEmbedUnroll; ++u) {
+        const int64_t i = (int64_t)blockIdx.x * (kEmbedThreads * kEmbedUnroll) + u * kEmbedThreads + threadIdx.x;
+        token[u] = i <= 0xffffffffll ? (int64_t)((uint32_t)i / (uint32_t)per) : i / per;
+        piece[u] = (int)(i - token[u] * per);
+    }
+    int64_t row[kEmbedUnroll];
+#pragma unroll
+    for (int u = 0; u < kEmbedUnroll; ++u) row[u] = token[u] < a.n ? embed_row(a.ids, a.wide, token[u], a.rows) : -1;
+    uint4 low[kEmbedUnroll], high[kEmbedUnroll];
+    uint32_t shift[kEmbedUnroll];
+#pragma unroll
+    for (int u = 0; u < kEmbedUnroll; ++u) {
+        const uintptr_t to = reinterpret_cast<uintptr_t>(static_cast<T*>(a.out) + token[u] * a.out_stride);
+        const uintptr_t from = reinterpret_cast<uintptr_t>(static_cast<const T*>(a.table) + row[u] * a.table_stride);
+        // of the table what the output's vector holds; it may begin before the row
+        const int64_t offset = (int64_t)piece[u] * 16 - (int64_t)(to & 15);
+        const uintptr_t first = (from + offset) & ~(uintptr_t)15;
+        shift[u] = (uint32_t)(from + offset) & 15;
+        low[u] = high[u] = make_uint4(0, 0, 0, 0);
+        if (row[u] >= 0 && offset < length) {  // only vectors that hold some of the row
+            if (first + 16 > from && first < from + length) low[u] = __ldg(reinterpret_cast<const uint4*>(first));
+            if (shift[u] != 0 && first + 16 < from + length) high[u] = __ldg(reinterpret_cast<const uint4*>(first) + 1);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kEmbedUnroll; ++u) {
+        if (token[u] >= a.n) continue;
+        T* to = static_cast<T*>(a.out) + token[u] * a.out_stride;
+        const int64_t offset = (int64_t)piece[u] * 16 - (int64_t)(reinterpret_cast<uintptr_t>(to) & 15);
+        if (offset >= length) continue;
+        uint32_t w[8] = {low[u].x, low[u].y, low[u].z, low[u].w, high[u].x, high[u].y, high[u].z, high[u].w};
+#pragma unroll
+        for (int k = 0; k < 6; ++k) w[k] = shift[u] & 8 ? w[k + 2] : w[k];
+#pragma unroll
+        for (int k = 0; k < 5; ++k) w[k] = shift[u] & 4 ? w[k + 1] : w[k];
+        uint4 bits;
+        bits.x = __funnelshift_r(w[0], w[1], 8 * (shift[u] & 3)), bits.y = __funnelshift_r(w[1], w[2], 8 * (shift[u] & 3));
+        bits.z = __funnelshift_r(w[2], w[3], 8 * (shift[u] & 3)), bits.w = __funnelshift_r(w[3], w[4], 8 * (shift[u] & 3));
+        ValueVec<T, kValues> v = *reinterpret_cast<const ValueVec<T, kValues>*>(&bits);
+        if (a.scale != 1.0f && row[u] >= 0) {
+#pragma unroll
+            for (int k = 0; k < kValues; ++k) v.v[k] = from_float<T>(to_float(v.v[k]) * a.scale);
+        }
+        T* at = to + offset / (int)sizeof(T);
+        if (offset >= 0 && offset + 16 <= length) {
+            store_streaming(reinterpret_cast<ValueVec<T, kValues>*>(at), v);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kValues; ++k)
+                if (offset + k * (int)sizeof(T) >= 0 && offset + k * (int)sizeof(T) < length) at[k] = v.v[k];
+        }
     }
 }
 

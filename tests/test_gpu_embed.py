@@ -57,6 +57,22 @@ def test_lookup_strided_tables(gpu, dtype):
         assert torch.equal(out, table[ids])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_lookup_odd_rows_and_guards(gpu, dtype):
+    ids = torch.tensor([3, -1, 0, 6, 6, 2, 7, 5], device="cuda")
+    for width in (*range(1, 20), 31, 33, 127, 1025):
+        for shift in range(9):
+            apart = width + shift % 3
+            buf = torch.randn(7 * apart + 16, device="cuda").to(dtype)
+            table = buf[8 - shift:8 - shift + 7 * apart].view(7, apart)[:, :width]
+            around = torch.full((8 * width + 32,), 99.0, device="cuda", dtype=dtype)
+            out = around[shift:shift + 8 * width].view(8, width)
+            gpu.embed_lookup(ids, table, 2.0, out=out)
+            want = torch.where(((ids >= 0) & (ids < 7))[:, None], table[ids.clamp(0, 6)] * 2, 0.0)
+            assert torch.equal(out, want)  # doubling rounds nothing
+            assert torch.all(around[:shift] == 99) and torch.all(around[shift + 8 * width:] == 99)
+
+
 def test_lookup_offsets_past_32_bits(gpu):
     table = torch.zeros(1 << 20, 2200, dtype=torch.float16, device="cuda")  # 4.6 GB
     table[-1], table[(1 << 20) - 7, -1] = 3.0, 4.0
