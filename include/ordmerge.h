@@ -574,6 +574,7 @@ om_status om_embed_lookup(int value_type, const void *table, int64_t rows,
  * nothing.  The tokens are sorted stably and each row's terms added in 32 bits in
  * the order of i, in pieces of 32 (of 128 where n > 16384) that are then added in
  * their order: the same call repeats bit for bit.
+ * Whole aligned 16 bytes around grad's rows are read.
  * Takes stream-ordered scratch from the library's pool: 16 n bytes and, with n >
  * 32, n * width / 4 (a quarter of that where n > 16384).  n <= 2^30, width <=
  * 2^20, n * width < 2^38, rows and strides as above, else OM_ERANGE.

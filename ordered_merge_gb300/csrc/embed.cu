@@ -94,9 +94,8 @@ static cudaError_t launch_backward(EmbedBackArgs a, int sm_count, cudaStream_t s
         const om_status s = om_merge_sort_u32(a.keys, a.slots, a.n, st);
         if (s != OM_OK) return s == OM_ENOMEM ? cudaErrorMemoryAllocation : cudaErrorUnknown;
     }
-    const int step = no == kMostO ? nt : std::min(nt, no);
-    const int values = step == kMostT ? kMostT : step >= 2 ? 2 : 1;
-    a.tiles = (a.width + 32 * values - 1) / (32 * values);
+    const bool whole = nt == kMostT && no == kMostO;  // vectors of every row
+    a.tiles = (a.width + 32 * kMostT - 1) / (32 * kMostT);
     // sorted places of a warp: as few as still give every SM its 48 warps
     a.window = 4;
     while (a.window < 32 && a.n * a.tiles / a.window > 96 * (int64_t)sm_count) a.window *= 2;
@@ -108,9 +107,7 @@ static cudaError_t launch_backward(EmbedBackArgs a, int sm_count, cudaStream_t s
     const int64_t ctas = a.sum_ctas + (zeros + per - 1) / per;
     if (ctas == 0) return e;
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-    auto* kern = values == kMostT ? embed_sum_kernel<T, O, kMostT>
-                 : values == 2    ? embed_sum_kernel<T, O, 2>
-                                  : embed_sum_kernel<T, O, 1>;
+    auto* kern = whole ? embed_sum_kernel<T, O, false> : embed_sum_kernel<T, O, true>;
     e = counted([&] { launch_early(kern, (unsigned)ctas, kEmbedSumThreads, 0, st, a); });
     const int64_t joins = (a.n - 1) >> a.piece_bits;  // multiples of a piece's length in (0, n)
     if (e == cudaSuccess && joins > 0) {

@@ -32,6 +32,18 @@ __device__ __forceinline__ void store_streaming(ValueVec<T, N>* p, const ValueVe
     else __stcs(reinterpret_cast<unsigned short*>(p), *reinterpret_cast<const unsigned short*>(&v));
 }
 
+// 16 of 32 bytes, from byte `shift` (a multiple of two) below 16 on.
+__device__ __forceinline__ uint4 shifted_vector(const uint4& low, const uint4& high, uint32_t shift) {
+    uint32_t w[8] = {low.x, low.y, low.z, low.w, high.x, high.y, high.z, high.w};
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = shift & 8 ? w[k + 2] : w[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = shift & 4 ? w[k + 1] : w[k];
+    const uint32_t bits = 8 * (shift & 3);
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
 // --------------------------------------------------------------- lookup --
 
 struct EmbedArgs {
@@ -136,14 +148,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_lookup_odd_kernel(const E
         T* to = static_cast<T*>(a.out) + token[u] * a.out_stride;
         const int64_t offset = (int64_t)piece[u] * 16 - (int64_t)(reinterpret_cast<uintptr_t>(to) & 15);
         if (offset >= length) continue;
-        uint32_t w[8] = {low[u].x, low[u].y, low[u].z, low[u].w, high[u].x, high[u].y, high[u].z, high[u].w};
-#pragma unroll
-        for (int k = 0; k < 6; ++k) w[k] = shift[u] & 8 ? w[k + 2] : w[k];
-#pragma unroll
-        for (int k = 0; k < 5; ++k) w[k] = shift[u] & 4 ? w[k + 1] : w[k];
-        uint4 bits;
-        bits.x = __funnelshift_r(w[0], w[1], 8 * (shift[u] & 3)), bits.y = __funnelshift_r(w[1], w[2], 8 * (shift[u] & 3));
-        bits.z = __funnelshift_r(w[2], w[3], 8 * (shift[u] & 3)), bits.w = __funnelshift_r(w[3], w[4], 8 * (shift[u] & 3));
+        const uint4 bits = shifted_vector(low[u], high[u], shift[u]);
         ValueVec<T, kValues> v = *reinterpret_cast<const ValueVec<T, kValues>*>(&bits);
         if (a.scale != 1.0f && row[u] >= 0) {
 #pragma unroll
@@ -397,14 +402,9 @@ __global__ void __launch_bounds__(256) embed_keys_kernel(const EmbedBackArgs a) 
 constexpr int kEmbedSumThreads = 128;
 constexpr int kEmbedSumRows = 16;  // rows of a warp in flight
 
-// Copies a lane's vector into its own place of shared memory, in the background
-// where the hardware has such copies (4, 8 and 16 bytes).
-template <typename V>
-__device__ __forceinline__ void copy_async(V* to, const V* from) {
-    constexpr int B = (int)sizeof(V);
-    if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
-    else if constexpr (B >= 4) asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(to)), "l"(from), "n"(B) : "memory");
-    else *to = *from;
+// Copies a vector into shared memory in the background.
+__device__ __forceinline__ void copy_async(uint4* to, const uint4* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Until at most N of the groups committed last are on their way.
@@ -464,9 +464,9 @@ __device__ __forceinline__ void store_sums(const EmbedBackArgs& a, uint32_t row,
 }
 
 // Zeros in those rows of a warp's share that no token asks for.
-template <typename O, int N>
+template <typename O, bool ODD>
 __device__ __forceinline__ void zero_rows(const EmbedBackArgs& a, int64_t warp) {
-    constexpr int W = N * (int)sizeof(O) > 16 ? 16 / (int)sizeof(O) : N;  // values of a store
+    constexpr int W = 16 / (int)sizeof(O);  // values of a store
     using V = ValueVec<O, W>;
     const int lane = threadIdx.x & 31;
     const int64_t lo = warp * a.zero_rows, mine = lo + lane;
@@ -485,7 +485,14 @@ __device__ __forceinline__ void zero_rows(const EmbedBackArgs& a, int64_t warp) 
     for (int k = 0; k < W; ++k) none.v[k] = from_float<O>(0.0f);
     for (unsigned todo = __ballot_sync(0xffffffffu, absent); todo != 0; todo &= todo - 1) {
         O* out = static_cast<O*>(a.grad_table) + (lo + __ffs(todo) - 1) * a.table_stride;
-        for (int c = lane * W; c < a.width; c += 32 * W) store_streaming(reinterpret_cast<V*>(out + c), none);
+        int from = 0;  // what lies before the first whole vector
+        if constexpr (ODD) {
+            from = min((int)(-reinterpret_cast<uintptr_t>(out) & 15) / (int)sizeof(O), a.width);
+            if (lane < from) out[lane] = none.v[0];
+            const int rest = (a.width - from) % W;
+            if (lane < rest) out[a.width - rest + lane] = none.v[0];
+        }
+        for (int c = from + lane * W, end = a.width - W; c <= end; c += 32 * W) store_streaming(reinterpret_cast<V*>(out + c), none);
     }
 }
 
@@ -497,23 +504,29 @@ __device__ __forceinline__ void zero_rows(const EmbedBackArgs& a, int64_t warp) 
 // in its order and putting the sum away where a piece ends: to the table, or, for
 // pieces of a longer run, to `partial`.
 //
+// ODD: rows that 16-byte vectors do not fit come in as the aligned vectors that hold
+// them, 33 for the 32 of a tile, and each lane shifts its columns out of two; sums go out
+// through shared memory, neighbouring lanes' value by value.  (32784 rows of 2047 bf16 to
+// as many rows 88 us, by single values 201; of 2046 to f32 98, by two values 122.)
+//
 // Zeros: a warp searches the sorted tokens for its rows.
 //
 // Bound by memory: 65537 tokens into 131072 rows of 2048, bf16 to f32, 1.34 GB, 188 us
 // (7.1 TB/s).  (Rows in registers, eight at a time, took 128 us for the sums alone,
 // which take 83 so; the zeros apart from them, beside the sort, as much in all.)
-template <typename T, typename O, int N>
+template <typename T, typename O, bool ODD>
 __global__ void __launch_bounds__(kEmbedSumThreads) embed_sum_kernel(const EmbedBackArgs a) {
     wait_for_stream();
     if ((int64_t)blockIdx.x >= a.sum_ctas) {
-        zero_rows<O, N>(a, ((int64_t)blockIdx.x - a.sum_ctas) * (kEmbedSumThreads / 32) + (threadIdx.x >> 5));
+        zero_rows<O, ODD>(a, ((int64_t)blockIdx.x - a.sum_ctas) * (kEmbedSumThreads / 32) + (threadIdx.x >> 5));
         return;
     }
+    constexpr int N = 16 / (int)sizeof(T), D = kEmbedSumRows, R = ODD ? 33 : 32;
     using V = ValueVec<T, N>;
-    constexpr int D = kEmbedSumRows;
-    __shared__ V s_ring[kEmbedSumThreads / 32][D][32];
+    // a warp's ring and, ODD, the sums on their way out
+    __shared__ uint4 s_ring[kEmbedSumThreads / 32][D * R + (ODD ? 8 * N : 0)];
     const int lane = threadIdx.x & 31;
-    V* ring = &s_ring[threadIdx.x >> 5][0][lane];
+    uint4* ring = &s_ring[threadIdx.x >> 5][lane];
     const int64_t warp = (int64_t)blockIdx.x * (kEmbedSumThreads / 32) + (threadIdx.x >> 5);
     const int64_t w = warp / a.tiles, lo = w * a.window;
     if (lo >= a.n) return;
@@ -527,7 +540,27 @@ __global__ void __launch_bounds__(kEmbedSumThreads) embed_sum_kernel(const Embed
 #pragma unroll
     for (int n = 0; n < N; ++n) sum[n] = 0.0f;
     auto put_away = [&](uint32_t next_key) {
-        if (at < 0 || !inside) return;
+        if (at < 0) return;
+        if constexpr (ODD) {  // neighbouring lanes store neighbouring values
+            float* all = reinterpret_cast<float*>(&s_ring[threadIdx.x >> 5][D * R]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < N; ++k) all[lane * N + k] = sum[k];
+            __syncwarp();
+            const bool whole_run = run_start && next_key != row;
+            const int first = column - lane * N, most = min(32 * N, a.width - first);
+            O* table = static_cast<O*>(a.grad_table) + (int64_t)row * a.table_stride + first;
+            float* part = a.partial + piece_slot(a, at, run_start) * a.width + first;
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int c = 32 * k + lane;
+                if (c >= most) break;
+                if (whole_run) table[c] = from_float<O>(a.accumulate ? to_float(table[c]) + all[c] * a.scale : all[c] * a.scale);
+                else part[c] = all[c];
+            }
+            return;
+        }
+        if (!inside) return;
         if (run_start && next_key != row) {
             store_sums<O, N>(a, row, column, sum);
         } else {
@@ -572,13 +605,34 @@ __global__ void __launch_bounds__(kEmbedSumThreads) embed_sum_kernel(const Embed
         const int count = stop - r;
         auto fetch = [&](int i) {
             const uint32_t from = __shfl_sync(0xffffffffu, slot, (r + i) & 31);
-            if (i < count && inside) copy_async(ring + (i % D) * 32, reinterpret_cast<const V*>(grad + (int64_t)from * a.grad_stride));
+            if constexpr (ODD) {  // the aligned vectors that hold some of the row's part
+                const uintptr_t row_at = reinterpret_cast<uintptr_t>(static_cast<const T*>(a.grad) + (int64_t)from * a.grad_stride);
+                const uintptr_t end = row_at + (uintptr_t)a.width * sizeof(T);
+                const uintptr_t first = (row_at + (uintptr_t)(column - lane * N) * sizeof(T)) & ~(uintptr_t)15;
+                if (i < count && first + 16 * lane < end)
+                    copy_async(ring + (i % D) * R, reinterpret_cast<const uint4*>(first) + lane);
+                if (i < count && lane == 0 && first + 512 < end)
+                    copy_async(ring + (i % D) * R + 32, reinterpret_cast<const uint4*>(first) + 32);
+            } else {
+                if (i < count && inside)
+                    copy_async(ring + (i % D) * R, reinterpret_cast<const uint4*>(grad + (int64_t)from * a.grad_stride));
+            }
             copy_commit();
         };
         for (int i = 0; i < D; ++i) fetch(i);
         for (int i = 0; i < count; ++i) {
             copy_wait<D - 1>();
-            const V v = ring[(i % D) * 32];
+            uint4 bits;
+            if constexpr (ODD) {
+                __syncwarp();  // other lanes' copies
+                const uint32_t from = __shfl_sync(0xffffffffu, slot, r + i);
+                const uint32_t low_bits = (uint32_t)reinterpret_cast<uintptr_t>(grad) + from * (uint32_t)(a.grad_stride * (int)sizeof(T));
+                bits = shifted_vector(ring[(i % D) * R], ring[(i % D) * R + 1], low_bits & 15);
+                __syncwarp();  // the vectors are copied over next
+            } else {
+                bits = ring[(i % D) * R];
+            }
+            const V v = *reinterpret_cast<const V*>(&bits);
             const uint32_t k = __shfl_sync(0xffffffffu, key, r + i);
             if (start >> (r + i) & 1) {
                 put_away(k);

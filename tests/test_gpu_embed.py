@@ -172,6 +172,23 @@ def test_backward_strided_table_and_guards(gpu):
         assert torch.all(buf == 5.0)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_backward_odd_rows(gpu, dtype):
+    gen = _gen(12)
+    for width, n in ((7, 20000), (257, 900), (1031, 300)):
+        for shift in range(9):
+            flat = torch.randn(n * width + 16, generator=gen, device="cuda").to(dtype)
+            flat[:shift], flat[shift + n * width:] = float("nan"), float("nan")  # none of the rows' values
+            grad = flat[shift:shift + n * width].view(n, width)
+            into = torch.float32 if shift % 2 else dtype
+            buf = torch.full((90 * (width + 2) + 16,), 5.0, device="cuda", dtype=into)
+            table = buf[8 - shift:8 - shift + 90 * (width + 2)].view(90, width + 2)[:, 1:width + 1]
+            base = torch.randn(90, width, generator=gen, device="cuda").to(into) if shift % 3 == 0 else None
+            _check_backward(gpu, grad, IDS["skewed"](n, 90, gen), 90, 0.5, into, base, table)
+            table.fill_(5.0)
+            assert torch.all(buf == 5.0)
+
+
 def test_backward_repeats_bit_for_bit_and_on_a_stream(gpu):
     gen = _gen(12)
     grad = torch.randn(20_000, 96, generator=gen, device="cuda").bfloat16()
