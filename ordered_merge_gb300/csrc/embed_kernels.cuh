@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_lookup_odd_kernel(const E
         shift[u] = (uint32_t)(from + offset) & 15;
         low[u] = high[u] = make_uint4(0, 0, 0, 0);
         if (row[u] >= 0 && offset < length) {  // only vectors that hold some of the row
-            if (first + 16 > from && first < from + length) low[u] = __ldg(reinterpret_cast<const uint4*>(first));
-            if (shift[u] != 0 && first + 16 < from + length) high[u] = __ldg(reinterpret_cast<const uint4*>(first) + 1);
+            if (first + 16 > from && first < from + length) low[u] = *reinterpret_cast<const uint4*>(first);
+            if (shift[u] != 0 && first + 16 < from + length) high[u] = reinterpret_cast<const uint4*>(first)[1];
         }
     }
 #pragma unroll
