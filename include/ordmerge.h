@@ -603,8 +603,9 @@ typedef enum {
  * starts e * *_expert + r * *_row values after the first, its values contiguous
  * (gate and up may lie in one array).  ids (outside [0, experts): an empty slot)
  * and weights hold tokens * picks values, dense.
- * Sums run in 32 bits; h goes to the second product as the sum of two values of
- * value_type; out is rounded once.  An h beyond f16's range is infinite there.
+ * Sums run in 32 bits; h goes to the second product as two values of value_type,
+ * within 2^-16 (bf16) or 2^-22 of it (f16; of 2^-14 where h is less); out is
+ * rounded once.  An h beyond f16's range is infinite there.
  * Only the weights of experts that are asked for are read, once for every 8 tokens
  * that ask for them.  The same call repeats bit for bit.  Takes stream-ordered
  * scratch from the library's pool: 4 * tokens * picks * (inner + hidden) bytes.
