@@ -491,9 +491,10 @@ om_status om_evict_gather(const int32_t *keep, int64_t batch, int64_t heads,
  *   c[i][v] = scores[b][i] + (logits[b][i][v] - log sum_u exp logits[b][i][u])
  *   out_* [b][0 .. top) = the `top` greatest c, greatest first: c itself,
  *   the beam it goes on from (parent) and its token.
- * Equal c go to the lower beam, then to the lower token.  Sums of exponentials
- * run in 32 bits; c is formed and compared in 64 bits and rounded once, within
- * a beam the order is that of the logits themselves.
+ * Sums of exponentials run in 32 bits; c is formed and compared in 64 bits and
+ * rounded once.  Equal c go to the lower beam; within a beam the order is that of
+ * the logits themselves, also where a great score rounds their c to one number,
+ * and equal logits go to the lower token.
  *  - scores (NULL: all zero) holds batch * beams cumulative log probabilities.
  *    A beam whose score is -inf or NaN does not go on.
  *  - finished (NULL: none), batch * beams bytes: a beam where it is not zero

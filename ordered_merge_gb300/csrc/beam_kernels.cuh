@@ -370,6 +370,23 @@ __device__ __forceinline__ int place_of(const uint64_t* numbers, int n, int c, i
     for (int d = 1; d < lanes; d <<= 1) place += __shfl_xor_sync(0xffffffffu, place, d);
     return place;
 }
+// The same of continuations whose rows are cut: equal images of one beam go by their keys
+// (logit, then token), which a great score may have rounded together; others, and those of
+// no continuation, by their places.
+__device__ __forceinline__ int place_of_cut(const uint64_t* images, const uint64_t* keys, int n, int per, int c, int bits) {
+    const int lanes = 1 << bits, own = min(c, n - 1), beam = own / per;
+    const uint64_t mine = images[own];
+    int place = 0;
+#pragma unroll 4
+    for (int o = (int)threadIdx.x & (lanes - 1); o < n; o += lanes) {
+        const uint64_t image = images[o];
+        bool before = image + (o < c) > mine;
+        if (image == mine && mine != 0 && o != own && o / per == beam) before = keys[o] > keys[own];
+        place += before;
+    }
+    for (int d = 1; d < lanes; d <<= 1) place += __shfl_xor_sync(0xffffffffu, place, d);
+    return place;
+}
 // As many threads for each of n as there are, in bits.
 __device__ __forceinline__ int place_bits(int n) { return min(max(__clz(max(n - 1, 1)) - (32 - kBeamThreadBits), 0), 5); }
 
@@ -654,7 +671,8 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
         // the place of a continuation is the number of those before it
         const int bits = place_bits(n), own = (int)threadIdx.x >> bits;
         for (int c0 = 0; c0 < n; c0 += kBeamThreads >> bits) {
-            const int c = c0 + own, place = place_of(images, n, c, bits);
+            const int c = c0 + own;
+            const int place = a.parts > 1 ? place_of_cut(images, lists, n, per, c, bits) : place_of(images, n, c, bits);
             if (c >= n || place >= a.top || own << bits != (int)threadIdx.x) continue;
             const uint64_t mine = images[c];
             const int64_t to = b * a.top + place;
@@ -690,7 +708,14 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
         }
         const unsigned in0 = __ballot_sync(0xffffffffu, head[0] == best);
         const unsigned in1 = __ballot_sync(0xffffffffu, head[1] == best);
-        const int win = in0 != 0 ? __ffs(in0) - 1 : __ffs(in1) - 1;
+        int win = in0 != 0 ? __ffs(in0) - 1 : __ffs(in1) - 1;
+        if (a.parts > 1 && (in0 & (in0 - 1)) != 0) {  // slices of one beam (16 units at most then): by their keys
+            const bool same = (in0 >> lane & 1) && lane / a.parts == win / a.parts;
+            const uint64_t key = same ? lists[at[0]] : 0;
+            const uint32_t key_hi = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32));
+            const uint32_t key_lo = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32) == key_hi ? (uint32_t)key : 0);
+            win = __ffs(__ballot_sync(0xffffffffu, same && key == ((uint64_t)key_hi << 32 | key_lo))) - 1;
+        }
         if (lane == win) {
             const int i = in0 != 0 ? 0 : 1;
             const int from = i == 0 ? at[0] : at[1];

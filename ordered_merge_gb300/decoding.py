@@ -28,7 +28,8 @@ def om_beam_select(logits, top: int, scores=None, finished=None, end_id: int = 0
                    tokens=None, stream=None):
     """(scores, parents, tokens), each [batch, top]: the greatest scores[b, i]
     + log_softmax(logits[b, i])[v] of each sequence of logits [batch, beams,
-    vocab], greatest first, ties to the lower beam, then the lower token.
+    vocab], greatest first, ties to the lower beam; within a beam by logit, ties
+    to the lower token.
     scores (float32 [batch, beams]; None: zeros) are the beams' cumulative log
     probabilities; a finished beam (bool [batch, beams]) goes on with end_id
     alone, at its score.  Logits of -inf or NaN are never chosen; score -inf and
