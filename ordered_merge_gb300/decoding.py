@@ -16,7 +16,7 @@ import struct
 import torch
 
 from . import BeamArray, _check, _lib
-from .selection import VALUE_TYPES, _dense, _empty, _launch_stream, _lengths, _ptr, _rows, _value_type
+from .selection import VALUE_TYPES, _dense, _empty, _launch_stream, _lengths, _ptr, _rows, _value_type, _written
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
 ID_BYTES = {torch.int32: 4, torch.int64: 8}
@@ -40,6 +40,7 @@ def om_beam_select(logits, top: int, scores=None, finished=None, end_id: int = 0
         _dense(scores, "scores", (batch, beams), torch.float32)
     if finished is not None:
         _dense(finished, "finished", (batch, beams), torch.bool)
+    given = out_scores, parents, tokens
     if out_scores is None:
         out_scores = _empty((batch, top), torch.float32, logits.device, stream)
     if parents is None:
@@ -57,6 +58,7 @@ def om_beam_select(logits, top: int, scores=None, finished=None, end_id: int = 0
                             end_id, top, _ptr(out_scores), _ptr(parents), _ptr(tokens), handle),
         "om_beam_select",
     )
+    _written(*given)
     return out_scores, parents, tokens
 
 
@@ -133,6 +135,7 @@ def om_beam_gather(parents, arrays, starts=None, lengths=None, out=None, stream=
     # om_beam_array, whose fields are 64-bit words in this order
     _check(_lib.om_beam_gather(_ptr(parents), *shape, heads, entries, start_ptr, length_ptr, pack(*table), len(arrays),
                                handle), "om_beam_gather")
+    _written(*out)
     return out
 
 
@@ -181,6 +184,7 @@ def om_embed_lookup(ids, table, scale: float = 1.0, out=None, stream=None):
     table_stride = _rows(table, "table", 2)[0]
     rows, width = table.shape
     shape = (*ids.shape, width)
+    given = out
     if out is None:
         out = _empty(shape, table.dtype, table.device, stream)
     _dense(out, "out", shape, table.dtype)
@@ -190,6 +194,7 @@ def om_embed_lookup(ids, table, scale: float = 1.0, out=None, stream=None):
                              ids.numel(), scale, _ptr(out), width, handle),
         "om_embed_lookup",
     )
+    _written(given)
     return out
 
 
@@ -203,6 +208,7 @@ def om_embed_lookup_backward(grad, ids, rows: int, scale: float = 1.0, accumulat
     if grad.dim() < 1 or grad.shape[:-1] != ids.shape or not grad.is_contiguous():
         raise ValueError(f"grad must be contiguous, of shape {(*ids.shape, 'width')} (got {tuple(grad.shape)})")
     width = grad.shape[-1]
+    given = grad_table
     if grad_table is None:
         if accumulate:
             raise ValueError("accumulate needs a grad_table to add to")
@@ -218,6 +224,7 @@ def om_embed_lookup_backward(grad, ids, rows: int, scale: float = 1.0, accumulat
                                       _ptr(grad_table), table_stride, handle),
         "om_embed_lookup_backward",
     )
+    _written(given)
     return grad_table
 
 
@@ -248,6 +255,7 @@ def om_expert_mlp(x, ids, weights, up, down, gate=None, act: str = "silu", out=N
                            (gate, "gate", (experts, inner, hidden))):
         if t is not None and (t.dtype != x.dtype or tuple(t.shape) != shape):
             raise ValueError(f"{name} must be {x.dtype} of shape {shape} (got {t.dtype}, {tuple(t.shape)})")
+    given = out
     if out is None:
         out = _empty((tokens, hidden), x.dtype, x.device, stream)
     out_stride = _rows(out, "out", 2)[0]
@@ -261,4 +269,5 @@ def om_expert_mlp(x, ids, weights, up, down, gate=None, act: str = "silu", out=N
                            down_strides[0], down_strides[1], ACTIVATIONS[act], _ptr(out), out_stride, handle),
         "om_expert_mlp",
     )
+    _written(given)
     return out

@@ -57,6 +57,14 @@ def _launch_stream(stream, names, *tensors):
     return _stream(stream)
 
 
+def _written(*tensors):
+    """Tells autograd that the library has written into these tensors (None: not given), which were handed in: a
+    backward pass that saved one of them before refuses it then, as after any other operation in place."""
+    given = tuple(t for t in tensors if t is not None)
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def _dense(t, name: str, shape, dtype):
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
@@ -101,9 +109,6 @@ class _RouteWithGradient(torch.autograd.Function):
     def forward(ctx, logits, top_k, options):
         # outputs handed in come as options: what an earlier call wrote into them is no part of this one
         ids, weights = om_route_topk(logits, top_k, **options)
-        for given in (options["ids"], options["weights"]):
-            if given is not None:
-                torch.autograd.graph.increment_version(given)
         ctx.mark_non_differentiable(ids)
         ctx.save_for_backward(logits, ids)
         ctx.options = {name: options[name] for name in ("score", "renorm", "scale")}
@@ -131,6 +136,7 @@ def om_route_topk(logits, top_k: int, score: str = "softmax", bias=None, groups:
         return _RouteWithGradient.apply(logits, top_k, options)
     row_stride = _rows(logits, "logits", 2)[0]
     tokens, experts = logits.shape
+    given = ids, weights
     if bias is not None:
         _dense(bias, "bias", (experts,), torch.float32)
     if ids is None:
@@ -146,6 +152,7 @@ def om_route_topk(logits, top_k: int, score: str = "softmax", bias=None, groups:
                            group_best, top_k, 1 if renorm else 0, scale, _ptr(ids), _ptr(weights), handle),
         "om_route_topk",
     )
+    _written(*given)
     return ids, weights
 
 
@@ -160,6 +167,7 @@ def om_route_topk_backward(logits, ids, grad_weights, score: str = "softmax", re
     top_k = ids.shape[1]
     _dense(ids, "ids", (tokens, top_k), torch.int32)
     _dense(grad_weights, "grad_weights", (tokens, top_k), torch.float32)
+    given = grad_logits
     if grad_logits is None:
         grad_logits = _empty((tokens, experts), logits.dtype, logits.device, stream)
     _dense(grad_logits, "grad_logits", (tokens, experts), logits.dtype)
@@ -170,6 +178,7 @@ def om_route_topk_backward(logits, ids, grad_weights, score: str = "softmax", re
                                     scale, _ptr(grad_logits), handle),
         "om_route_topk_backward",
     )
+    _written(given)
     return grad_logits
 
 
@@ -181,6 +190,7 @@ def om_group_by_id(ids, groups: int, offsets=None, order=None, place=None, strea
     if ids.dtype != torch.int32 or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int32 tensor")
     n = ids.numel()
+    given = offsets, order, place
     if offsets is None:
         offsets = _empty((groups + 1,), torch.int32, ids.device, stream)
     if order is None:
@@ -193,6 +203,7 @@ def om_group_by_id(ids, groups: int, offsets=None, order=None, place=None, strea
     handle = _launch_stream(stream, "ids offsets order place", ids, offsets, order, place)
     _check(_lib.om_group_by_id(_ptr(ids), n, groups, _ptr(offsets), _ptr(order), _ptr(place), handle),
            "om_group_by_id")
+    _written(*given)
     return offsets, order, place
 
 
@@ -212,6 +223,7 @@ def om_accumulate_weights(weights, score=None, lengths=None, decay: float = 1.0,
             raise ValueError(f"score must be float32 of shape {(batch, kv_heads, length)}")
     if kv_heads is None:
         raise ValueError("kv_heads is needed without a score")
+    given = out
     if out is None:
         out = _empty((batch, kv_heads, length), torch.float32, weights.device, stream)
     o_batch, o_head, _ = _rows(out, "out", 3)
@@ -225,6 +237,7 @@ def om_accumulate_weights(weights, score=None, lengths=None, decay: float = 1.0,
                                    s_head, length_ptr, decay, _ptr(out), o_batch, o_head, handle),
         "om_accumulate_weights",
     )
+    _written(given)
     return out
 
 
@@ -238,6 +251,7 @@ def om_evict_select(score, budget: int, first: int = 0, last: int = 0, lengths=N
     if score.dtype != torch.float32:
         raise ValueError(f"score must be float32 (got {score.dtype})")
     batch, heads, length = score.shape
+    given = keep, kept
     if keep is None:
         keep = _empty((batch, heads, budget), torch.int32, score.device, stream)
     if kept is None:
@@ -251,6 +265,7 @@ def om_evict_select(score, budget: int, first: int = 0, last: int = 0, lengths=N
                              _ptr(keep), _ptr(kept), handle),
         "om_evict_select",
     )
+    _written(*given)
     return keep, kept
 
 
@@ -300,9 +315,8 @@ def om_evict_gather(keep, arrays, out=None, stream=None):
     _dense(keep, "keep", shape, torch.int32)
     if not arrays:
         raise ValueError("no arrays to gather")
-    if out is None:
-        out = tuple(_empty((*shape, *t.shape[3:]), t.dtype, t.device, stream) for t in arrays)
-    out = tuple(out)
+    handed = out is not None
+    out = tuple(out) if handed else tuple(_empty((*shape, *t.shape[3:]), t.dtype, t.device, stream) for t in arrays)
     if len(out) != len(arrays):
         raise ValueError("out must hold one tensor for each array")
     handle = _launch_stream(stream, "keep array", keep, *arrays, *out)
@@ -317,4 +331,6 @@ def om_evict_gather(keep, arrays, out=None, stream=None):
         table += (src.data_ptr(), dst.data_ptr(), *fixed)
     # om_cache_array, whose fields are 64-bit words in this order
     _check(_lib.om_evict_gather(_ptr(keep), *shape, length, pack(*table), len(arrays), handle), "om_evict_gather")
+    if handed:
+        _written(*out)
     return out
