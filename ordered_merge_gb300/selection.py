@@ -14,6 +14,7 @@ import functools
 import struct
 
 import torch
+from torch.autograd import forward_ad
 
 from . import CacheArray, _check, _lib, _stream
 
@@ -41,9 +42,19 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _no_tangents(names, tensors):
+    """Refuses tensors that carry a forward-mode tangent: the library reads their values alone."""
+    for i, t in enumerate(tensors):
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            name = names.split()[min(i, names.count(" "))]
+            raise ValueError(f"{name} carries a forward-mode tangent, for which the library has no derivative")
+
+
 def _launch_stream(stream, names, *tensors):
     """The handle of `stream`, or of the current one, on the current device,
     where every tensor (None: not given) has to be."""
+    if getattr(forward_ad, "_current_level", 0) >= 0:  # in a dual_level, where tensors may have tangents
+        _no_tangents(names, tensors)
     device = _current_device() if _cuda_ready() else -2
     for t in tensors:
         if t is not None and t.get_device() != device:
