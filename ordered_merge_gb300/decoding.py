@@ -5,8 +5,10 @@ experts' layer for a few tokens.
 Argument marshalling only, as in ``selection.py``: tensors' pointers, strides and
 the current stream go to the C ABI (declared in ``include/ordmerge.h``), which
 validates and launches.  Outputs may be passed in; those not passed are allocated.
-om_embed_lookup's rows carry their gradient to the table; the other calls stand
-outside autograd: what they give has none.
+om_embed_lookup's rows carry their gradient to the table.  om_beam_select's choice
+is a constant: what it gives has none.  The other calls have no gradient, and while
+autograd records they refuse tensors that require one (under torch.no_grad(), or
+detached, they take them).
 """
 from __future__ import annotations
 
@@ -20,6 +22,12 @@ from .selection import VALUE_TYPES, _dense, _empty, _launch_stream, _lengths, _p
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
 ID_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def _no_gradient(call: str, *tensors):
+    """Refuses tensors whose gradient would end in `call` without a word, or be that of values it has moved."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{call} has no gradient: use torch.no_grad(), or detached tensors")
 
 
 # ------------------------------------------------------------ beam search --
@@ -41,6 +49,7 @@ def om_beam_select(logits, top: int, scores=None, finished=None, end_id: int = 0
     if finished is not None:
         _dense(finished, "finished", (batch, beams), torch.bool)
     given = out_scores, parents, tokens
+    _no_gradient("what is written into out_scores", out_scores)
     if out_scores is None:
         out_scores = _empty((batch, top), torch.float32, logits.device, stream)
     if parents is None:
@@ -115,6 +124,7 @@ def om_beam_gather(parents, arrays, starts=None, lengths=None, out=None, stream=
     out = arrays if in_place else tuple(out)
     if len(out) != len(arrays):
         raise ValueError("out must hold one tensor for each array")
+    _no_gradient("om_beam_gather", *(arrays if in_place else arrays + out))
     start_ptr = _row_ints(starts, "starts", shape[0])
     length_ptr = _lengths(lengths, shape[0])
     tensors = arrays if in_place else arrays + out
@@ -185,6 +195,7 @@ def om_embed_lookup(ids, table, scale: float = 1.0, out=None, stream=None):
     rows, width = table.shape
     shape = (*ids.shape, width)
     given = out
+    _no_gradient("what is written into out", out)
     if out is None:
         out = _empty(shape, table.dtype, table.device, stream)
     _dense(out, "out", shape, table.dtype)
@@ -213,6 +224,7 @@ def om_embed_lookup_backward(grad, ids, rows: int, scale: float = 1.0, accumulat
         if accumulate:
             raise ValueError("accumulate needs a grad_table to add to")
         grad_table = _empty((rows, width), grad.dtype, grad.device, stream)
+    _no_gradient("om_embed_lookup_backward", grad, grad_table)
     table_stride = _rows(grad_table, "grad_table", 2)[0]
     if tuple(grad_table.shape) != (rows, width) or grad_table.dtype not in (grad.dtype, torch.float32):
         raise ValueError(f"grad_table must be {grad.dtype} or float32 of shape {(rows, width)} "
@@ -256,6 +268,7 @@ def om_expert_mlp(x, ids, weights, up, down, gate=None, act: str = "silu", out=N
         if t is not None and (t.dtype != x.dtype or tuple(t.shape) != shape):
             raise ValueError(f"{name} must be {x.dtype} of shape {shape} (got {t.dtype}, {tuple(t.shape)})")
     given = out
+    _no_gradient("om_expert_mlp", x, weights, up, gate, down, out)
     if out is None:
         out = _empty((tokens, hidden), x.dtype, x.device, stream)
     out_stride = _rows(out, "out", 2)[0]
