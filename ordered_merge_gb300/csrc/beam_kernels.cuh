@@ -120,6 +120,7 @@ struct BeamShared {
     uint32_t eight[2 * kBeamThreads];  // which, times 256, and whose
     int count;        // (settling) those counted
     int ties[kBeamWarps];
+    int stop;         // a wait has run out (1), and thread 0 has waited for the other stages (2)
     int live, dead;   // units of this CTA that have logits to look at, and others
     uint8_t unit[kMaxBeams];  // the former from the front, the latter from the back
 };
@@ -516,6 +517,15 @@ __device__ __forceinline__ void beam_slice_end(const BeamArgs& a, const BeamSlic
     __syncthreads();  // s is used again
 }
 
+// A stage's wait has run out (om_device_error says so; the outputs are none then): no more
+// copies are asked for, and those of the other stages get as long to end.
+__device__ __noinline__ void ring_stops(const BeamArgs& a, int stage, uint32_t phase, BeamShared& s) {
+    if (s.stop != 1) return;
+    for (int i = 1; i < a.stages; ++i)
+        mbar_wait_bounded(&s.full[(stage + i) % a.stages], phase ^ (stage + i >= a.stages), a.err);
+    s.stop = 2;
+}
+
 // Bytes of BeamShared before the ring.
 __host__ __device__ constexpr int beam_ring_offset() { return ((int)sizeof(BeamShared) + 127) / 128 * 128; }
 
@@ -584,7 +594,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
         }
         __syncwarp();
         if (threadIdx.x == 0) {
-            s.live = live, s.dead = dead;
+            s.live = live, s.dead = dead, s.stop = 0;
             for (int i = 0; i < a.stages; ++i) fill(i);
         }
     } else if (rank == 0 && (int)threadIdx.x - 32 < a.beams) {  // for the end
@@ -607,7 +617,10 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(const Beam
         const bool odd = skip & 2;
         int left = slice.n;
         for (int c = 0; c < chunks; ++c, left -= kBeamChunk * WordOf<T>::kPer) {
-            mbar_wait_bounded(&s.full[stage], phase, a.err);
+            if (!mbar_wait_or_stop(&s.full[stage], phase, a.err, &s.stop) && threadIdx.x == 0) {
+                ring_stops(a, stage, phase, s);
+                copies = 0, next_slice = live;  // nothing more to fill with
+            }
             const uint32_t* mine = words + stage * (kBeamStageBytes / 4);
             if (left < kBeamChunk * WordOf<T>::kPer) beam_last_chunk<T>(mine, odd, left, c, run);
             else if (sizeof(T) == 2 && odd) beam_whole_chunk<T, sizeof(T) == 2>(mine, c, run);

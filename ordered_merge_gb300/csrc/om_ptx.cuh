@@ -77,6 +77,23 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
     return true;
 }
 
+// The same for the threads of a CTA that share `stop`: a thread that hits the limit sets
+// it, and waits that would have to spin then give up at once, so that the kernel ends
+// however many were to come.
+__device__ __forceinline__ bool mbar_wait_or_stop(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* stop) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*stop) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(err, kErrWaitTimeout);
+            *stop = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 // L2 policy for data read exactly once (streamed inputs).
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
     uint64_t pol;
