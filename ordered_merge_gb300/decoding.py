@@ -18,7 +18,8 @@ import struct
 import torch
 
 from . import BeamArray, _check, _lib
-from .selection import VALUE_TYPES, _dense, _empty, _launch_stream, _lengths, _ptr, _rows, _value_type, _written
+from .selection import (VALUE_TYPES, _dense, _empty, _grad_enabled, _launch_stream, _lengths, _rows, _value_type,
+                        _written)
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
 ID_BYTES = {torch.int32: 4, torch.int64: 8}
@@ -26,8 +27,10 @@ ID_BYTES = {torch.int32: 4, torch.int64: 8}
 
 def _no_gradient(call: str, *tensors):
     """Refuses tensors whose gradient would end in `call` without a word, or be that of values it has moved."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError(f"{call} has no gradient: use torch.no_grad(), or detached tensors")
+    if _grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{call} has no gradient: use torch.no_grad(), or detached tensors")
 
 
 # ------------------------------------------------------------ beam search --
@@ -49,7 +52,8 @@ def om_beam_select(logits, top: int, scores=None, finished=None, end_id: int = 0
     if finished is not None:
         _dense(finished, "finished", (batch, beams), torch.bool)
     given = out_scores, parents, tokens
-    _no_gradient("what is written into out_scores", out_scores)
+    if out_scores is not None and out_scores.requires_grad:
+        _no_gradient("what is written into out_scores", out_scores)
     if out_scores is None:
         out_scores = _empty((batch, top), torch.float32, logits.device, stream)
     if parents is None:
@@ -62,9 +66,9 @@ def om_beam_select(logits, top: int, scores=None, finished=None, end_id: int = 0
     handle = _launch_stream(stream, "logits scores finished out_scores parents tokens", logits, scores, finished,
                             out_scores, parents, tokens)
     _check(
-        _lib.om_beam_select(_value_type(logits, "logits"), _ptr(logits), batch, beams, vocab, b_stride, n_stride,
-                            None if scores is None else _ptr(scores), None if finished is None else _ptr(finished),
-                            end_id, top, _ptr(out_scores), _ptr(parents), _ptr(tokens), handle),
+        _lib.om_beam_select(_value_type(logits, "logits"), logits.data_ptr(), batch, beams, vocab, b_stride, n_stride,
+                            None if scores is None else scores.data_ptr(),
+                            None if finished is None else finished.data_ptr(), end_id, top, out_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(), handle),
         "om_beam_select",
     )
     _written(*given)
@@ -85,7 +89,7 @@ def _state_entry(shape, strides, name: str, batch: int, beams: int) -> int:
 
 @functools.lru_cache(maxsize=256)
 def _state_geometry(parents_shape, in_place, *arrays):
-    """Checks the arrays' shapes and strides (each array: element size, shape and
+    """Checks the arrays' shapes and strides (each array: element type, shape and
     strides, then those of the output if there is another) and returns, as
     om_beam_array wants them, every array's bytes per entry and strides in bytes,
     then heads, entries and a packer.  Of the shapes alone, so it is kept from call
@@ -93,7 +97,8 @@ def _state_geometry(parents_shape, in_place, *arrays):
     batch, beams = parents_shape
     words, common, step = [], None, 3 if in_place else 5
     for i in range(0, len(arrays), step):
-        size, shape, src_strides = arrays[i:i + 3]
+        dtype, shape, src_strides = arrays[i:i + 3]
+        size = dtype.itemsize
         dst_shape, dst_strides = (shape, src_strides) if in_place else arrays[i + 3:i + 5]
         inner = _state_entry(shape, src_strides, "array", batch, beams)
         if dst_shape != shape or _state_entry(dst_shape, dst_strides, "out", batch, beams) != inner:
@@ -117,43 +122,41 @@ def om_beam_gather(parents, arrays, starts=None, lengths=None, out=None, stream=
     shape = parents.shape
     if len(shape) != 2:
         raise ValueError("parents must have 2 dimensions")
-    _dense(parents, "parents", shape, torch.int32)
+    if parents.dtype != torch.int32 or not parents.is_contiguous():
+        raise ValueError(f"parents must be a contiguous {torch.int32} tensor (got {parents.dtype})")
     if not arrays:
         raise ValueError("no arrays to move")
     in_place = out is None
     out = arrays if in_place else tuple(out)
     if len(out) != len(arrays):
         raise ValueError("out must hold one tensor for each array")
-    _no_gradient("om_beam_gather", *(arrays if in_place else arrays + out))
-    start_ptr = _row_ints(starts, "starts", shape[0])
+    start_ptr = _lengths(starts, shape[0], "starts")
     length_ptr = _lengths(lengths, shape[0])
-    tensors = arrays if in_place else arrays + out
-    handle = _launch_stream(stream, "parents starts lengths array", parents, starts, lengths, *tensors)
     key = []
     if in_place:
         for t in arrays:
-            key += (t.element_size(), t.shape, t.stride())
+            if t.requires_grad:
+                _no_gradient("om_beam_gather", t)
+            key += (t.dtype, t.shape, t.stride())
     else:
         for src, dst in zip(arrays, out):
-            if dst.dtype != src.dtype:
-                raise ValueError(f"out must be {src.dtype} (got {dst.dtype})")
-            key += (src.element_size(), src.shape, src.stride(), dst.shape, dst.stride())
+            if src.requires_grad or dst.requires_grad:
+                _no_gradient("om_beam_gather", src, dst)
+            dtype = src.dtype
+            if dst.dtype != dtype:
+                raise ValueError(f"out must be {dtype} (got {dst.dtype})")
+            key += (dtype, src.shape, src.stride(), dst.shape, dst.stride())
+    tensors = arrays if in_place else arrays + out
+    handle = _launch_stream(stream, "parents starts lengths array", parents, starts, lengths, *tensors)
     words, heads, entries, pack = _state_geometry(shape, in_place, *key)
     table = []
     for src, dst, fixed in zip(arrays, out, words):
         table += (src.data_ptr(), dst.data_ptr(), *fixed)
     # om_beam_array, whose fields are 64-bit words in this order
-    _check(_lib.om_beam_gather(_ptr(parents), *shape, heads, entries, start_ptr, length_ptr, pack(*table), len(arrays),
-                               handle), "om_beam_gather")
+    _check(_lib.om_beam_gather(parents.data_ptr(), *shape, heads, entries, start_ptr, length_ptr, pack(*table),
+                               len(arrays), handle), "om_beam_gather")
     _written(*out)
     return out
-
-
-def _row_ints(t, name: str, batch: int):
-    if t is None:
-        return None
-    _dense(t, name, (batch,), torch.int32)
-    return _ptr(t)
 
 
 # -------------------------------------------------------------- embedding --
@@ -195,14 +198,15 @@ def om_embed_lookup(ids, table, scale: float = 1.0, out=None, stream=None):
     rows, width = table.shape
     shape = (*ids.shape, width)
     given = out
-    _no_gradient("what is written into out", out)
+    if out is not None and out.requires_grad:
+        _no_gradient("what is written into out", out)
     if out is None:
         out = _empty(shape, table.dtype, table.device, stream)
     _dense(out, "out", shape, table.dtype)
     handle = _launch_stream(stream, "ids table out", ids, table, out)
     _check(
-        _lib.om_embed_lookup(_value_type(table, "table"), _ptr(table), rows, width, table_stride, _ptr(ids), id_bytes,
-                             ids.numel(), scale, _ptr(out), width, handle),
+        _lib.om_embed_lookup(_value_type(table, "table"), table.data_ptr(), rows, width, table_stride, ids.data_ptr(),
+                             id_bytes, ids.numel(), scale, out.data_ptr(), width, handle),
         "om_embed_lookup",
     )
     _written(given)
@@ -231,9 +235,9 @@ def om_embed_lookup_backward(grad, ids, rows: int, scale: float = 1.0, accumulat
                          f"(got {grad_table.dtype}, {tuple(grad_table.shape)})")
     handle = _launch_stream(stream, "grad ids grad_table", grad, ids, grad_table)
     _check(
-        _lib.om_embed_lookup_backward(_value_type(grad, "grad"), _ptr(grad), ids.numel(), width, width, _ptr(ids),
-                                      id_bytes, rows, scale, 1 if accumulate else 0, VALUE_TYPES[grad_table.dtype],
-                                      _ptr(grad_table), table_stride, handle),
+        _lib.om_embed_lookup_backward(_value_type(grad, "grad"), grad.data_ptr(), ids.numel(), width, width,
+                                      ids.data_ptr(), id_bytes, rows, scale, 1 if accumulate else 0, VALUE_TYPES[grad_table.dtype],
+                                      grad_table.data_ptr(), table_stride, handle),
         "om_embed_lookup_backward",
     )
     _written(given)
@@ -276,10 +280,10 @@ def om_expert_mlp(x, ids, weights, up, down, gate=None, act: str = "silu", out=N
         raise ValueError(f"out must be {x.dtype} of shape {(tokens, hidden)} (got {out.dtype}, {tuple(out.shape)})")
     handle = _launch_stream(stream, "x ids weights up down gate out", x, ids, weights, up, down, gate, out)
     _check(
-        _lib.om_expert_mlp(VALUE_TYPES[x.dtype], _ptr(x), tokens, hidden, x_stride, _ptr(ids), _ptr(weights), picks,
-                           experts, inner, _ptr(up), up_strides[0], up_strides[1],
-                           None if gate is None else _ptr(gate), gate_strides[0], gate_strides[1], _ptr(down),
-                           down_strides[0], down_strides[1], ACTIVATIONS[act], _ptr(out), out_stride, handle),
+        _lib.om_expert_mlp(VALUE_TYPES[x.dtype], x.data_ptr(), tokens, hidden, x_stride, ids.data_ptr(),
+                           weights.data_ptr(), picks, experts, inner, up.data_ptr(), up_strides[0], up_strides[1],
+                           None if gate is None else gate.data_ptr(), gate_strides[0], gate_strides[1], down.data_ptr(),
+                           down_strides[0], down_strides[1], ACTIVATIONS[act], out.data_ptr(), out_stride, handle),
         "om_expert_mlp",
     )
     _written(given)

@@ -22,14 +22,19 @@ VALUE_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
 
 
-# The current stream's handle without building a Stream object, where this
-# torch has the call (3 us less a call on the measured host).
+# The current stream's handle without building a Stream object, the device without a
+# look whether CUDA is up (a tensor there says so) and the versions of several tensors
+# at once, where this torch has the calls (3 us, and a few tenths each, less a call on
+# the measured host).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raise_versions = getattr(torch._C, "_increment_version", torch.autograd.graph.increment_version)
+_grad_enabled = torch.is_grad_enabled
 _current_device, _cuda_ready = torch.cuda.current_device, torch.cuda.is_initialized
 
 
 def _ptr(t):
-    return t.data_ptr() if t.numel() else None
+    return t.data_ptr()  # NULL where there are no elements
 
 
 def _empty(shape, dtype, device, stream):
@@ -50,19 +55,28 @@ def _no_tangents(names, tensors):
             raise ValueError(f"{name} carries a forward-mode tangent, for which the library has no derivative")
 
 
-def _launch_stream(stream, names, *tensors):
-    """The handle of `stream`, or of the current one, on the current device,
-    where every tensor (None: not given) has to be."""
-    if getattr(forward_ad, "_current_level", 0) >= 0:  # in a dual_level, where tensors may have tangents
-        _no_tangents(names, tensors)
+def _elsewhere(names, tensors):
+    """Refuses the first of the tensors that is not on the current device."""
     device = _current_device() if _cuda_ready() else -2
-    for t in tensors:
+    for i, t in enumerate(tensors):
         if t is not None and t.get_device() != device:
-            i = next(i for i, x in enumerate(tensors) if x is t)
             name = names.split()[min(i, names.count(" "))]
             if not t.is_cuda:
                 raise ValueError(f"{name} must be a CUDA tensor")
             raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _launch_stream(stream, names, *tensors):
+    """The handle of `stream`, or of the current one, on the current device,
+    where every tensor (None: not given; the first is) has to be."""
+    if forward_ad._current_level >= 0:  # in a dual_level, where tensors may have tangents
+        _no_tangents(names, tensors)
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            _elsewhere(names, tensors)
+    if device < 0 or device != _get_device():
+        _elsewhere(names, tensors)
     if stream is None and _raw_stream is not None:
         return _raw_stream(device)
     return _stream(stream)
@@ -71,9 +85,9 @@ def _launch_stream(stream, names, *tensors):
 def _written(*tensors):
     """Tells autograd that the library has written into these tensors (None: not given), which were handed in: a
     backward pass that saved one of them before refuses it then, as after any other operation in place."""
-    given = tuple(t for t in tensors if t is not None)
+    given = [t for t in tensors if t is not None]
     if given:
-        torch.autograd.graph.increment_version(given)
+        _raise_versions(given)
 
 
 def _dense(t, name: str, shape, dtype):
@@ -104,11 +118,12 @@ def _score_code(score: str) -> int:
     return SCORES[score]
 
 
-def _lengths(lengths, batch: int):
+def _lengths(lengths, batch: int, name: str = "lengths"):
     if lengths is None:
         return None
-    _dense(lengths, "lengths", (batch,), torch.int32)
-    return _ptr(lengths)
+    if lengths.dtype != torch.int32 or lengths.shape != (batch,) or not lengths.is_contiguous():
+        _dense(lengths, name, (batch,), torch.int32)
+    return lengths.data_ptr()
 
 
 class _RouteWithGradient(torch.autograd.Function):
