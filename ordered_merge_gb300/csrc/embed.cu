@@ -12,21 +12,17 @@
 
 namespace om {
 
-// Values of the widest vector (16 bytes at most) that the addresses, strides (in
-// values) and the width allow.
-static int vector_values(int value, const void* p, int64_t stride, int64_t width) {
-    int n = 16 / value;
-    while (n > 1 && ((reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n * value - 1)) != 0 || stride % n != 0 || width % n != 0))
-        n /= 2;
-    return n;
+// Whether every row of T at p consists of whole aligned vectors of 16 bytes.
+template <typename T>
+static bool whole_vectors(const void* p, int64_t stride, int64_t width) {
+    constexpr int N = 16 / (int)sizeof(T);
+    return !misaligned(p, 16) && stride % N == 0 && width % N == 0;
 }
 
 template <typename T>
 static cudaError_t launch_lookup(EmbedArgs a, cudaStream_t st) {
     constexpr int kMost = 16 / (int)sizeof(T);
-    const int values = std::min(vector_values(sizeof(T), a.table, a.table_stride, a.width),
-                                vector_values(sizeof(T), a.out, a.out_stride, a.width));
-    const bool whole = values == kMost;  // vectors of every row
+    const bool whole = whole_vectors<T>(a.table, a.table_stride, a.width) && whole_vectors<T>(a.out, a.out_stride, a.width);
     const int64_t vectors = a.n * (whole ? a.width / kMost : ((int64_t)a.width * (int)sizeof(T) + 30) / 16);
     const int64_t ctas = (vectors + kEmbedThreads * kEmbedUnroll - 1) / (kEmbedThreads * kEmbedUnroll);
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
@@ -60,9 +56,7 @@ static om_status prepare_embed(const DeviceState* d) {
 
 template <typename T, typename O>
 static cudaError_t launch_backward(EmbedBackArgs a, int sm_count, cudaStream_t st) {
-    constexpr int kMostT = 16 / (int)sizeof(T), kMostO = 16 / (int)sizeof(O);
-    const int nt = vector_values(sizeof(T), a.grad, a.grad_stride, a.width);
-    const int no = vector_values(sizeof(O), a.grad_table, a.table_stride, a.width);
+    constexpr int kMostT = 16 / (int)sizeof(T);
     cudaError_t e = cudaSuccess;
     if (a.n > 0 && a.n <= kEmbedSortMost) {
         int bits = 1;
@@ -94,7 +88,8 @@ static cudaError_t launch_backward(EmbedBackArgs a, int sm_count, cudaStream_t s
         const om_status s = om_merge_sort_u32(a.keys, a.slots, a.n, st);
         if (s != OM_OK) return s == OM_ENOMEM ? cudaErrorMemoryAllocation : cudaErrorUnknown;
     }
-    const bool whole = nt == kMostT && no == kMostO;  // vectors of every row
+    const bool whole = whole_vectors<T>(a.grad, a.grad_stride, a.width) &&
+                       whole_vectors<O>(a.grad_table, a.table_stride, a.width);
     a.tiles = (a.width + 32 * kMostT - 1) / (32 * kMostT);
     // sorted places of a warp: as few as still give every SM its 48 warps
     a.window = 4;

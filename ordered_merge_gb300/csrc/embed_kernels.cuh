@@ -16,20 +16,17 @@ __device__ __forceinline__ int64_t embed_row(const void* ids, int wide, int64_t 
     return id >= 0 && id < rows ? id : -1;
 }
 
-// N values of type T as one vector, the widest that the addresses allow.
+// N values of type T as one vector.
 template <typename T, int N>
 struct alignas(sizeof(T) * N) ValueVec {
     T v[N];
 };
 
-// A vector stored past the caches' usual order: it is not read again soon.
+// 16 bytes stored past the caches' usual order: they are not read again soon.
 template <typename T, int N>
 __device__ __forceinline__ void store_streaming(ValueVec<T, N>* p, const ValueVec<T, N>& v) {
-    constexpr int B = (int)sizeof(T) * N;
-    if constexpr (B == 16) __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&v));
-    else if constexpr (B == 8) __stcs(reinterpret_cast<uint2*>(p), *reinterpret_cast<const uint2*>(&v));
-    else if constexpr (B == 4) __stcs(reinterpret_cast<unsigned*>(p), *reinterpret_cast<const unsigned*>(&v));
-    else __stcs(reinterpret_cast<unsigned short*>(p), *reinterpret_cast<const unsigned short*>(&v));
+    static_assert(sizeof(v) == 16, "one vector");
+    __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&v));
 }
 
 // 16 of 32 bytes, from byte `shift` (a multiple of two) below 16 on.

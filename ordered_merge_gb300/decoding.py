@@ -68,7 +68,8 @@ def om_beam_select(logits, top: int, scores=None, finished=None, end_id: int = 0
     _check(
         _lib.om_beam_select(_value_type(logits, "logits"), logits.data_ptr(), batch, beams, vocab, b_stride, n_stride,
                             None if scores is None else scores.data_ptr(),
-                            None if finished is None else finished.data_ptr(), end_id, top, out_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(), handle),
+                            None if finished is None else finished.data_ptr(), end_id, top, out_scores.data_ptr(),
+                            parents.data_ptr(), tokens.data_ptr(), handle),
         "om_beam_select",
     )
     _written(*given)
@@ -236,8 +237,8 @@ def om_embed_lookup_backward(grad, ids, rows: int, scale: float = 1.0, accumulat
     handle = _launch_stream(stream, "grad ids grad_table", grad, ids, grad_table)
     _check(
         _lib.om_embed_lookup_backward(_value_type(grad, "grad"), grad.data_ptr(), ids.numel(), width, width,
-                                      ids.data_ptr(), id_bytes, rows, scale, 1 if accumulate else 0, VALUE_TYPES[grad_table.dtype],
-                                      grad_table.data_ptr(), table_stride, handle),
+                                      ids.data_ptr(), id_bytes, rows, scale, 1 if accumulate else 0,
+                                      VALUE_TYPES[grad_table.dtype], grad_table.data_ptr(), table_stride, handle),
         "om_embed_lookup_backward",
     )
     _written(given)
