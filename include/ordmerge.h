@@ -544,8 +544,9 @@ typedef struct {
  * lengths, nor between its own entries.  Arrays may lie between each other's
  * rows as in om_evict_gather, and `arrays` is read before the call returns as
  * there.  Vectors of 16 bytes where every address allows them.  beams <= 64,
- * heads <= 65535, batch <= 32767, entries < 2^31, entries' bytes and strides
- * at most 2^30, other strides 2^40, else OM_ERANGE.  No scratch.
+ * heads <= 65535, batch <= 32767, batch * heads * count and entries < 2^31,
+ * entries' bytes and strides at most 2^30, other strides 2^40, else OM_ERANGE.
+ * No scratch.
  */
 om_status om_beam_gather(const int32_t *parents, int64_t batch, int64_t beams,
                          int64_t heads, int64_t entries, const int32_t *starts,
@@ -607,14 +608,20 @@ typedef enum {
  * Sums run in 32 bits; h goes to the second product as two values of value_type,
  * within 2^-16 (bf16) or 2^-22 of it (f16; of 2^-14 where h is less); out is
  * rounded once.  An h beyond f16's range is infinite there.
- * Only the weights of experts that are asked for are read, once for every 8 tokens
- * that ask for them.  The same call repeats bit for bit.  Takes stream-ordered
- * scratch from the library's pool: 4 * tokens * picks * (inner + hidden) bytes.
- * One cooperative launch, of two CTAs on every SM.  out shares no byte with the
- * inputs.
+ * Only the weights of experts that are asked for are read.  The same call repeats
+ * bit for bit.  Takes stream-ordered scratch from the library's pool.  out shares
+ * no byte with the inputs.
+ *  - Where hidden and inner are multiples of 8 and the rows of x and of all weights
+ *    start on 16 bytes: one cooperative launch, of two CTAs on every SM of the
+ *    device (a context that holds fewer SMs gets OM_ECUDA); weights are taken once
+ *    for every 8 tokens that ask for them; 4 * tokens * picks * (inner + hidden)
+ *    bytes of scratch.
+ *  - Otherwise two ordinary launches that read single values (2 to 5 times
+ *    slower): the weights of up and gate are taken once for every 16 tokens of an
+ *    expert, or 64 where tokens * picks > 8 * experts, those of down for every 16;
+ *    4 * tokens * picks * inner bytes of scratch, inner rounded up to 8.
  * At most 64 tokens, 32 picks, 1024 experts, hidden and inner 2^20, strides
- * 2^40, else OM_ERANGE.  Whole 16-byte vectors where hidden, inner, strides and
- * addresses allow them; single values (several times slower) otherwise.
+ * 2^40, else OM_ERANGE.
  */
 om_status om_expert_mlp(int value_type, const void *x, int64_t tokens,
                         int64_t hidden, int64_t x_stride, const int32_t *ids,

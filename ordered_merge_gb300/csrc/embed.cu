@@ -91,7 +91,8 @@ static cudaError_t launch_backward(EmbedBackArgs a, int sm_count, cudaStream_t s
     const bool whole = whole_vectors<T>(a.grad, a.grad_stride, a.width) &&
                        whole_vectors<O>(a.grad_table, a.table_stride, a.width);
     a.tiles = (a.width + 32 * kMostT - 1) / (32 * kMostT);
-    // sorted places of a warp: as few as still give every SM its 48 warps
+    // sorted places of a warp: as few as leave at most 96 warps to an SM, four waves of the
+    // 24 that its shared memory holds
     a.window = 4;
     while (a.window < 32 && a.n * a.tiles / a.window > 96 * (int64_t)sm_count) a.window *= 2;
     const int64_t per = kEmbedSumThreads / 32;
