@@ -108,26 +108,28 @@ __device__ __forceinline__ float activate(float x, int act) {
     return x > 0.0f || x != x ? x : 0.0f;
 }
 
-// An activation goes to the second product as two values of the weights' type: itself
-// rounded, and what that left.  In bf16 the pair is within 2^-16 of it, 2^-8 of what the
-// output's rounding may take.  In f16 it is within 2^-22; f16's smallest step, 2^-24, would
-// spoil that for activations below 1/8, so the second value is kept times 2^11, in sums of
-// its own: 2^-22 down to activations of 2^-14, and 2^-36 at most beneath.  (Times 2^12, what
-// the greatest activations leave would overflow.)  Times are as without it: 12 tokens of 4
-// of 32 experts, 2000 x 1400, 59.7 us.
+// An activation goes to the second product as two values of the weights' type, each with
+// sums of its own: itself rounded, and what that left.  In bf16 the pair is within 2^-16 of
+// it, 2^-8 of what the output's rounding may take.  In f16 it is within 2^-22; f16's smallest
+// step, 2^-24, would spoil that for activations below 1/8, so the second value is kept times
+// 2^11: 2^-22 down to activations of 2^-14, and 2^-36 at most beneath.  (Times 2^12, what the
+// greatest activations leave would overflow.)  Times are as with one sum and no factor: 12
+// tokens of 4 of 32 experts, 2000 x 1400 f16, 59.7 us.
 template <typename T>
-struct RestOf {
-    static constexpr bool kScaled = std::is_same<T, __half>::value;
-    static constexpr float kScale = kScaled ? 2048.0f : 1.0f;
-    static constexpr int kSums = kScaled ? 2 : 1;  // of the second product
-};
+constexpr float kRestScale = std::is_same<T, __half>::value ? 2048.0f : 1.0f;
+// The sum of both.  An infinite weight makes the first one infinite; what was left has any
+// sign there, or is zero, and says nothing.
+template <typename T>
+__device__ __forceinline__ float pair_sum(float first, float rest) {
+    return isinf(first) ? first : first + rest * (1.0f / kRestScale<T>);
+}
 template <typename T>
 __device__ __forceinline__ void store_pair(const ExpertArgs& a, int64_t at, float h) {
     const T high = from_float<T>(h);
     // beyond f16's range the first value is infinite, and nothing is left
     const float rest = isinf(to_float(high)) ? 0.0f : h - to_float(high);
     static_cast<T*>(a.high)[at] = high;
-    static_cast<T*>(a.low)[at] = from_float<T>(rest * RestOf<T>::kScale);
+    static_cast<T*>(a.low)[at] = from_float<T>(rest * kRestScale<T>);
 }
 
 // ---- rows that no 16-byte copy can take (odd sizes, strides or addresses): two
@@ -276,8 +278,7 @@ __global__ void __launch_bounds__(kExpertWarps * 32) expert_down_kernel(const Ex
                 high[n] = c < count ? static_cast<const T*>(a.high) + (int64_t)s_list[warp][c] * a.inner_pad : nullptr;
                 low[n] = c < count ? static_cast<const T*>(a.low) + (int64_t)s_list[warp][c] * a.inner_pad : nullptr;
             }
-            constexpr int SUMS = RestOf<T>::kSums;
-            float d[SUMS][NT][4] = {};
+            float d[2][NT][4] = {};
             for (int s = s_lo; s < s_hi; ++s) {
                 const int k = s * 32 + 8 * t;
                 const uint4 w0 = load8<T>(row0, k, a.inner), w1 = load8<T>(row1, k, a.inner);
@@ -287,15 +288,13 @@ __global__ void __launch_bounds__(kExpertWarps * 32) expert_down_kernel(const Ex
                     uint4 h = make_uint4(0, 0, 0, 0), l = h;
                     if (high[n] != nullptr) h = load8<T>(high[n], k, a.inner), l = load8<T>(low[n], k, a.inner);
                     mma_step<T>(d[0][n], w0, w1, h);
-                    mma_step<T>(d[SUMS - 1][n], w0, w1, l);
+                    mma_step<T>(d[1][n], w0, w1, l);
                 }
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                if constexpr (SUMS == 2) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) d[0][n][i] += d[1][n][i] * (1.0f / RestOf<T>::kScale);
-                }
+                for (int i = 0; i < 4; ++i) d[0][n][i] = pair_sum<T>(d[0][n][i], d[1][n][i]);
                 float* to = &s_tile[warp][8 * n + 2 * t][g];
                 to[0] = d[0][n][0], to[kExpertRows] = d[0][n][1], to[8] = d[0][n][2], to[kExpertRows + 8] = d[0][n][3];
             }
@@ -383,8 +382,7 @@ struct LayerProduct {
     const ExpertArgs& a;
     static constexpr int kMats = GATED ? 2 : 1;       // matrices that give 16 TILES / kMats rows each
     static constexpr int kRows = 16 * TILES / kMats;  // rows of the result in an item
-    static constexpr int kSets = SECOND ? 2 : 1;      // rows of a token
-    static constexpr int kSums = SECOND ? RestOf<T>::kSums : 1;  // and sums of each
+    static constexpr int kSets = SECOND ? 2 : 1;      // rows of a token, and sums
     static constexpr bool kSecond = SECOND;
     __device__ __forceinline__ int columns() const { return SECOND ? a.inner : a.hidden; }
     __device__ __forceinline__ int result() const { return SECOND ? a.hidden : a.inner; }
@@ -483,7 +481,7 @@ struct LayerWork {
                 else x[u][set] = *reinterpret_cast<const uint4*>(from);
             }
     }
-    __device__ __forceinline__ void multiply(float (&d)[P::kSums][TILES][4]) {
+    __device__ __forceinline__ void multiply(float (&d)[P::kSets][TILES][4]) {
         const int warp_column = c + 32 * (int)(threadIdx.x >> 5);
 #pragma unroll
         for (int u = 0; u < S; ++u) {
@@ -491,7 +489,7 @@ struct LayerWork {
 #pragma unroll
             for (int set = 0; set < P::kSets; ++set)
 #pragma unroll
-                for (int m = 0; m < TILES; ++m) mma_step<T>(d[P::kSums == 2 ? set : 0][m], w[u][m][0], w[u][m][1], x[u][set]);
+                for (int m = 0; m < TILES; ++m) mma_step<T>(d[set][m], w[u][m][0], w[u][m][1], x[u][set]);
         }
     }
 };
@@ -501,7 +499,7 @@ struct LayerWork {
 template <typename T, int TILES, typename P, typename F>
 __device__ __forceinline__ void layer_product(LayerWork<T, TILES, P>& work, float* sums, int& turn, F&& done) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    float d[P::kSums][TILES][4] = {};
+    float d[P::kSets][TILES][4] = {};
     while (work.here()) {
         work.multiply(d);
         const bool last = work.last_columns();
@@ -515,9 +513,9 @@ __device__ __forceinline__ void layer_product(LayerWork<T, TILES, P>& work, floa
         turn ^= 1;
 #pragma unroll
         for (int m = 0; m < TILES; ++m) {
-            if constexpr (P::kSums == 2) {
+            if constexpr (P::kSets == 2) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) d[0][m][i] += d[1][m][i] * (1.0f / RestOf<T>::kScale), d[1][m][i] = 0.0f;
+                for (int i = 0; i < 4; ++i) d[0][m][i] = pair_sum<T>(d[0][m][i], d[1][m][i]), d[1][m][i] = 0.0f;
             }
             float* to = mine + ((warp * TILES + m) * kLayerTokens + 2 * t) * kExpertRows + g;
             to[0] = d[0][m][0], to[kExpertRows] = d[0][m][1];
