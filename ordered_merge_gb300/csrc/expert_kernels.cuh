@@ -104,7 +104,8 @@ __device__ __forceinline__ int next_slots(const int32_t* ids, int slots, int e, 
 
 __device__ __forceinline__ float activate(float x, int act) {
     if (act == kActSilu) return x / (1.0f + expf(-x));
-    if (act == kActGelu) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
+    // 1 + erf(y) as erfc(-y): the sum would cancel in 32 bits far below zero (6 % of it at x = -5)
+    if (act == kActGelu) return 0.5f * x * erfcf(x * -0.70710678118654752f);
     return x > 0.0f || x != x ? x : 0.0f;
 }
 
